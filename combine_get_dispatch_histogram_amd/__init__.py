@@ -17,6 +17,8 @@ sections 4.1-4.3, for ranks that are partitions of one GPU):
   low_latency_dispatch(x, topk_idx, max_tokens, num_experts, dest_rank, ...)  4.3
   low_latency_combine(y, topk_idx, topk_weights, <dispatch outputs>, ...)     4.3
   update_mask_buffer / clean_mask_buffer / query_mask_buffer        rank masking
+  expert_order, grouped_gemm (+ _dgrad, _wgrad, _fp8), swiglu (+ _fp8, _backward), expert_reduce (+ _backward):
+  what the experts compute between dispatch and combine (experts.py)
 The ``*_into`` variants take preallocated outputs and allocate nothing.
 """
 from __future__ import annotations
@@ -28,7 +30,13 @@ from typing import Optional
 import torch
 
 from . import _lib
+from ._call import _Args, _run, _want, check_status
 from ._lib import MIEP_ECAPACITY, MiepError, X_BF16, X_BF16_CAST_FP8, X_FP8  # noqa: F401
+from .experts import (ExpertOrder, RowGroups, expert_order, expert_order_into, expert_reduce, expert_reduce_backward,
+                      expert_reduce_backward_into, expert_reduce_into, grouped_gemm, grouped_gemm_dgrad,
+                      grouped_gemm_dgrad_into, grouped_gemm_fp8, grouped_gemm_fp8_into, grouped_gemm_into,
+                      grouped_gemm_wgrad, grouped_gemm_wgrad_into, swiglu, swiglu_backward, swiglu_backward_into,
+                      swiglu_fp8, swiglu_fp8_into, swiglu_into)
 
 __all__ = ["Handle", "MiepError", "get_dispatch_layout", "get_dispatch_layout_into", "dispatch", "dispatch_into", "cached_dispatch",
            "cached_dispatch_into", "combine", "combine_into", "low_latency_dispatch", "low_latency_dispatch_into",
@@ -36,66 +44,16 @@ __all__ = ["Handle", "MiepError", "get_dispatch_layout", "get_dispatch_layout_in
            "clean_mask_buffer",
            "RelayHandle", "relay_dispatch", "relay_dispatch_into", "relay_cached_dispatch",
            "relay_cached_dispatch_into", "relay_combine", "relay_combine_into",
-           "query_mask_buffer", "check_status", "ll_msg_bytes", "version", "MIEP_ECAPACITY"]
-
-
-class _Args:
-    """Pointer marshalling for one library call: every tensor it passes must be
-    a contiguous device tensor on one and the same GPU, and the call runs with
-    that GPU current and on its current stream."""
-
-    def __init__(self):
-        self.dev = None
-
-    def _see(self, t: torch.Tensor) -> None:
-        if not t.is_cuda:
-            raise ValueError("miep expects device tensors")
-        if self.dev is None:
-            self.dev = t.device
-        elif t.device != self.dev:
-            raise ValueError("miep expects every tensor of a call on one device (%s and %s)" % (self.dev, t.device))
-
-    def p(self, t: Optional[torch.Tensor]):
-        if t is None:
-            return None
-        self._see(t)
-        if not t.is_contiguous():
-            raise ValueError("miep expects contiguous tensors")
-        return ctypes.c_void_p(t.data_ptr())
-
-    def handle(self, h) -> None:
-        for t in h.tensors():
-            self.p(t)
-
-
-def _run(a: _Args, name: str, *args) -> None:
-    if a.dev is None:
-        raise ValueError("miep call without device tensors")
-    with torch.cuda.device(a.dev):
-        stream = ctypes.c_void_p(torch.cuda.current_stream(a.dev).cuda_stream)
-        _lib.check(getattr(_lib.load(), name)(*args, stream))
-
-
-def _want(t: Optional[torch.Tensor], name: str, dtype, shape=None):
-    if t is None:
-        return
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+           "query_mask_buffer", "check_status", "ll_msg_bytes", "version", "MIEP_ECAPACITY",
+           "RowGroups", "ExpertOrder", "expert_order", "expert_order_into", "expert_reduce", "expert_reduce_into",
+           "expert_reduce_backward", "expert_reduce_backward_into", "grouped_gemm", "grouped_gemm_into",
+           "grouped_gemm_dgrad", "grouped_gemm_dgrad_into", "grouped_gemm_wgrad", "grouped_gemm_wgrad_into",
+           "grouped_gemm_fp8", "grouped_gemm_fp8_into", "swiglu", "swiglu_into", "swiglu_fp8", "swiglu_fp8_into",
+           "swiglu_backward", "swiglu_backward_into"]
 
 
 def version() -> str:
     return _lib.load().miep_version().decode()
-
-
-def check_status(status: torch.Tensor) -> None:
-    """Read a dispatch's device status word (synchronous: waits for the
-    current stream); raises MiepError(MIEP_ECAPACITY) if the receive rows
-    exceeded their fixed capacity."""
-    _want(status, "status", torch.int32, (1,))
-    a = _Args()
-    _run(a, "miep_check_status", a.p(status))
 
 
 def ll_msg_bytes(hidden: int, use_fp8: bool) -> int:

@@ -18,6 +18,9 @@ X_BF16, X_FP8, X_BF16_CAST_FP8 = 0, 1, 2
 EXPORTS = ("miep_get_dispatch_layout", "miep_dispatch", "miep_cached_dispatch", "miep_check_status", "miep_combine",
            "miep_relay_dispatch", "miep_relay_cached_dispatch", "miep_relay_combine", "miep_ll_dispatch",
            "miep_ll_dispatch_noalloc", "miep_ll_combine", "miep_mask_update", "miep_mask_clean", "miep_mask_query", "miep_ll_msg_bytes",
+           "miep_expert_order", "miep_expert_reduce", "miep_expert_reduce_backward", "miep_grouped_gemm",
+           "miep_grouped_gemm_dgrad", "miep_grouped_gemm_wgrad", "miep_grouped_gemm_fp8", "miep_swiglu",
+           "miep_swiglu_fp8", "miep_swiglu_backward",
            "miep_last_error", "miep_version")
 
 
@@ -47,6 +50,11 @@ class LLProblem(ctypes.Structure):
                 ("dest_rank", ctypes.c_int32)]
 
 
+class RowGroupsC(ctypes.Structure):
+    _fields_ = [("begin", ctypes.c_void_p), ("rows", ctypes.c_void_p), ("num_rows", ctypes.c_int64),
+                ("num_groups", ctypes.c_int32), ("stride", ctypes.c_int32)]
+
+
 class MiepError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__("miep status %d: %s" % (status, msg))
@@ -56,6 +64,7 @@ class MiepError(RuntimeError):
 _lib = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 
 
 def load() -> ctypes.CDLL:
@@ -85,6 +94,21 @@ def load() -> ctypes.CDLL:
         lib.miep_mask_update.argtypes = [_P, _I32, _I32, _I32, _P]
         lib.miep_mask_clean.argtypes = [_P, _I32, _P]
         lib.miep_mask_query.argtypes = [_P, _I32, _P, _P]
+        groups = ctypes.POINTER(RowGroupsC)
+        lib.miep_expert_order.argtypes = [_P, _P, _I64, _I32, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _I64, _P, _P, _P]
+        lib.miep_expert_reduce.argtypes = [_P, _I64, _I32, _P, _I64, _I32, _P, _P, _P, _P]
+        lib.miep_expert_reduce_backward.argtypes = [_P, _P, _I64, _I32, _P, _I64, _I32, _P, _P, _P, _P, _P]
+        lib.miep_grouped_gemm.argtypes = [groups, _P, _I64, _P, _I32, _I32, _P, _I32, _P, _P]
+        lib.miep_grouped_gemm_dgrad.argtypes = [groups, _P, _P, _I32, _I32, _I32, _P, _P]
+        lib.miep_grouped_gemm_wgrad.argtypes = [groups, _P, _P, _I64, _P, _I32, _I32, _I32, _I32, _P, _P]
+        lib.miep_grouped_gemm_fp8.argtypes = [groups, _P, _P, _I64, _P, _P, _I32, _I32, _I32, _P, _I32, _P, _P]
+        lib.miep_swiglu.argtypes = [groups, _P, _I32, _P, _P]
+        lib.miep_swiglu_fp8.argtypes = [groups, _P, _I32, _I32, _P, _P, _P, _P]
+        lib.miep_swiglu_backward.argtypes = [groups, _P, _P, _I32, _P, _P]
+        for f in ("miep_expert_order", "miep_expert_reduce", "miep_expert_reduce_backward", "miep_grouped_gemm",
+                  "miep_grouped_gemm_dgrad", "miep_grouped_gemm_wgrad", "miep_grouped_gemm_fp8", "miep_swiglu",
+                  "miep_swiglu_fp8", "miep_swiglu_backward"):
+            getattr(lib, f).restype = ctypes.c_int
         for f in ("miep_get_dispatch_layout", "miep_dispatch", "miep_cached_dispatch", "miep_check_status", "miep_combine",
                   "miep_relay_dispatch", "miep_relay_cached_dispatch", "miep_relay_combine",
                   "miep_ll_dispatch", "miep_ll_dispatch_noalloc", "miep_ll_combine", "miep_mask_update",

@@ -22,7 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(ROOT, "_build", "miep")
 LIB = os.path.join(HERE, "libmiep.so")
 
-SOURCES = ["api.cpp", "layout.hip", "notify.hip", "pack.hip", "combine.hip", "ll.hip", "relay.hip"]
+SOURCES = ["api.cpp", "layout.hip", "notify.hip", "pack.hip", "combine.hip", "ll.hip", "relay.hip", "order.hip", "gemm.hip",
+           "gemm_fp8.hip", "gemm_weight.hip", "swiglu.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -204,6 +204,81 @@ miep_status check_ll_problem(const miep_ll_problem* q) {
   return MIEP_OK;
 }
 
+constexpr int64_t kMaxRowsI32 = (1ll << 31) - 1;
+
+miep_status check_groups(const miep_row_groups* g, miep::GroupArgs* out) {
+  if (!g) return fail(MIEP_EINVAL, "groups is NULL");
+  if (g->num_groups < 0 || g->num_rows < 0 || g->num_rows > kMaxRowsI32)
+    return fail(MIEP_EINVAL, "num_groups must be >= 0 and num_rows in [0, 2^31-1]");
+  if (g->num_groups > miep::kMaxExperts) return fail(MIEP_EUNSUPPORTED, "num_groups > %d", miep::kMaxExperts);
+  if (g->num_groups > 0 && !g->rows) return fail(MIEP_EINVAL, "groups' rows is NULL");
+  if (g->num_groups > 0 && !g->begin && g->stride <= 0)
+    return fail(MIEP_EINVAL, "groups need begin or a stride > 0");
+  out->G = g->num_groups;
+  out->stride = g->stride;
+  out->begin = g->begin;
+  out->rows = g->rows;
+  out->limit = g->num_rows;
+  return MIEP_OK;
+}
+
+// Sizes of a grouped product over n x k weights.
+miep_status check_gemm(const miep_row_groups* g, int32_t n, int32_t k, int32_t expected_rows, miep::GroupArgs* out) {
+  miep_status st = check_groups(g, out);
+  if (st != MIEP_OK) return st;
+  if (n <= 0 || k <= 0 || expected_rows < 0) return fail(MIEP_EINVAL, "n and k must be > 0, expected_rows >= 0");
+  if (n % 8 != 0 || k % 8 != 0) return fail(MIEP_EUNSUPPORTED, "n and k must be multiples of 8 (16-byte rows)");
+  if (n > (1 << 21) || k > (1 << 21)) return fail(MIEP_EUNSUPPORTED, "n or k > 2^21");
+  const int64_t wide = (n > k ? n : k) / 128 + 1;
+  if ((g->num_rows / 32 + 1 + g->num_groups) * wide > kMaxRowsI32)
+    return fail(MIEP_EUNSUPPORTED, "more than 2^31-1 tiles of rows and columns");
+  return MIEP_OK;
+}
+
+// The rows operand of a grouped product: in layout rows, or gathered.
+miep_status check_source(const miep_row_groups* g, const void* x, int64_t x_rows, const int32_t* row_index) {
+  if (x_rows < 0 || x_rows > kMaxRowsI32) return fail(MIEP_EINVAL, "x_rows must be in [0, 2^31-1]");
+  if (!row_index && x_rows != g->num_rows)
+    return fail(MIEP_EINVAL, "x has %lld rows, the layout %lld (and there is no row_index)",
+                static_cast<long long>(x_rows), static_cast<long long>(g->num_rows));
+  if (x_rows > 0 && !x) return fail(MIEP_EINVAL, "x is NULL");
+  if (!aligned16(x)) return fail(MIEP_EUNSUPPORTED, "x must be 16-byte aligned");
+  return MIEP_OK;
+}
+
+miep_status check_array(const void* p, bool required, const char* name) {
+  if (required && !p) return fail(MIEP_EINVAL, "%s is NULL", name);
+  if (!aligned16(p)) return fail(MIEP_EUNSUPPORTED, "%s must be 16-byte aligned", name);
+  return MIEP_OK;
+}
+
+miep_status check_swiglu(const miep_row_groups* g, const uint16_t* h, int32_t inner, const void* out,
+                         const char* name, miep::SwigluArgs* a) {
+  miep_status st = check_groups(g, &a->g);
+  if (st != MIEP_OK) return st;
+  if (inner <= 0) return fail(MIEP_EINVAL, "inner must be > 0");
+  if (inner % 8 != 0) return fail(MIEP_EUNSUPPORTED, "inner must be a multiple of 8 (16-byte rows)");
+  if (inner > (1 << 21)) return fail(MIEP_EUNSUPPORTED, "inner > 2^21");
+  const bool any = g->num_rows > 0 && g->num_groups > 0;
+  if ((st = check_array(h, any, "h")) != MIEP_OK) return st;
+  if ((st = check_array(out, any, name)) != MIEP_OK) return st;
+  a->I = inner;
+  a->h = h;
+  return MIEP_OK;
+}
+
+miep_status check_reduce(int64_t num_slots, int32_t hidden, const int32_t* row_slot, int64_t num_rows,
+                         int32_t num_topk) {
+  if (num_slots < 0 || num_slots > kMaxRowsI32 || num_rows < 0 || num_rows > kMaxRowsI32)
+    return fail(MIEP_EINVAL, "num_slots and num_rows must be in [0, 2^31-1]");
+  if (hidden <= 0 || num_topk <= 0) return fail(MIEP_EINVAL, "hidden and num_topk must be > 0");
+  if (hidden % 8 != 0) return fail(MIEP_EUNSUPPORTED, "hidden must be a multiple of 8 (16-byte rows)");
+  if (hidden > (1 << 24)) return fail(MIEP_EUNSUPPORTED, "hidden > 2^24");
+  if (num_topk > 64) return fail(MIEP_EUNSUPPORTED, "num_topk > 64");
+  if (num_rows > 0 && !row_slot) return fail(MIEP_EINVAL, "row_slot is NULL");
+  return MIEP_OK;
+}
+
 }  // namespace
 
 namespace miep {
@@ -730,6 +805,216 @@ miep_status miep_mask_clean(int32_t* mask_buffer, int32_t num_ranks, void* strea
 miep_status miep_mask_query(const int32_t* mask_buffer, int32_t num_ranks, int32_t* out, void* stream) {
   if (!mask_buffer || !out || num_ranks <= 0) return fail(MIEP_EINVAL, "a pointer is NULL or num_ranks <= 0");
   return hip_status(miep::launch_copy_i32(mask_buffer, out, num_ranks, static_cast<hipStream_t>(stream)), "mask launch");
+}
+
+miep_status miep_expert_order(const int64_t* recv_topk_idx, const int32_t* recv_rank_offset, int64_t num_rows,
+                              int32_t num_topk, int32_t num_experts, int32_t num_ranks, int32_t expert_alignment,
+                              int32_t* workspace, int32_t parts, int32_t* group_begin, int32_t* group_rows,
+                              int32_t* slot_row, int64_t num_slots, int32_t* row_slot, int32_t* status, void* stream) {
+  if (num_rows < 0 || num_slots < 0 || num_rows > kMaxRowsI32 || num_slots > kMaxRowsI32)
+    return fail(MIEP_EINVAL, "num_rows and num_slots must be in [0, 2^31-1]");
+  if (num_topk <= 0 || num_experts <= 0 || num_ranks <= 0 || expert_alignment <= 0 || parts <= 0)
+    return fail(MIEP_EINVAL, "num_topk, num_experts, num_ranks, expert_alignment, parts must be > 0");
+  if (num_experts % num_ranks != 0) return fail(MIEP_EINVAL, "num_experts must be a multiple of num_ranks");
+  if (num_ranks > miep::kMaxRanks) return fail(MIEP_EUNSUPPORTED, "num_ranks > %d", miep::kMaxRanks);
+  if (num_experts > miep::kMaxExperts) return fail(MIEP_EUNSUPPORTED, "num_experts > %d", miep::kMaxExperts);
+  if (num_experts / num_ranks > miep::kMaxLocalExperts)
+    return fail(MIEP_EUNSUPPORTED, "more than %d experts a rank", miep::kMaxLocalExperts);
+  if (num_topk > 64) return fail(MIEP_EUNSUPPORTED, "num_topk > 64");
+  if (num_rows * num_topk + static_cast<int64_t>(expert_alignment) * num_experts > kMaxRowsI32)
+    return fail(MIEP_EUNSUPPORTED, "num_rows * num_topk + expert_alignment * num_experts > 2^31-1 (int32 slots)");
+  if (!recv_rank_offset || !workspace || !group_begin || !group_rows)
+    return fail(MIEP_EINVAL, "recv_rank_offset / workspace / group_begin / group_rows NULL");
+  if (num_rows > 0 && (!recv_topk_idx || !row_slot)) return fail(MIEP_EINVAL, "recv_topk_idx / row_slot NULL");
+  if (num_slots > 0 && !slot_row) return fail(MIEP_EINVAL, "slot_row is NULL");
+  miep::OrderArgs a{};
+  a.rows = num_rows;
+  a.K = num_topk;
+  a.E = num_experts;
+  a.R = num_ranks;
+  a.L = num_experts / num_ranks;
+  a.align = expert_alignment;
+  a.parts = parts;
+  a.slots = num_slots;
+  a.topk = recv_topk_idx;
+  a.off = recv_rank_offset;
+  a.counts = workspace;
+  a.begin = group_begin;
+  a.group_rows = group_rows;
+  a.slot_row = slot_row;
+  a.row_slot = row_slot;
+  a.status = status;
+  return hip_status(miep::launch_order(a, static_cast<hipStream_t>(stream)), "expert order launch");
+}
+
+miep_status miep_expert_reduce(const uint16_t* z, int64_t num_slots, int32_t hidden, const int32_t* row_slot,
+                               int64_t num_rows, int32_t num_topk, const int32_t* total_rows,
+                               const float* topk_weights, uint16_t* y, void* stream) {
+  miep_status st = check_reduce(num_slots, hidden, row_slot, num_rows, num_topk);
+  if (st != MIEP_OK) return st;
+  if ((st = check_array(z, num_slots > 0, "z")) != MIEP_OK) return st;
+  if ((st = check_array(y, num_rows > 0, "y")) != MIEP_OK) return st;
+  miep::ReduceArgs a{};
+  a.rows = num_rows;
+  a.slots = num_slots;
+  a.H = hidden;
+  a.K = num_topk;
+  a.row_slot = row_slot;
+  a.num_rows = total_rows;
+  a.w = topk_weights;
+  a.z = z;
+  a.out = y;
+  return hip_status(miep::launch_reduce(a, static_cast<hipStream_t>(stream)), "expert reduce launch");
+}
+
+miep_status miep_expert_reduce_backward(const uint16_t* dy, const uint16_t* z, int64_t num_slots, int32_t hidden,
+                                        const int32_t* row_slot, int64_t num_rows, int32_t num_topk,
+                                        const int32_t* total_rows, const float* topk_weights, uint16_t* dz,
+                                        float* d_topk_weights, void* stream) {
+  miep_status st = check_reduce(num_slots, hidden, row_slot, num_rows, num_topk);
+  if (st != MIEP_OK) return st;
+  if ((st = check_array(dy, num_rows > 0, "dy")) != MIEP_OK) return st;
+  if ((st = check_array(z, num_slots > 0 && d_topk_weights, "z")) != MIEP_OK) return st;
+  if ((st = check_array(dz, num_slots > 0, "dz")) != MIEP_OK) return st;
+  miep::ReduceArgs a{};
+  a.rows = num_rows;
+  a.slots = num_slots;
+  a.H = hidden;
+  a.K = num_topk;
+  a.row_slot = row_slot;
+  a.num_rows = total_rows;
+  a.w = topk_weights;
+  a.z = z;
+  a.dy = dy;
+  a.out = dz;
+  a.dw = d_topk_weights;
+  return hip_status(miep::launch_reduce_backward(a, static_cast<hipStream_t>(stream)), "expert reduce backward launch");
+}
+
+miep_status miep_grouped_gemm(const miep_row_groups* g, const uint16_t* x, int64_t x_rows, const uint16_t* w,
+                              int32_t n, int32_t k, const int32_t* row_index, int32_t expected_rows, uint16_t* y,
+                              void* stream) {
+  miep::GemmRowsArgs a{};
+  miep_status st = check_gemm(g, n, k, expected_rows, &a.g);
+  if (st == MIEP_OK) st = check_source(g, x, x_rows, row_index);
+  if (st == MIEP_OK) st = check_array(w, g->num_groups > 0, "w");
+  if (st == MIEP_OK) st = check_array(y, g->num_rows > 0, "y");
+  if (st != MIEP_OK) return st;
+  a.q = x;
+  a.p = w;
+  a.row_index = row_index;
+  a.q_rows = x_rows;
+  a.C = k;
+  a.NO = n;
+  a.out = y;
+  a.type = miep::kGemmBf16;
+  a.expected = expected_rows;
+  return hip_status(miep::launch_gemm_rows(a, static_cast<hipStream_t>(stream)), "grouped gemm launch");
+}
+
+miep_status miep_grouped_gemm_dgrad(const miep_row_groups* g, const uint16_t* dy, const uint16_t* w, int32_t n,
+                                    int32_t k, int32_t expected_rows, uint16_t* dx, void* stream) {
+  miep::GemmRowsArgs a{};
+  miep_status st = check_gemm(g, n, k, expected_rows, &a.g);
+  if (st == MIEP_OK) st = check_array(dy, g->num_rows > 0, "dy");
+  if (st == MIEP_OK) st = check_array(w, g->num_groups > 0, "w");
+  if (st == MIEP_OK) st = check_array(dx, g->num_rows > 0, "dx");
+  if (st != MIEP_OK) return st;
+  a.q = dy;
+  a.p = w;
+  a.q_rows = g->num_rows;
+  a.C = n;
+  a.NO = k;
+  a.out = dx;
+  a.type = miep::kGemmBf16;
+  a.transposed = 1;
+  a.expected = expected_rows;
+  return hip_status(miep::launch_gemm_rows(a, static_cast<hipStream_t>(stream)), "grouped gemm dgrad launch");
+}
+
+miep_status miep_grouped_gemm_wgrad(const miep_row_groups* g, const uint16_t* dy, const uint16_t* x, int64_t x_rows,
+                                    const int32_t* row_index, int32_t n, int32_t k, int32_t dw_f32,
+                                    int32_t accumulate, void* dw, void* stream) {
+  miep::GemmWeightArgs a{};
+  miep_status st = check_gemm(g, n, k, 0, &a.g);
+  if (st == MIEP_OK) st = check_array(dy, g->num_rows > 0, "dy");
+  if (st == MIEP_OK) st = check_source(g, x, x_rows, row_index);
+  if (st == MIEP_OK) st = check_array(dw, g->num_groups > 0, "dw");
+  if (st != MIEP_OK) return st;
+  if (accumulate && !dw_f32) return fail(MIEP_EINVAL, "accumulate needs an fp32 dw");
+  if (static_cast<int64_t>((n + 127) / 128) * ((k + 127) / 128) * g->num_groups > (1 << 24))
+    return fail(MIEP_EUNSUPPORTED, "dw has more than 2^24 tiles of 128 x 128");
+  a.q = dy;
+  a.p = x;
+  a.row_index = row_index;
+  a.p_rows = x_rows;
+  a.N = n;
+  a.K = k;
+  a.out = dw;
+  a.out_f32 = dw_f32 != 0;
+  a.accumulate = accumulate != 0;
+  return hip_status(miep::launch_gemm_weight(a, static_cast<hipStream_t>(stream)), "grouped gemm wgrad launch");
+}
+
+miep_status miep_grouped_gemm_fp8(const miep_row_groups* g, const uint8_t* x, const void* x_scales, int64_t x_rows,
+                                  const uint8_t* w, const void* w_scales, int32_t scales_ue8m0, int32_t n, int32_t k,
+                                  const int32_t* row_index, int32_t expected_rows, uint16_t* y, void* stream) {
+  miep::GemmRowsArgs a{};
+  miep_status st = check_gemm(g, n, k, expected_rows, &a.g);
+  if (st == MIEP_OK && k % miep::kFp8Group != 0) st = fail(MIEP_EINVAL, "FP8 products need k %% 128 == 0");
+  if (st == MIEP_OK) st = check_source(g, x, x_rows, row_index);
+  if (st == MIEP_OK) st = check_array(w, g->num_groups > 0, "w");
+  if (st == MIEP_OK) st = check_array(y, g->num_rows > 0, "y");
+  if (st != MIEP_OK) return st;
+  if ((x_rows > 0 && !x_scales) || (g->num_groups > 0 && !w_scales))
+    return fail(MIEP_EINVAL, "x_scales / w_scales NULL");
+  a.q = x;
+  a.p = w;
+  a.q_scales = x_scales;
+  a.p_scales = w_scales;
+  a.row_index = row_index;
+  a.q_rows = x_rows;
+  a.C = k;
+  a.NO = n;
+  a.out = y;
+  a.type = scales_ue8m0 ? miep::kGemmFp8Ue8m0 : miep::kGemmFp8;
+  a.expected = expected_rows;
+  return hip_status(miep::launch_gemm_rows(a, static_cast<hipStream_t>(stream)), "grouped fp8 gemm launch");
+}
+
+miep_status miep_swiglu(const miep_row_groups* g, const uint16_t* h, int32_t inner, uint16_t* out, void* stream) {
+  miep::SwigluArgs a{};
+  miep_status st = check_swiglu(g, h, inner, out, "a", &a);
+  if (st != MIEP_OK) return st;
+  a.out = out;
+  return hip_status(miep::launch_swiglu(a, miep::kSwigluBf16, static_cast<hipStream_t>(stream)), "swiglu launch");
+}
+
+miep_status miep_swiglu_fp8(const miep_row_groups* g, const uint16_t* h, int32_t inner, int32_t round_scale,
+                            uint8_t* out, float* a_scales, uint8_t* a_scales_ue8m0, void* stream) {
+  miep::SwigluArgs a{};
+  miep_status st = check_swiglu(g, h, inner, out, "a", &a);
+  if (st != MIEP_OK) return st;
+  if (inner % miep::kFp8Group != 0) return fail(MIEP_EINVAL, "the FP8 cast needs inner %% 128 == 0");
+  if (g->num_rows > 0 && g->num_groups > 0 && !a_scales) return fail(MIEP_EINVAL, "a_scales is NULL");
+  if (a_scales_ue8m0 && !round_scale) return fail(MIEP_EINVAL, "a_scales_ue8m0 needs round_scale");
+  a.out = out;
+  a.scales = a_scales;
+  a.scales_ue8m0 = a_scales_ue8m0;
+  a.round_scale = round_scale != 0;
+  return hip_status(miep::launch_swiglu(a, miep::kSwigluFp8, static_cast<hipStream_t>(stream)), "swiglu fp8 launch");
+}
+
+miep_status miep_swiglu_backward(const miep_row_groups* g, const uint16_t* da, const uint16_t* h, int32_t inner,
+                                 uint16_t* dh, void* stream) {
+  miep::SwigluArgs a{};
+  miep_status st = check_swiglu(g, h, inner, dh, "dh", &a);
+  if (st == MIEP_OK) st = check_array(da, g->num_rows > 0 && g->num_groups > 0, "da");
+  if (st != MIEP_OK) return st;
+  a.da = da;
+  a.out = dh;
+  return hip_status(miep::launch_swiglu(a, miep::kSwigluBackward, static_cast<hipStream_t>(stream)),
+                    "swiglu backward launch");
 }
 
 }  // extern "C"

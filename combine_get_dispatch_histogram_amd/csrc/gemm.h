@@ -1,0 +1,134 @@
+// gemm.h -- device building blocks of the grouped matrix products on gfx950:
+// asynchronous global -> LDS tiles, MFMA operand reads, and the walk from a
+// tile number to its group of rows.
+//
+// Both operands of a product are named by their place in the MFMA: P gives
+// the rows of the 16 x 16 result (four consecutive ones to a lane), Q its
+// columns (one to a lane).  The result of a rows kernel is out[q][p]: with the
+// weights as P and the tokens as Q a lane holds consecutive output channels of
+// one token, so results go to memory as wide row-contiguous vectors without a
+// transposition, and a token's scale is one value a lane.
+#pragma once
+
+#include "device.h"
+#include "kernels.h"
+
+namespace miep {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
+
+// A tile's K extent is 128 bytes a row in every type (64 bf16, 128 E4M3).
+constexpr int kStepBytes = 128;
+
+// Sixteen zero bytes in device memory: the source of every element of a tile
+// that lies past the contraction's end (0 * NaN would not be 0, so both
+// operands read zeros there).
+__device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0u, 0u, 0u, 0u};
+
+// One wavefront's 1 KiB of a tile: lane i's 16 bytes go to lds + 16 * i.  The
+// loads carry no register results; the kernel waits for them by count
+// (wait_tiles) before the barrier that publishes the tile.
+__device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
+}
+// The same from a scalar base and a 32-bit lane offset.
+__device__ __forceinline__ void dma16s(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+// 4 bytes a lane to lds + 4 * i.
+__device__ __forceinline__ void dma4(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory");
+}
+
+// One byte a lane, zero-extended to the dword at lds + 4 * i.
+__device__ __forceinline__ void dma1(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" ::"s"(lds), "v"(src) : "memory");
+}
+
+// Waits until at most N vector memory operations of this wavefront are in
+// flight and its LDS reads have returned, then for the workgroup: tiles whose
+// loads every wavefront has waited for may be read, and tiles that every
+// wavefront has read may be overwritten.
+template <int N>
+__device__ __forceinline__ void wait_tiles() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+template <class T>
+__device__ __forceinline__ T lds_read(uint32_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) T*>(at);
+}
+__device__ __forceinline__ i16x4 lds_read_tr(uint32_t at) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) i16x4*>(at));
+}
+
+// ---- the groups' rows, never trusted: a group reads as the part of
+// [begin, begin + rows) inside [0, limit).
+__device__ __forceinline__ void group_range(const GroupArgs& g, int i, int64_t* begin, int* rows) {
+  const int64_t b = g.begin ? g.begin[i] : static_cast<int64_t>(i) * g.stride;
+  int64_t n = g.rows[i];
+  if (!g.begin && n > g.stride) n = g.stride;
+  if (b < 0 || b >= g.limit) n = 0;
+  else if (n > g.limit - b) n = g.limit - b;
+  *begin = b;
+  *rows = n > 0 ? static_cast<int>(n) : 0;
+}
+
+struct TileAt {
+  int group;       // -1: past the last tile
+  int first;       // the tile's place among the group's (ceil(rows / bq) * per) tiles
+  int64_t begin;
+  int rows;
+};
+
+// Tile t of the sequence in which group i has ceil(rows / bq) * per tiles.
+// Every wavefront walks for itself: one load a lane for each 64 groups and a
+// scan of the lane counts.  *total (when wanted) is the number of tiles.
+__device__ __forceinline__ TileAt find_tile(const GroupArgs& g, int bq, int per, int t) {
+  const int lane = lane_id();
+  int before = 0;
+  TileAt r;
+  r.group = -1;
+  r.first = 0;
+  r.begin = 0;
+  r.rows = 0;
+  for (int g0 = 0; g0 < g.G; g0 += kWave) {
+    int64_t b = 0;
+    int n = 0;
+    if (g0 + lane < g.G) group_range(g, g0 + lane, &b, &n);
+    const int tiles = (n + bq - 1) / bq * per;
+    const int inc = wave_inclusive_scan(tiles);
+    const uint64_t past = ballot(before + inc > t);
+    if (past != 0) {
+      const int l = __builtin_ctzll(past);
+      r.group = g0 + l;
+      r.first = t - before - (readlane(inc, l) - readlane(tiles, l));
+      r.rows = readlane(n, l);
+      r.begin = (static_cast<int64_t>(readlane(static_cast<int>(b >> 32), l)) << 32) |
+                static_cast<uint32_t>(readlane(static_cast<int>(b), l));
+      return r;
+    }
+    before += readlane(inc, 63);
+  }
+  return r;
+}
+
+__device__ __forceinline__ int count_tiles(const GroupArgs& g, int bq, int per) {
+  const int lane = lane_id();
+  int total = 0;
+  for (int g0 = 0; g0 < g.G; g0 += kWave) {
+    int64_t b = 0;
+    int n = 0;
+    if (g0 + lane < g.G) group_range(g, g0 + lane, &b, &n);
+    total += readlane(wave_inclusive_scan((n + bq - 1) / bq * per), 63);
+  }
+  return total;
+}
+
+}  // namespace miep

@@ -1,0 +1,355 @@
+// gemm_rows.h -- the rows kernel of the grouped products (forward, and the
+// rows' gradient), instantiated for bf16 in gemm.hip and for E4M3 in
+// gemm_fp8.hip.
+//
+//   out[i][p] = sum_c Q[src(i)][c] * P_g[p][c]        for the rows i of group g
+//
+// A workgroup computes BQ rows x BP output channels.  Each 128-byte step of
+// the contraction comes to LDS by asynchronous 16-byte loads, NST buffers deep,
+// with one barrier a step; wavefront (wp, wq) multiplies its BP/WP x BQ/WQ part
+// with 16x16 MFMAs.
+#pragma once
+
+#include "gemm.h"
+
+namespace miep {
+
+template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NST>
+struct RowsTile {
+  static constexpr int kWaves = WP * WQ;
+  static constexpr int kTP = BP / WP / 16, kTQ = BQ / WQ / 16;       // 16 x 16 results a wavefront
+  static constexpr bool kFp8 = EL != kGemmBf16;
+  static constexpr int kEB = kFp8 ? 1 : 2;                           // bytes of an element
+  static constexpr int kPBytes = BP * kStepBytes, kQBytes = BQ * kStepBytes;
+  // FP8 scales of a stage, a dword each: the rows' (BQ, at least one load's
+  // 64), then the P blocks' (one load; a tile has at most 2)
+  static constexpr int kQScales = BQ < kWave ? kWave : BQ;
+  static constexpr int kScaleBytes = kFp8 ? kQScales * 4 + 256 : 0;
+  static_assert(!kFp8 || kQScales / kWave < kWaves, "one scale load a wavefront");
+  static constexpr int kStage = kPBytes + kQBytes + kScaleBytes;
+  static constexpr int kPLoads = kPBytes / 1024 / kWaves, kQLoads = kQBytes / 1024 / kWaves;
+  static constexpr int kLoads = kPLoads + kQLoads + (kFp8 ? 1 : 0);  // a wavefront's loads of a stage
+  static_assert(kPLoads * kWaves * 1024 == kPBytes && kQLoads * kWaves * 1024 == kQBytes, "whole loads a wavefront");
+  static_assert(kTP % 2 == 0 && kTQ >= 1 && NST >= 2 && kLoads * (NST - 1) < 64, "tile shape");
+  static_assert(!(PT && kFp8), "the transposed operand is bf16");
+};
+
+// Swizzles: the 16-byte chunk c of a tile row is kept at chunk c ^ s(row), so
+// that the 16 rows of one operand read lie in 16 different 16-byte banks
+// groups of the 256-byte LDS line (rows are 128 bytes: their parity is one
+// bit of the place, s the other three).  Q reads 16 consecutive rows; P reads
+// rows 4*TP*(m/4) + 4*i + m%4 (m = lane % 16), which gives a lane the 4*TP
+// consecutive output channels of its results.
+__device__ __forceinline__ int swz_q(int row) { return (row >> 1) & 7; }
+template <int TP>
+__device__ __forceinline__ int swz_p(int row) {
+  return ((row >> 1) & 1) | (((row / (4 * TP)) & 3) << 1);
+}
+// A transposed tile has 64 contraction rows of BP channels.  A transposing
+// read takes 32 bytes of each of 4 rows a 16-lane group: rows 0-3, 8-11 (then
+// 4-7, 12-15) by half wavefront; f spreads those 8 rows over the line.
+__device__ __forceinline__ int swz_t(int row) { return ((row & 3) | ((row >> 1) & 4)) << 1; }
+
+template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NST>
+__global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsArgs a) {
+  using S = RowsTile<EL, PT, GATHER, BP, BQ, WP, WQ, NST>;
+  constexpr int TP = S::kTP, TQ = S::kTQ, EB = S::kEB;
+  __shared__ __align__(1024) uint8_t lds_mem[NST * S::kStage];
+  const uint32_t lds = (uint32_t)(uintptr_t)(lds_byte*)lds_mem;
+
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+  // consecutive wavefronts share their rows of Q, so that the wavefronts a
+  // short tile leaves idle are spread evenly over the four SIMDs
+  const int wp = wave % WP, wq = wave / WP;
+  const int m = lane & 15, quarter = lane >> 4;
+
+  const int NO = a.NO, C = a.C;
+  const int ntiles = (NO + BP - 1) / BP;
+  const int64_t ldq = static_cast<int64_t>(C) * EB;                   // bytes
+  const int64_t ldp = static_cast<int64_t>(PT ? NO : C) * EB;
+  const int cbytes = C * EB;                                          // contraction, bytes of a k-major row
+  const int KE = kStepBytes / EB;
+  const int nk = (C + KE - 1) / KE;
+  const bool ragged_end = C % KE != 0;
+  const int64_t kb = C / kFp8Group;                                       // scale blocks of a row (FP8)
+
+  int total = count_tiles(a.g, BQ, ntiles);
+  if (total < 0 || total > a.max_tiles) total = a.max_tiles;
+  // Workgroups go to the 8 XCDs in turn: XCD x walks the x-th eighth of the
+  // tiles, so tiles that share weights or rows meet in one L2.
+  const int chunk = (total + 7) / 8;
+  const int xcd = blockIdx.x & 7;
+  const int end = min(total, (xcd + 1) * chunk);
+
+  for (int t = xcd * chunk + (blockIdx.x >> 3); t < end; t += gridDim.x >> 3) {
+    const TileAt at = find_tile(a.g, BQ, ntiles, t);
+    if (at.group < 0) break;
+    const int mtiles = (at.rows + BQ - 1) / BQ;
+    const int first = min(max(at.first, 0), mtiles * ntiles - 1);
+    const int pt = first / mtiles, qt = first - pt * mtiles;
+    const int p0 = pt * BP, q0 = qt * BQ;
+    const int live = min(BQ, at.rows - q0);                           // rows of this tile
+    const int64_t row0 = at.begin + q0;
+    const uint8_t* pg = static_cast<const uint8_t*>(a.p) + static_cast<int64_t>(at.group) * NO * C * EB;
+
+    // Sources of this lane's 16 bytes of every load of a stage.
+    const uint8_t* pbase = pg + (PT ? static_cast<int64_t>(p0) * EB : static_cast<int64_t>(p0) * ldp);
+    uint32_t poff[S::kPLoads];
+#pragma unroll
+    for (int i = 0; i < S::kPLoads; ++i) {
+      const int l = i * S::kWaves + wave;
+      if constexpr (PT) {
+        constexpr int CH = BP * 2 / 16;                               // chunks of a tile row
+        const int row = l * (64 / CH) + lane / CH;
+        int col = ((lane % CH) ^ swz_t(row)) * 16;
+        if (p0 + col / 2 >= NO) col = 0;
+        poff[i] = static_cast<uint32_t>(row * ldp + col);
+      } else {
+        int row = l * 8 + lane / 8;
+        const int c = (lane & 7) ^ swz_p<TP>(row);
+        if (p0 + row >= NO) row = NO - 1 - p0;
+        poff[i] = static_cast<uint32_t>(row * ldp + c * 16);
+      }
+    }
+    const uint8_t* qbase = static_cast<const uint8_t*>(a.q) + (GATHER ? 0 : row0 * ldq);
+    uint32_t qoff[GATHER ? 1 : S::kQLoads];
+    const uint8_t* qptr[GATHER ? S::kQLoads : 1];
+    int qc[S::kQLoads];                                               // its chunk of the step
+#pragma unroll
+    for (int i = 0; i < S::kQLoads; ++i) {
+      const int l = i * S::kWaves + wave;
+      int row = l * 8 + lane / 8;
+      qc[i] = (lane & 7) ^ swz_q(row);
+      row = min(row, live - 1);
+      if constexpr (GATHER) {
+        const int64_t src = a.row_index[row0 + row];
+        qptr[i] = (src >= 0 && src < a.q_rows ? qbase + src * ldq : pg) + qc[i] * 16;   // a row without a source reads weights, and stores zeros
+      } else {
+        qoff[i] = static_cast<uint32_t>(row * ldq + qc[i] * 16);
+      }
+    }
+    // FP8: this wavefront's one load of a stage's scales -- 64 rows of Q's, or
+    // the P blocks' (every further wavefront repeats those)
+    constexpr int SB = EL == kGemmFp8 ? 4 : 1;                        // bytes of a scale
+    const uint8_t* sptr = nullptr;
+    uint32_t sto = 0;
+    if constexpr (S::kFp8) {
+      constexpr int QL = S::kQScales / kWave;
+      const int64_t pb = static_cast<int64_t>(at.group) * ((NO + 127) / 128);
+      const uint8_t* ps = static_cast<const uint8_t*>(a.p_scales) + pb * kb * SB;
+      if (wave < QL) {
+        int64_t src = row0 + min((wave * kWave + lane) % BQ, live - 1);
+        if constexpr (GATHER) {
+          src = a.row_index[src];
+          if (src >= a.q_rows) src = -1;
+        }
+        sptr = src >= 0 ? static_cast<const uint8_t*>(a.q_scales) + src * kb * SB : ps;
+      } else {
+        sptr = ps + static_cast<int64_t>(min(p0 / 128 + lane, (NO - 1) / 128)) * kb * SB;
+      }
+      sto = S::kPBytes + S::kQBytes + min(wave, QL) * 256;
+    }
+
+    auto issue = [&](int step, int buf) {
+      const uint32_t st = lds + buf * S::kStage;
+      const bool tail = ragged_end && step == nk - 1;
+      const uint8_t* pb = pbase + static_cast<int64_t>(step) * (PT ? (kStepBytes / 2) * ldp : kStepBytes);
+#pragma unroll
+      for (int i = 0; i < S::kPLoads; ++i) {
+        const int l = i * S::kWaves + wave;
+        if (!tail) {
+          dma16s(pb, poff[i], st + l * 1024);
+        } else {
+          bool in;
+          if constexpr (PT) in = step * KE + l * (64 / (BP * 2 / 16)) + lane / (BP * 2 / 16) < C;
+          else in = step * kStepBytes + ((lane & 7) ^ swz_p<TP>(l * 8 + lane / 8)) * 16 < cbytes;
+          dma16(in ? static_cast<const void*>(pb + poff[i]) : static_cast<const void*>(g_zero16), st + l * 1024);
+        }
+      }
+      const uint8_t* qb = qbase + static_cast<int64_t>(step) * kStepBytes;
+#pragma unroll
+      for (int i = 0; i < S::kQLoads; ++i) {
+        const uint32_t to = st + S::kPBytes + (i * S::kWaves + wave) * 1024;
+        const bool in = step * kStepBytes + qc[i] * 16 < cbytes;
+        if constexpr (GATHER) {
+          const void* src = qptr[i] + static_cast<int64_t>(step) * kStepBytes;
+          dma16(!tail || in ? src : static_cast<const void*>(g_zero16), to);
+        } else {
+          if (!tail) dma16s(qb, qoff[i], to);
+          else dma16(in ? static_cast<const void*>(qb + qoff[i]) : static_cast<const void*>(g_zero16), to);
+        }
+      }
+      if constexpr (S::kFp8) {
+        if constexpr (SB == 4) dma4(sptr + static_cast<int64_t>(step) * 4, st + sto);
+        else dma1(sptr + step, st + sto);
+      }
+    };
+
+    f32x4 acc[TP][TQ];
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const bool busy = wq * 16 * TQ < live;
+    // lane addresses of the operand reads, within a stage
+    uint32_t pa[PT ? TP : 2], qa[2];
+    if constexpr (PT) {
+#pragma unroll
+      for (int i = 0; i < TP; ++i) {
+        const int row = quarter * 8 + m / 4;
+        const int ch = wp * 2 * TP + i * 2 + (m & 3) / 2;
+        pa[i] = row * (2 * BP) + (ch ^ swz_t(row)) * 16 + (m & 1) * 8;
+      }
+    } else {
+      const int row = wp * 16 * TP + (m / 4) * 4 * TP + (m & 3);
+      pa[0] = row * kStepBytes + (quarter ^ swz_p<TP>(row)) * 16;
+      pa[1] = pa[0] ^ 64;
+    }
+    {
+      const int row = wq * 16 * TQ + m;
+      qa[0] = S::kPBytes + row * kStepBytes + (quarter ^ swz_q(row)) * 16;
+      qa[1] = qa[0] ^ 64;
+    }
+
+    wait_tiles<0>();                                                  // the previous tile's reads
+#pragma unroll
+    for (int s = 0; s < NST - 1; ++s)
+      if (s < nk) issue(s, s);
+
+    int buf = 0;
+    for (int step = 0; step < nk; ++step) {
+      if (step + NST - 2 < nk) wait_tiles<(NST - 2) * S::kLoads>();
+      else wait_tiles<0>();
+      const int ahead = step + NST - 1;
+      if (ahead < nk) issue(ahead, buf == 0 ? NST - 1 : buf - 1);
+      const uint32_t st = lds + buf * S::kStage;
+      buf = buf == NST - 1 ? 0 : buf + 1;
+      if (!busy) continue;
+      if constexpr (!S::kFp8) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          bf16x8 pf[TP], qf[TQ];
+#pragma unroll
+          for (int j = 0; j < TQ; ++j) qf[j] = lds_read<bf16x8>(st + qa[h] + j * 16 * kStepBytes);
+#pragma unroll
+          for (int i = 0; i < TP; ++i) {
+            if constexpr (PT) {
+              struct { i16x4 lo, hi; } t;
+              t.lo = lds_read_tr(st + pa[i] + h * 32 * 2 * BP);
+              t.hi = lds_read_tr(st + pa[i] + (h * 32 + 4) * 2 * BP);
+              pf[i] = __builtin_bit_cast(bf16x8, t);
+            } else {
+              pf[i] = lds_read<bf16x8>(st + pa[h] + i * 4 * kStepBytes);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < TP; ++i)
+#pragma unroll
+            for (int j = 0; j < TQ; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[i], qf[j], acc[i][j], 0, 0, 0);
+        }
+      } else {
+        i32x8 qf[TQ];
+#pragma unroll
+        for (int j = 0; j < TQ; ++j) {
+          struct { i32x4 lo, hi; } t;
+          t.lo = lds_read<i32x4>(st + qa[0] + j * 16 * kStepBytes);
+          t.hi = lds_read<i32x4>(st + qa[1] + j * 16 * kStepBytes);
+          qf[j] = __builtin_bit_cast(i32x8, t);
+        }
+        // fp32 scales multiply each 128-channel block's fp32 sum; power-of-two
+        // scales go into the MFMA as their exponent bytes
+        const uint32_t sat = st + S::kPBytes + S::kQBytes;
+        const uint32_t pat = sat + S::kQScales * 4 + wp * 16 * TP / 128 * 4;
+        float s[TQ];
+        int e[TQ], ep = 0;
+        if constexpr (EL == kGemmFp8) {
+          const float sp = lds_read<float>(pat);
+#pragma unroll
+          for (int j = 0; j < TQ; ++j) s[j] = sp * lds_read<float>(sat + ((wq * TQ + j) * 16 + m) * 4);
+        } else {
+          ep = lds_read<int>(pat);
+#pragma unroll
+          for (int j = 0; j < TQ; ++j) e[j] = lds_read<int>(sat + ((wq * TQ + j) * 16 + m) * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < TP; ++i) {
+          struct { i32x4 lo, hi; } t;
+          t.lo = lds_read<i32x4>(st + pa[0] + i * 4 * kStepBytes);
+          t.hi = lds_read<i32x4>(st + pa[1] + i * 4 * kStepBytes);
+          const i32x8 pf = __builtin_bit_cast(i32x8, t);
+#pragma unroll
+          for (int j = 0; j < TQ; ++j) {
+            if constexpr (EL == kGemmFp8) {
+              const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+              const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf, qf[j], z, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[r], s[j], acc[i][j][r]);
+            } else {
+              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf, qf[j], acc[i][j], 0, 0, 0, ep, 0, e[j]);
+            }
+          }
+        }
+      }
+    }
+
+    if (!busy) continue;
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) {
+      const int row = (wq * TQ + j) * 16 + m;
+      if (row >= live) continue;
+      bool none = false;
+      if constexpr (GATHER) {
+        const int src = a.row_index[row0 + row];
+        none = src < 0 || src >= a.q_rows;
+      }
+      uint16_t* o = a.out + (row0 + row) * NO;
+      if constexpr (PT) {
+#pragma unroll
+        for (int i = 0; i < TP; ++i) {
+          const int p = p0 + (wp * TP + i) * 16 + quarter * 4;
+          v2u v{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+          if (p < NO) *reinterpret_cast<v2u*>(o + p) = v;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < TP; i += 2) {
+          const int p = p0 + wp * 16 * TP + quarter * 4 * TP + i * 4;
+          v4u v{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]),
+                pack_bf16x2(acc[i + 1][j][0], acc[i + 1][j][1]), pack_bf16x2(acc[i + 1][j][2], acc[i + 1][j][3])};
+          if (none) v = v4u{0u, 0u, 0u, 0u};
+          if (p < NO) *reinterpret_cast<v4u*>(o + p) = v;
+        }
+      }
+    }
+  }
+}
+
+template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NST>
+hipError_t launch_rows_tile(GemmRowsArgs a, hipStream_t st) {
+  const int64_t per = (a.NO + BP - 1) / BP;
+  const int64_t most = ((a.g.limit + BQ - 1) / BQ + a.g.G) * per;     // disjoint groups have no more tiles
+  if (most > (1ll << 31) - 1) return hipErrorInvalidConfiguration;
+  a.max_tiles = static_cast<int>(most);
+  int per_cu = 0;
+  // resident workgroups: by LDS (160 KiB a CU) and two wavefronts a SIMD
+  per_cu = 163840 / (NST * RowsTile<EL, PT, GATHER, BP, BQ, WP, WQ, NST>::kStage);
+  const int by_waves = 8 / (WP * WQ);
+  per_cu = per_cu < by_waves ? per_cu : by_waves;
+  int64_t grid = 256ll * (per_cu > 0 ? per_cu : 1);
+  if (grid > (most + 7) / 8 * 8) grid = (most + 7) / 8 * 8;
+  gemm_rows_kernel<EL, PT, GATHER, BP, BQ, WP, WQ, NST><<<static_cast<unsigned>(grid), WP * WQ * kWave, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+template <int EL, bool PT, bool GATHER>
+hipError_t launch_rows(const GemmRowsArgs& a, hipStream_t st) {
+  if (a.expected <= 32) return launch_rows_tile<EL, PT, GATHER, 128, 32, 4, 1, EL == kGemmBf16 ? 4 : 3>(a, st);
+  if (a.expected <= 64) return launch_rows_tile<EL, PT, GATHER, 128, 64, 2, 2, 3>(a, st);
+  if (a.expected <= 128) return launch_rows_tile<EL, PT, GATHER, 256, 128, 4, 2, 3>(a, st);
+  return launch_rows_tile<EL, PT, GATHER, 256, 256, 2, 4, 2>(a, st);
+}
+
+}  // namespace miep

@@ -199,6 +199,98 @@ hipError_t launch_ll_combine(const LLCombineArgs& a, hipStream_t st);
 hipError_t launch_mask_set(int32_t* mask, int rank, int value, hipStream_t st);
 hipError_t launch_copy_i32(const int32_t* src, int32_t* dst, int n, hipStream_t st);
 
+// ---- groups of rows of one layout: group i holds rows[i] rows from begin[i]
+// (null: from i * stride, at most stride of them).  Device data, never
+// trusted: kernels read each group as its part inside [0, limit).
+struct GroupArgs {
+  int G;
+  int stride;
+  const int32_t* begin;
+  const int32_t* rows;
+  int64_t limit;             // rows of the layout
+};
+
+// ---- grouped products, rows side: out[i][p] = sum_c Q[src(i)][c] * P_g[p][c]
+// for the rows i of every group g (P_g transposed for the rows' gradient)
+enum GemmType { kGemmBf16 = 0, kGemmFp8 = 1, kGemmFp8Ue8m0 = 2 };
+struct GemmRowsArgs {
+  GroupArgs g;
+  const void* q;               // [q_rows][C]
+  const void* p;               // [G][NO][C], or [G][C][NO] (bf16, transposed)
+  const void* q_scales;        // FP8: [q_rows][C/128]
+  const void* p_scales;        // FP8: [G][ceil(NO/128)][C/128]
+  const int32_t* row_index;    // [limit] source row of each layout row, or null (itself)
+  int64_t q_rows;
+  int C, NO;                   // contraction and output width, elements
+  uint16_t* out;               // [limit][NO]
+  int type, transposed;
+  int expected;                // rows a group is expected to hold (0: limit / G)
+  int max_tiles;               // set by the launcher
+};
+hipError_t launch_gemm_rows(const GemmRowsArgs& a, hipStream_t st);
+
+// ---- grouped products, weight gradient: out_g[n][k] (+)= sum over the rows i
+// of group g of Q[i][n] * P[src(i)][k]
+struct GemmWeightArgs {
+  GroupArgs g;
+  const uint16_t* q;           // [limit][N] output gradients
+  const uint16_t* p;           // [p_rows][K] the product's rows
+  const int32_t* row_index;    // [limit] or null
+  int64_t p_rows;
+  int N, K;
+  void* out;                   // [G][N][K] fp32 or bf16
+  int out_f32, accumulate;
+};
+hipError_t launch_gemm_weight(const GemmWeightArgs& a, hipStream_t st);
+
+// ---- activation between the two products: rows of [gate | up], 2 * I wide
+struct SwigluArgs {
+  GroupArgs g;
+  int I;
+  int round_scale;
+  const uint16_t* h;         // [limit][2 * I]
+  const uint16_t* da;        // backward: [limit][I]
+  void* out;                 // [limit][I] bf16 or E4M3; backward: [limit][2 * I] bf16
+  float* scales;             // FP8: [limit][I/128]
+  uint8_t* scales_ue8m0;     // FP8: [limit][I/128] or null
+  int rows_per_tile, max_tiles;  // set by the launcher
+};
+enum SwigluKind { kSwigluBf16 = 0, kSwigluFp8 = 1, kSwigluBackward = 2 };
+hipError_t launch_swiglu(const SwigluArgs& a, int kind, hipStream_t st);
+
+// ---- expert order: stable counting sort of the received rows' (row, k)
+// entries by expert, in `parts` workgroups a rank
+constexpr int kMaxLocalExperts = 2048;   // LDS counters of one rank
+struct OrderArgs {
+  int64_t rows;              // receive rows allocated
+  int K, E, R, L, align, parts;
+  int64_t slots;             // slots allocated
+  const int64_t* topk;       // [rows][K] local expert of each entry, or -1
+  const int32_t* off;        // [R+1]
+  int32_t* counts;           // [parts][E] workspace
+  int32_t* begin;            // [E]
+  int32_t* group_rows;       // [E]
+  int32_t* slot_row;         // [slots]
+  int32_t* row_slot;         // [rows][K]
+  int32_t* status;           // or null
+};
+hipError_t launch_order(const OrderArgs& a, hipStream_t st);
+
+// ---- expert reduce: y[row] = sum over k of w[row][k] * z[slot(row, k)], and its gradient
+struct ReduceArgs {
+  int64_t rows, slots;
+  int H, K;
+  const int32_t* row_slot;   // [rows][K]
+  const int32_t* num_rows;   // device: rows in use, or null (all)
+  const float* w;            // [rows][K] or null (1)
+  const uint16_t* z;         // [slots][H]
+  const uint16_t* dy;        // backward: [rows][H]
+  uint16_t* out;             // y [rows][H]; backward: dz [slots][H]
+  float* dw;                 // backward: [rows][K] or null
+};
+hipError_t launch_reduce(const ReduceArgs& a, hipStream_t st);
+hipError_t launch_reduce_backward(const ReduceArgs& a, hipStream_t st);
+
 // Optional launch-geometry overrides read once from the environment
 // (MIEP_PACK_VPL, MIEP_PACK_SLICES, MIEP_COMBINE_VPL, MIEP_COMBINE_SLICES,
 // MIEP_COMBINE_MAXR, MIEP_PACK_NT, MIEP_COMBINE_NT, MIEP_LL_SPLIT,

@@ -1,0 +1,319 @@
+// order.hip -- between a normal dispatch and its experts: received rows to
+// slots in expert order, and expert outputs back to received rows.
+//
+// expert_order is a stable counting sort of the (row, k) entries by expert.
+// A rank's rows name only its own L experts, so the work is cut by rank and,
+// inside a rank, into parts: one kernel counts each part's entries per expert;
+// the second starts every counter at its expert's first slot plus the entries
+// of the parts (and, in the part, of the wavefronts) before it, and gives out
+// slots 64 entries at a time, equal experts in lane order.  No counter is
+// shared between wavefronts then, so the order never depends on timing.
+#include "device.h"
+#include "kernels.h"
+
+namespace miep {
+
+constexpr int kOrderWaves = 4;
+
+// Rows [first, last) of part p of rank r, inside the allocated rows whatever
+// the offsets hold.
+__device__ __forceinline__ void part_rows(const OrderArgs& a, int r, int p, int64_t* first, int64_t* last) {
+  int64_t lo = a.off[r], hi = a.off[r + 1];
+  lo = lo < 0 ? 0 : lo > a.rows ? a.rows : lo;
+  hi = hi < lo ? lo : hi > a.rows ? a.rows : hi;
+  *first = lo + (hi - lo) * p / a.parts;
+  *last = lo + (hi - lo) * (p + 1) / a.parts;
+}
+
+__global__ __launch_bounds__(256) void order_count_kernel(OrderArgs a) {
+  __shared__ int count[kMaxLocalExperts];
+  const int r = blockIdx.x / a.parts, p = blockIdx.x - r * a.parts;
+  for (int l = threadIdx.x; l < a.L; l += 256) count[l] = 0;
+  __syncthreads();
+  int64_t first, last;
+  part_rows(a, r, p, &first, &last);
+  for (int64_t i = first * a.K + threadIdx.x; i < last * a.K; i += 256) {
+    const int64_t e = a.topk[i];
+    if (e >= 0 && e < a.L) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  int32_t* out = a.counts + static_cast<int64_t>(p) * a.E + r * a.L;
+  for (int l = threadIdx.x; l < a.L; l += 256) out[l] = count[l];
+}
+
+__global__ __launch_bounds__(256) void order_place_kernel(OrderArgs a) {
+  __shared__ int next[kOrderWaves][kMaxLocalExperts];   // each wavefront's next slot per expert
+  __shared__ int sums[256], waves[kOrderWaves];
+  const int tid = threadIdx.x, lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int r = blockIdx.x / a.parts, p = blockIdx.x - r * a.parts;
+  int64_t first, last;
+  part_rows(a, r, p, &first, &last);
+  // this wavefront's entries
+  const int64_t entries = (last - first) * a.K;
+  const int64_t i0 = first * a.K + entries * wave / kOrderWaves, i1 = first * a.K + entries * (wave + 1) / kOrderWaves;
+
+  for (int l = tid; l < kOrderWaves * a.L; l += 256) next[l / a.L][l % a.L] = 0;
+  __syncthreads();
+  for (int64_t i = i0 + lane; i < i1; i += kWave) {
+    const int64_t e = a.topk[i];
+    if (e >= 0 && e < a.L) atomicAdd(&next[wave][e], 1);
+  }
+  __syncthreads();
+
+  // first slots: prefix of the experts' aligned totals, 256 experts at a time
+  // (fewer experts: several threads add up the parts of one)
+  int64_t slots = 0;
+  int width = 256;
+  while (width / 2 >= a.E) width /= 2;
+  for (int e0 = 0; e0 < a.E; e0 += 256) {
+    const int e = e0 + (tid & (width - 1));
+    int all = 0, before = 0;
+    if (e < a.E)
+      for (int q = tid / width; q < a.parts; q += 256 / width) {
+        const int c = a.counts[static_cast<int64_t>(q) * a.E + e];
+        all += c;
+        before += q < p ? c : 0;
+      }
+    if (width < 256) {
+      __syncthreads();
+      if (tid < width) sums[tid] = 0;
+      if (tid >= 128 && width <= 128) sums[tid] = 0;
+      __syncthreads();
+      atomicAdd(&sums[tid & (width - 1)], all);
+      atomicAdd(&sums[128 + (tid & (width - 1))], before);
+      __syncthreads();
+      all = tid < width ? sums[tid] : 0;
+      before = tid < width ? sums[128 + tid] : 0;
+    }
+    const bool mine = e < a.E && tid < width;
+    const int padded = mine ? (all + a.align - 1) / a.align * a.align : 0;
+    const int inc = wave_inclusive_scan(padded);
+    __syncthreads();
+    if (lane == kWave - 1) waves[wave] = inc;
+    __syncthreads();
+    int64_t at = slots + inc - padded;
+    for (int w = 0; w < kOrderWaves; ++w) {
+      if (w < wave) at += waves[w];
+      slots += waves[w];
+    }
+    if (mine) {
+      if (blockIdx.x == 0) {
+        a.begin[e] = static_cast<int>(at);
+        a.group_rows[e] = all;
+      }
+      if (e / a.L == r) {
+        int s = static_cast<int>(at) + before;
+        for (int w = 0; w < kOrderWaves; ++w) {
+          const int c = next[w][e - r * a.L];
+          next[w][e - r * a.L] = s;
+          s += c;
+        }
+        if (p == 0)
+          for (int64_t q = at + all; q < at + padded; ++q)
+            if (q < a.slots) a.slot_row[q] = -1;
+      }
+    }
+  }
+  __syncthreads();
+
+  int bits = 0;
+  while ((1 << bits) < a.L) ++bits;
+  for (int64_t i = i0; i < i1; i += kWave) {
+    const bool in = i + lane < i1;
+    const int64_t e64 = in ? a.topk[i + lane] : -1;
+    const bool named = e64 >= 0 && e64 < a.L;
+    const int e = named ? static_cast<int>(e64) : 0;
+    uint64_t same = ballot(named);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t set = ballot((e >> b) & 1);
+      same &= ((e >> b) & 1) ? set : ~set;
+    }
+    int slot = -1;
+    if (named) {
+      const int base = next[wave][e];
+      slot = base + __popcll(same & lanemask_lt());
+      if ((same >> lane) == 1) next[wave][e] = slot + 1;              // the last of the equal ones
+      if (slot < a.slots) a.slot_row[slot] = static_cast<int>((i + lane) / a.K);
+      else slot = -1;
+    }
+    if (in) a.row_slot[i + lane] = slot;
+  }
+
+  // slots behind the last expert's, and rows behind the last received one
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t s = slots + blockIdx.x * 256ll + tid; s < a.slots; s += step) a.slot_row[s] = -1;
+  int64_t end = a.off[a.R];
+  end = end < 0 ? 0 : end > a.rows ? a.rows : end;
+  for (int64_t i = end * a.K + blockIdx.x * 256ll + tid; i < a.rows * a.K; i += step) a.row_slot[i] = -1;
+  if (a.status && blockIdx.x == 0 && tid == 0) *a.status = slots > a.slots ? kStatusCapacity : 0;
+}
+
+hipError_t launch_order(const OrderArgs& args, hipStream_t st) {
+  OrderArgs a = args;
+  // a part is worth about 2048 entries (8 a lane): fewer leave more to sum up than to sort
+  const int64_t want = (a.rows * a.K / a.R + 2047) / 2048;
+  if (want < a.parts) a.parts = want < 1 ? 1 : static_cast<int>(want);
+  const int64_t grid = static_cast<int64_t>(a.parts) * a.R;
+  if (grid > max_blocks(256)) return hipErrorInvalidConfiguration;
+  order_count_kernel<<<static_cast<unsigned>(grid), 256, 0, st>>>(a);
+  order_place_kernel<<<static_cast<unsigned>(grid), 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+// ---- reduce
+__device__ __forceinline__ void widen(const v4u& v, float (&f)[8]) {
+  f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
+  f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
+}
+__device__ __forceinline__ v4u narrow(const float (&f)[8]) {
+  return v4u{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+}
+
+// One workgroup a row; a thread owns 8 channels at a time.  The row's slots
+// and weights are read by the lanes k of every wavefront and broadcast.
+// Terms are added in ascending k in fp32, one rounding to bf16.
+__global__ __launch_bounds__(256) void reduce_kernel(ReduceArgs a) {
+  const int lane = lane_id();
+  int64_t rows = a.rows;
+  if (a.num_rows) rows = min(rows, static_cast<int64_t>(max(*a.num_rows, 0)));
+  const int nv = a.H / 8;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    int slot = -1;
+    float w = 1.f;
+    if (lane < a.K) {
+      slot = a.row_slot[row * a.K + lane];
+      if (a.w) w = a.w[row * a.K + lane];
+    }
+    const uint64_t live = ballot(slot >= 0 && slot < a.slots);
+    for (int v = threadIdx.x; v < nv; v += 256) {
+      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      uint64_t left = live;
+      while (left) {
+        v4u d[4];
+        float g[4];
+        int n = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          g[q] = 0.f;
+          if (left) {
+            const int b = __builtin_ctzll(left);
+            left &= left - 1;
+            g[q] = __int_as_float(readlane(__float_as_int(w), b));
+            d[q] = ld16(a.z + static_cast<int64_t>(readlane(slot, b)) * a.H + v * 8);
+            n = q + 1;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < n) {
+            float f[8];
+            widen(d[q], f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[k] = fmaf(g[q], f[k], acc[k]);
+          }
+      }
+      *reinterpret_cast<v4u*>(a.out + row * a.H + v * 8) = narrow(acc);
+    }
+  }
+}
+
+// Gradient: dz[slot(row, k)] = w[row][k] * dy[row], dw[row][k] = <dy[row],
+// z[slot(row, k)]>.  Eight entries at a time share one read of dy's row; the
+// dot products are summed over lanes, then wavefronts, in a fixed order.
+__global__ __launch_bounds__(256) void reduce_backward_kernel(ReduceArgs a) {
+  constexpr int NB = 8;
+  __shared__ float part[4][NB];
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+  int64_t rows = a.rows;
+  if (a.num_rows) rows = min(rows, static_cast<int64_t>(max(*a.num_rows, 0)));
+  const int nv = a.H / 8;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    int slot = -1;
+    float w = 1.f;
+    if (lane < a.K) {
+      slot = a.row_slot[row * a.K + lane];
+      if (a.w) w = a.w[row * a.K + lane];
+    }
+    const bool ok = slot >= 0 && slot < a.slots;
+    uint64_t left = ballot(ok);
+    if (a.dw && wave == 0 && lane < a.K && !ok) a.dw[row * a.K + lane] = 0.f;
+    while (left) {
+      int64_t at[NB];
+      int which[NB];
+      float g[NB], dot[NB];
+      int n = 0;
+#pragma unroll
+      for (int q = 0; q < NB; ++q) {
+        dot[q] = 0.f;
+        g[q] = 0.f;
+        at[q] = 0;
+        which[q] = 0;
+        if (left) {
+          const int b = __builtin_ctzll(left);
+          left &= left - 1;
+          which[q] = b;
+          g[q] = __int_as_float(readlane(__float_as_int(w), b));
+          at[q] = static_cast<int64_t>(readlane(slot, b)) * a.H;
+          n = q + 1;
+        }
+      }
+      for (int v = threadIdx.x; v < nv; v += 256) {
+        float dy[8];
+        widen(ld16(a.dy + row * a.H + v * 8), dy);
+        v4u d[NB];
+        if (a.dw) {
+#pragma unroll
+          for (int q = 0; q < NB; ++q)
+            if (q < n) d[q] = ld16(a.z + at[q] + v * 8);
+        }
+#pragma unroll
+        for (int q = 0; q < NB; ++q)
+          if (q < n) {
+            float o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = g[q] * dy[k];
+            *reinterpret_cast<v4u*>(a.out + at[q] + v * 8) = narrow(o);
+            if (a.dw) {
+              float f[8];
+              widen(d[q], f);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) dot[q] = fmaf(dy[k], f[k], dot[q]);
+            }
+          }
+      }
+      if (a.dw) {
+#pragma unroll
+        for (int q = 0; q < NB; ++q) {
+#pragma unroll
+          for (int s = 32; s > 0; s >>= 1) dot[q] += __shfl_xor(dot[q], s);
+          if (lane == 0) part[wave][q] = dot[q];
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+#pragma unroll
+          for (int q = 0; q < NB; ++q)
+            if (q < n) a.dw[row * a.K + which[q]] = ((part[0][q] + part[1][q]) + part[2][q]) + part[3][q];
+        }
+        __syncthreads();
+      }
+    }
+  }
+}
+
+hipError_t launch_reduce(const ReduceArgs& a, hipStream_t st) {
+  if (a.rows == 0) return hipSuccess;
+  const unsigned grid = static_cast<unsigned>(a.rows < 65536 ? a.rows : 65536);
+  reduce_kernel<<<grid, 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_reduce_backward(const ReduceArgs& a, hipStream_t st) {
+  if (a.rows == 0) return hipSuccess;
+  const unsigned grid = static_cast<unsigned>(a.rows < 65536 ? a.rows : 65536);
+  reduce_backward_kernel<<<grid, 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace miep

@@ -3,8 +3,10 @@
  * layout histogram, normal-mode dispatch with its handle, cached dispatch,
  * combine (with optional bias rows), the two-level relay (dispatch through
  * one buffer per group of 8 ranks and the two-level combine), low-latency
- * (expert-major, optionally FP8) dispatch and combine, and the low-latency
- * rank mask.
+ * (expert-major, optionally FP8) dispatch and combine, the low-latency
+ * rank mask, and what the experts compute between dispatch and combine:
+ * expert order, grouped matrix products (bf16 with their gradients, E4M3),
+ * the activation between them, and the weighted sum back to received rows.
  *
  * One GPU plays every rank: the R logical ranks are partitions of one
  * device's HBM, and the S source partitions are the token blocks that the
@@ -374,6 +376,123 @@ miep_status miep_ll_combine(const miep_ll_problem* q, const uint16_t* y, const i
 miep_status miep_mask_update(int32_t* mask_buffer, int32_t num_ranks, int32_t rank, int32_t value, void* stream);
 miep_status miep_mask_clean(int32_t* mask_buffer, int32_t num_ranks, void* stream);
 miep_status miep_mask_query(const int32_t* mask_buffer, int32_t num_ranks, int32_t* out, void* stream);
+
+/* ------------------------------------------------------------------ experts
+ * Between dispatch and combine.  A set of row groups names, for each expert
+ * g, the rows of one layout that are its own: rows [begin[g], begin[g] +
+ * rows[g]) -- the slots of miep_expert_order, or any ragged layout -- or,
+ * with begin NULL, rows [g*stride, g*stride + min(rows[g], stride)), the
+ * packed blocks of the low-latency dispatch (rows = packed_recv_count, stride
+ * = R*M).  Both arrays are device data, read when the kernels run; whatever
+ * they hold, only rows in [0, num_rows) are touched.  Groups may be empty and
+ * need no alignment; groups that overlap leave either one's result in the
+ * shared rows.  Rows of an output that lie in no group are left as they were,
+ * and rows of an input that lie in no group are never read into a result. */
+typedef struct miep_row_groups {
+  const int32_t* begin;  /* [num_groups] first row, or NULL (g * stride)        */
+  const int32_t* rows;   /* [num_groups] rows                                   */
+  int64_t num_rows;      /* rows of the layout, 0..2^31-1                       */
+  int32_t num_groups;    /* 0..8192                                             */
+  int32_t stride;        /* rows between group starts where begin is NULL (> 0) */
+} miep_row_groups;
+
+/* expert_order -- the received rows of a normal dispatch in expert order: a
+ * slot for every (row, k) whose recv_topk_idx names a local expert.  Slots
+ * are expert-major (global expert e = rank * E/R + local), each expert's from
+ * a multiple of expert_alignment on, and inside an expert in (row, k) order.
+ *   recv_topk_idx    [num_rows][K] int64 from miep_dispatch (entries outside [0, E/R) have no slot)
+ *   recv_rank_offset [R + 1] int32 from the handle
+ *   workspace        [parts][E] int32, parts >= 1: the parts a rank's rows may be sorted in
+ *                    (256 / R is enough to fill the GPU)
+ *   group_begin      [E] int32 out: first slot of each expert
+ *   group_rows       [E] int32 out: its slots (num_recv_tokens_per_expert with expert_alignment 1)
+ *   slot_row         [num_slots] int32 out: received row of each slot, -1 where there is none
+ *   row_slot         [num_rows][K] int32 out: slot of each entry, or -1 (and for every row behind the last)
+ *   status           one int32, nullable: 0, or MIEP_ECAPACITY when the experts need more than num_slots
+ *                    (entries past it get no slot)
+ * num_rows * K + (expert_alignment - 1) * E slots are always enough.
+ * Errors: EINVAL for bad sizes or null pointers; EUNSUPPORTED for R > 256, E > 8192, E/R > 2048,
+ * K > 64, or num_rows * K + expert_alignment * E > 2^31-1. */
+miep_status miep_expert_order(const int64_t* recv_topk_idx, const int32_t* recv_rank_offset, int64_t num_rows,
+                              int32_t num_topk, int32_t num_experts, int32_t num_ranks, int32_t expert_alignment,
+                              int32_t* workspace, int32_t parts, int32_t* group_begin, int32_t* group_rows,
+                              int32_t* slot_row, int64_t num_slots, int32_t* row_slot, int32_t* status, void* stream);
+
+/* expert_reduce -- expert outputs in slot order back to received rows:
+ * y[row] = sum over k of topk_weights[row][k] * z[row_slot[row][k]], added in
+ * ascending k in fp32 and rounded once; entries without a slot add nothing, a
+ * row without any is zero.  With topk_weights NULL every weight is 1, which
+ * also turns the slots' input gradients into the rows'.
+ *   z          [num_slots][H] bf16, 16-byte aligned; H % 8 == 0
+ *   row_slot   [num_rows][K] int32
+ *   total_rows one int32 of device memory, nullable: rows at or past it (recv_rank_offset + R) are left as they were
+ *   y          [num_rows][H] bf16 out */
+miep_status miep_expert_reduce(const uint16_t* z, int64_t num_slots, int32_t hidden, const int32_t* row_slot,
+                               int64_t num_rows, int32_t num_topk, const int32_t* total_rows,
+                               const float* topk_weights, uint16_t* y, void* stream);
+
+/* expert_reduce_backward -- its gradients: dz[row_slot[row][k]] =
+ * topk_weights[row][k] * dy[row] (bf16; slots that no entry names are left as
+ * they were) and, when d_topk_weights is given, d_topk_weights[row][k] =
+ * <dy[row], z[row_slot[row][k]]> in fp32 (0 without a slot).  z may be NULL
+ * when d_topk_weights is. */
+miep_status miep_expert_reduce_backward(const uint16_t* dy, const uint16_t* z, int64_t num_slots, int32_t hidden,
+                                        const int32_t* row_slot, int64_t num_rows, int32_t num_topk,
+                                        const int32_t* total_rows, const float* topk_weights, uint16_t* dz,
+                                        float* d_topk_weights, void* stream);
+
+/* grouped_gemm -- every group's rows times its expert's weights:
+ *   y[i][n] = sum over k of x[src(i)][k] * w[g][n][k]     for the rows i of group g
+ * in fp32, rounded once to bf16.
+ *   x         [x_rows][K] bf16.  src(i) = i (x_rows == num_rows), or row_index[i]
+ *   row_index [num_rows] int32, nullable: source row of each layout row (slot_row of
+ *             miep_expert_order); a row whose index is outside [0, x_rows) gives zeros
+ *   w         [num_groups][N][K] bf16;  y [num_rows][N] bf16 out
+ *   expected_rows  rows a group is expected to hold, 0 = num_rows / num_groups: chooses the tile,
+ *             never the result's meaning.  Give it where the layout is mostly empty (low latency).
+ * x, w, y 16-byte aligned; N % 8 == 0, K % 8 == 0, both at most 2^21.
+ * Errors: EINVAL for null pointers or sizes, EUNSUPPORTED for the limits above. */
+miep_status miep_grouped_gemm(const miep_row_groups* g, const uint16_t* x, int64_t x_rows, const uint16_t* w,
+                              int32_t n, int32_t k, const int32_t* row_index, int32_t expected_rows, uint16_t* y,
+                              void* stream);
+
+/* grouped_gemm_dgrad -- gradient of the rows: dx[i][k] = sum over n of
+ * dy[i][n] * w[g][n][k].  dy [num_rows][N] bf16, dx [num_rows][K] bf16 out (in
+ * layout rows: expert_reduce without weights adds gathered rows up). */
+miep_status miep_grouped_gemm_dgrad(const miep_row_groups* g, const uint16_t* dy, const uint16_t* w, int32_t n,
+                                    int32_t k, int32_t expected_rows, uint16_t* dx, void* stream);
+
+/* grouped_gemm_wgrad -- gradient of the weights: dw[g][n][k] = sum over the
+ * rows i of group g of dy[i][n] * x[src(i)][k], summed in fp32.
+ *   dw_f32      1: dw is fp32; 0: bf16, rounded once
+ *   accumulate  1 (fp32 only): added to what dw holds.  0: dw is overwritten, with zeros for an empty group.
+ * Rows whose row_index is outside [0, x_rows) contribute nothing. */
+miep_status miep_grouped_gemm_wgrad(const miep_row_groups* g, const uint16_t* dy, const uint16_t* x, int64_t x_rows,
+                                    const int32_t* row_index, int32_t n, int32_t k, int32_t dw_f32,
+                                    int32_t accumulate, void* dw, void* stream);
+
+/* grouped_gemm_fp8 -- miep_grouped_gemm on E4M3 codes with the scales that an
+ * FP8 dispatch or the fused cast writes:
+ *   y[i][n] = sum over blocks b of x_scales[src(i)][b] * w_scales[g][n/128][b] *
+ *             (sum over k in block b of x[src(i)][k] * w[g][n][k])
+ *   x [x_rows][K], w [num_groups][N][K] E4M3; K % 128 == 0, N % 8 == 0
+ *   x_scales [x_rows][K/128], w_scales [num_groups][ceil(N/128)][K/128]: fp32, or with
+ *   scales_ue8m0 the exponent bytes e + 127 of power-of-two scales 2^e */
+miep_status miep_grouped_gemm_fp8(const miep_row_groups* g, const uint8_t* x, const void* x_scales, int64_t x_rows,
+                                  const uint8_t* w, const void* w_scales, int32_t scales_ue8m0, int32_t n, int32_t k,
+                                  const int32_t* row_index, int32_t expected_rows, uint16_t* y, void* stream);
+
+/* swiglu -- a = silu(gate) * up over the groups' rows of h [num_rows][2*I] =
+ * [gate | up], in fp32, rounded once.  a [num_rows][I] bf16; I % 8 == 0.
+ * swiglu_fp8 casts the fp32 value per 128 channels (I % 128 == 0) by the rule
+ * of the FP8 dispatch: a E4M3, a_scales [num_rows][I/128] fp32 (powers of two
+ * with round_scale), a_scales_ue8m0 their exponent bytes (nullable, needs
+ * round_scale).  swiglu_backward: dh [num_rows][2*I] from da [num_rows][I]. */
+miep_status miep_swiglu(const miep_row_groups* g, const uint16_t* h, int32_t inner, uint16_t* a, void* stream);
+miep_status miep_swiglu_fp8(const miep_row_groups* g, const uint16_t* h, int32_t inner, int32_t round_scale,
+                            uint8_t* a, float* a_scales, uint8_t* a_scales_ue8m0, void* stream);
+miep_status miep_swiglu_backward(const miep_row_groups* g, const uint16_t* da, const uint16_t* h, int32_t inner,
+                                 uint16_t* dh, void* stream);
 
 /* Description of the last failure on this thread ("" if none). Host-only. */
 const char* miep_last_error(void);
