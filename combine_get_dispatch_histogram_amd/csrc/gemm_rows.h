@@ -10,11 +10,13 @@
 // with 16x16 MFMAs.
 #pragma once
 
+#include <type_traits>
+
 #include "gemm.h"
 
 namespace miep {
 
-template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NST>
+template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
 struct RowsTile {
   static constexpr int kWaves = WP * WQ;
   static constexpr int kTP = BP / WP / 16, kTQ = BQ / WQ / 16;       // 16 x 16 results a wavefront
@@ -26,11 +28,16 @@ struct RowsTile {
   static constexpr int kQScales = BQ < kWave ? kWave : BQ;
   static constexpr int kScaleBytes = kFp8 ? kQScales * 4 + 256 : 0;
   static_assert(!kFp8 || kQScales / kWave < kWaves, "one scale load a wavefront");
-  static constexpr int kStage = kPBytes + kQBytes + kScaleBytes;
-  static constexpr int kPLoads = kPBytes / 1024 / kWaves, kQLoads = kQBytes / 1024 / kWaves;
-  static constexpr int kLoads = kPLoads + kQLoads + (kFp8 ? 1 : 0);  // a wavefront's loads of a stage
-  static_assert(kPLoads * kWaves * 1024 == kPBytes && kQLoads * kWaves * 1024 == kQBytes, "whole loads a wavefront");
-  static_assert(kTP % 2 == 0 && kTQ >= 1 && NST >= 2 && kLoads * (NST - 1) < 64, "tile shape");
+  static constexpr int kQStage = kQBytes + kScaleBytes;
+  static constexpr int kLds = NSP * kPBytes + NSQ * kQStage;
+  static constexpr int kPLoads = kPBytes / 1024 / kWaves;            // a wavefront's loads of a step
+  static constexpr int kQLoads = kQBytes / 1024 / kWaves + (kFp8 ? 1 : 0);
+  // Loads that may be in flight behind the tile that a barrier publishes (see
+  // `publish`): the buffers that are deeper than the two of every tile.
+  static constexpr int kBehind = (NSP > NSQ ? NSQ - 1 : NSQ - 2) * kPLoads + (NSQ - 2) * kQLoads;
+  static_assert(kPLoads * kWaves * 1024 == kPBytes && kQBytes % (kWaves * 1024) == 0, "whole loads a wavefront");
+  static_assert(kTP % 2 == 0 && kTQ >= 1 && NSQ >= 2 && NSP >= NSQ && kLds <= 163840, "tile shape");
+  static_assert(kBehind + kPLoads + kQLoads < 64, "loads in flight");
   static_assert(!(PT && kFp8), "the transposed operand is bf16");
 };
 
@@ -50,11 +57,11 @@ __device__ __forceinline__ int swz_p(int row) {
 // 4-7, 12-15) by half wavefront; f spreads those 8 rows over the line.
 __device__ __forceinline__ int swz_t(int row) { return ((row & 3) | ((row >> 1) & 4)) << 1; }
 
-template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NST>
+template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
 __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsArgs a) {
-  using S = RowsTile<EL, PT, GATHER, BP, BQ, WP, WQ, NST>;
+  using S = RowsTile<EL, PT, GATHER, BP, BQ, WP, WQ, NSP, NSQ>;
   constexpr int TP = S::kTP, TQ = S::kTQ, EB = S::kEB;
-  __shared__ __align__(1024) uint8_t lds_mem[NST * S::kStage];
+  __shared__ __align__(1024) uint8_t lds_mem[S::kLds];
   const uint32_t lds = (uint32_t)(uintptr_t)(lds_byte*)lds_mem;
 
   const int lane = lane_id();
@@ -87,7 +94,13 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
     if (at.group < 0) break;
     const int mtiles = (at.rows + BQ - 1) / BQ;
     const int first = min(max(at.first, 0), mtiles * ntiles - 1);
-    const int pt = first / mtiles, qt = first - pt * mtiles;
+    // bands of kBand row tiles, in a band the row tiles of one column of tiles
+    // after the other: the 32 tiles that an XCD works on at a time share 8
+    // tiles of rows and 4 of weights
+    constexpr int kBand = 8;
+    const int band = first / (kBand * ntiles), in_band = first - band * (kBand * ntiles);
+    const int bh = min(kBand, mtiles - band * kBand);
+    const int pt = in_band / bh, qt = band * kBand + in_band - pt * bh;
     const int p0 = pt * BP, q0 = qt * BQ;
     const int live = min(BQ, at.rows - q0);                           // rows of this tile
     const int64_t row0 = at.begin + q0;
@@ -112,21 +125,25 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
         poff[i] = static_cast<uint32_t>(row * ldp + c * 16);
       }
     }
+    // Q's rows: at a fixed stride, or anywhere in the gathered source (its
+    // offsets in 16-byte units, so that 32 bits reach 64 GiB).  A row without
+    // a source reads row 0 of the weights, and stores zeros.
     const uint8_t* qbase = static_cast<const uint8_t*>(a.q) + (GATHER ? 0 : row0 * ldq);
-    uint32_t qoff[GATHER ? 1 : S::kQLoads];
-    const uint8_t* qptr[GATHER ? S::kQLoads : 1];
-    int qc[S::kQLoads];                                               // its chunk of the step
+    constexpr int QL = S::kQBytes / 1024 / S::kWaves;
+    uint32_t qoff[QL];
+    uint32_t lost = 0;                                                // bit i: load i's row has no source
 #pragma unroll
-    for (int i = 0; i < S::kQLoads; ++i) {
-      const int l = i * S::kWaves + wave;
-      int row = l * 8 + lane / 8;
-      qc[i] = (lane & 7) ^ swz_q(row);
+    for (int i = 0; i < QL; ++i) {
+      int row = (i * S::kWaves + wave) * 8 + lane / 8;
+      const int c = (lane & 7) ^ swz_q(row);
       row = min(row, live - 1);
       if constexpr (GATHER) {
         const int64_t src = a.row_index[row0 + row];
-        qptr[i] = (src >= 0 && src < a.q_rows ? qbase + src * ldq : pg) + qc[i] * 16;   // a row without a source reads weights, and stores zeros
+        const bool ok = src >= 0 && src < a.q_rows;
+        qoff[i] = static_cast<uint32_t>((ok ? src * ldq / 16 : 0) + c);
+        if (!ok) lost |= 1u << i;
       } else {
-        qoff[i] = static_cast<uint32_t>(row * ldq + qc[i] * 16);
+        qoff[i] = static_cast<uint32_t>(row * ldq + c * 16);
       }
     }
     // FP8: this wavefront's one load of a stage's scales -- 64 rows of Q's, or
@@ -135,10 +152,10 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
     const uint8_t* sptr = nullptr;
     uint32_t sto = 0;
     if constexpr (S::kFp8) {
-      constexpr int QL = S::kQScales / kWave;
+      constexpr int SL = S::kQScales / kWave;
       const int64_t pb = static_cast<int64_t>(at.group) * ((NO + 127) / 128);
       const uint8_t* ps = static_cast<const uint8_t*>(a.p_scales) + pb * kb * SB;
-      if (wave < QL) {
+      if (wave < SL) {
         int64_t src = row0 + min((wave * kWave + lane) % BQ, live - 1);
         if constexpr (GATHER) {
           src = a.row_index[src];
@@ -148,41 +165,71 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
       } else {
         sptr = ps + static_cast<int64_t>(min(p0 / 128 + lane, (NO - 1) / 128)) * kb * SB;
       }
-      sto = S::kPBytes + S::kQBytes + min(wave, QL) * 256;
+      sto = S::kQBytes + min(wave, SL) * 256;
     }
 
-    auto issue = [&](int step, int buf) {
-      const uint32_t st = lds + buf * S::kStage;
-      const bool tail = ragged_end && step == nk - 1;
+    auto p_at = [&](int buf) { return lds + buf * S::kPBytes; };
+    auto q_at = [&](int buf) { return lds + NSP * S::kPBytes + buf * S::kQStage; };
+    // Load i of this wavefront's loads of a step of 128 whole bytes.
+    auto load_p = [&](int i, int step, int buf) {
+      dma16s(pbase + static_cast<int64_t>(step) * (PT ? (kStepBytes / 2) * ldp : kStepBytes), poff[i],
+             p_at(buf) + (i * S::kWaves + wave) * 1024);
+    };
+    auto load_q = [&](int i, int step, int buf) {
+      if (i < QL) {
+        const uint32_t to = q_at(buf) + (i * S::kWaves + wave) * 1024;
+        if constexpr (GATHER) {
+          const uint8_t* base = (lost >> i) & 1 ? pg : qbase;
+          dma16(base + static_cast<int64_t>(step) * kStepBytes + (static_cast<uint64_t>(qoff[i]) << 4), to);
+        } else {
+          dma16s(qbase + static_cast<int64_t>(step) * kStepBytes, qoff[i], to);
+        }
+      } else if constexpr (S::kFp8) {
+        if constexpr (SB == 4) dma4(sptr + static_cast<int64_t>(step) * 4, q_at(buf) + sto);
+        else dma1(sptr + step, q_at(buf) + sto);
+      }
+    };
+    // All of a step's loads, if there is such a step; the last step of a
+    // contraction that is not whole reads zeros behind its end.  (Its lane
+    // constants are computed anew: kept through the loop they would cost it
+    // registers.)
+    auto issue_p = [&](int step, int buf) {
+      if (step >= nk) return;
+      if (S::kFp8 || !ragged_end || step != nk - 1) {
+#pragma unroll
+        for (int i = 0; i < S::kPLoads; ++i) load_p(i, step, buf);
+        return;
+      }
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
       const uint8_t* pb = pbase + static_cast<int64_t>(step) * (PT ? (kStepBytes / 2) * ldp : kStepBytes);
 #pragma unroll
       for (int i = 0; i < S::kPLoads; ++i) {
         const int l = i * S::kWaves + wave;
-        if (!tail) {
-          dma16s(pb, poff[i], st + l * 1024);
-        } else {
-          bool in;
-          if constexpr (PT) in = step * KE + l * (64 / (BP * 2 / 16)) + lane / (BP * 2 / 16) < C;
-          else in = step * kStepBytes + ((lane & 7) ^ swz_p<TP>(l * 8 + lane / 8)) * 16 < cbytes;
-          dma16(in ? static_cast<const void*>(pb + poff[i]) : static_cast<const void*>(g_zero16), st + l * 1024);
-        }
+        bool in;
+        if constexpr (PT) in = step * KE + l * (64 / (BP * 2 / 16)) + ln / (BP * 2 / 16) < C;
+        else in = step * kStepBytes + ((ln & 7) ^ swz_p<TP>(l * 8 + ln / 8)) * 16 < cbytes;
+        dma16(in ? static_cast<const void*>(pb + poff[i]) : static_cast<const void*>(g_zero16), p_at(buf) + l * 1024);
       }
-      const uint8_t* qb = qbase + static_cast<int64_t>(step) * kStepBytes;
+    };
+    auto issue_q = [&](int step, int buf) {
+      if (step >= nk) return;
+      if (S::kFp8 || !ragged_end || step != nk - 1) {
 #pragma unroll
-      for (int i = 0; i < S::kQLoads; ++i) {
-        const uint32_t to = st + S::kPBytes + (i * S::kWaves + wave) * 1024;
-        const bool in = step * kStepBytes + qc[i] * 16 < cbytes;
-        if constexpr (GATHER) {
-          const void* src = qptr[i] + static_cast<int64_t>(step) * kStepBytes;
-          dma16(!tail || in ? src : static_cast<const void*>(g_zero16), to);
-        } else {
-          if (!tail) dma16s(qb, qoff[i], to);
-          else dma16(in ? static_cast<const void*>(qb + qoff[i]) : static_cast<const void*>(g_zero16), to);
-        }
+        for (int i = 0; i < S::kQLoads; ++i) load_q(i, step, buf);
+        return;
       }
-      if constexpr (S::kFp8) {
-        if constexpr (SB == 4) dma4(sptr + static_cast<int64_t>(step) * 4, st + sto);
-        else dma1(sptr + step, st + sto);
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
+#pragma unroll
+      for (int q = 0; q < QL; ++q) {
+        const int l = q * S::kWaves + wave;
+        const bool in = step * kStepBytes + ((ln & 7) ^ swz_q(l * 8 + ln / 8)) * 16 < cbytes;
+        const uint8_t* src;
+        if constexpr (GATHER) src = ((lost >> q) & 1 ? pg : qbase) + (static_cast<uint64_t>(qoff[q]) << 4);
+        else src = qbase + qoff[q];
+        dma16(in ? static_cast<const void*>(src + static_cast<int64_t>(step) * kStepBytes) : static_cast<const void*>(g_zero16),
+              q_at(buf) + l * 1024);
       }
     };
 
@@ -193,7 +240,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
       for (int j = 0; j < TQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     const bool busy = wq * 16 * TQ < live;
-    // lane addresses of the operand reads, within a stage
+    // lane addresses of the operand reads, within a buffer
     uint32_t pa[PT ? TP : 2], qa[2];
     if constexpr (PT) {
 #pragma unroll
@@ -209,76 +256,145 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
     }
     {
       const int row = wq * 16 * TQ + m;
-      qa[0] = S::kPBytes + row * kStepBytes + (quarter ^ swz_q(row)) * 16;
+      qa[0] = row * kStepBytes + (quarter ^ swz_q(row)) * 16;
       qa[1] = qa[0] ^ 64;
     }
 
     wait_tiles<0>();                                                  // the previous tile's reads
+    // P's buffers may be deeper than Q's: the weights stream from memory, the
+    // rows mostly come from L2.  Step t issues the loads of P's step t - 1 +
+    // NSP, spread over its MFMAs, and behind its barrier those of Q's step t +
+    // NSQ; before the first step come those that steps before it would have
+    // issued, in that order.
 #pragma unroll
-    for (int s = 0; s < NST - 1; ++s)
-      if (s < nk) issue(s, s);
-
-    int buf = 0;
-    for (int step = 0; step < nk; ++step) {
-      if (step + NST - 2 < nk) wait_tiles<(NST - 2) * S::kLoads>();
+    for (int t = -NSP; t < 0; ++t) {
+      if (t - 1 + NSP >= 0) issue_p(t - 1 + NSP, t - 1 + NSP);
+      if (t + NSQ >= 0) issue_q(t + NSQ, t + NSQ);
+    }
+    if (nk >= NSP) wait_tiles<S::kBehind + S::kQLoads>();
+    else wait_tiles<0>();
+    // The barrier of a step: the next step's tile has come (while the loads
+    // behind it may be in flight; at the contraction's end there are fewer),
+    // and every wavefront has read this step's.
+    auto publish = [&](int step) {
+      if (step - 1 + NSP < nk) wait_tiles<S::kBehind>();
       else wait_tiles<0>();
-      const int ahead = step + NST - 1;
-      if (ahead < nk) issue(ahead, buf == 0 ? NST - 1 : buf - 1);
-      const uint32_t st = lds + buf * S::kStage;
-      buf = buf == NST - 1 ? 0 : buf + 1;
-      if (!busy) continue;
-      if constexpr (!S::kFp8) {
+    };
+    int step = 0, pbuf = 0, qbuf = 0;
+    auto before = [&](int buf) { return buf == 0 ? NSP - 1 : buf - 1; };
+    auto next_buffers = [&]() {
+      pbuf = pbuf == NSP - 1 ? 0 : pbuf + 1;
+      qbuf = qbuf == NSQ - 1 ? 0 : qbuf + 1;
+    };
+    if (!busy) {
+      for (; step + 1 < nk; ++step) {
+        issue_p(step - 1 + NSP, before(pbuf));
+        publish(step);
+        issue_q(step + NSQ, qbuf);
+        next_buffers();
+      }
+    } else if constexpr (!S::kFp8) {
+      // A step is 2 * TP slots: slot k multiplies P's operand k % TP of the
+      // half k / TP (32 channels) with the half's TQ operands of Q.  Operands
+      // come from LDS D slots ahead of their use, P's through a ring of four.
+      // The barrier lies D slots before the step's end: behind it every
+      // wavefront holds the last operands of this step's buffers, and the next
+      // step's first operands are read under the last MFMAs.
+      constexpr int SLOTS = 2 * TP, D = TP < 3 ? TP : 3, RING = 4;
+      static_assert(SLOTS % RING == 0 && D < RING && TQ <= SLOTS - D && D <= TP, "operand ring");
+      bf16x8 pf[RING], qf[2][TQ];
+      auto read_q = [&](int h, uint32_t at, int j) { qf[h][j] = lds_read<bf16x8>(at + qa[h] + j * 16 * kStepBytes); };
+      auto read_p = [&](int k, uint32_t at) {
+        const int h = k / TP, i = k % TP;
+        if constexpr (PT) {
+          struct { i16x4 lo, hi; } t;
+          t.lo = lds_read_tr(at + pa[i] + h * 32 * 2 * BP);
+          t.hi = lds_read_tr(at + pa[i] + (h * 32 + 4) * 2 * BP);
+          pf[k % RING] = __builtin_bit_cast(bf16x8, t);
+        } else {
+          pf[k % RING] = lds_read<bf16x8>(at + pa[h] + i * 4 * kStepBytes);
+        }
+      };
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          bf16x8 pf[TP], qf[TQ];
+      for (int j = 0; j < TQ; ++j) read_q(0, q_at(0), j);
 #pragma unroll
-          for (int j = 0; j < TQ; ++j) qf[j] = lds_read<bf16x8>(st + qa[h] + j * 16 * kStepBytes);
+      for (int k = 0; k < D; ++k) read_p(k, p_at(0));
+      auto body = [&](auto more, auto last) {
+        const int pb = pbuf, qb = qbuf;
+        next_buffers();
+        if constexpr (!more) issue_p(step - 1 + NSP, before(pb));
 #pragma unroll
-          for (int i = 0; i < TP; ++i) {
-            if constexpr (PT) {
-              struct { i16x4 lo, hi; } t;
-              t.lo = lds_read_tr(st + pa[i] + h * 32 * 2 * BP);
-              t.hi = lds_read_tr(st + pa[i] + (h * 32 + 4) * 2 * BP);
-              pf[i] = __builtin_bit_cast(bf16x8, t);
-            } else {
-              pf[i] = lds_read<bf16x8>(st + pa[h] + i * 4 * kStepBytes);
+        for (int k = 0; k < SLOTS; ++k) {
+          const int late = k - (SLOTS - D);                           // slots behind the barrier
+          if constexpr (!last)
+            if (late == 0) publish(step);
+          if (k + D < SLOTS) read_p(k + D, p_at(pb));
+          else if constexpr (!last) read_p(k + D - SLOTS, p_at(pbuf));
+          if (k < TP) {
+#pragma unroll
+            for (int j = k * TQ / TP; j < (k + 1) * TQ / TP; ++j) read_q(1, q_at(qb), j);
+          }
+          if (late >= 0) {
+            if constexpr (!last) {
+#pragma unroll
+              for (int j = late * TQ / D; j < (late + 1) * TQ / D; ++j) read_q(0, q_at(qbuf), j);
             }
+            if constexpr (more) {
+#pragma unroll
+              for (int l = late * S::kQLoads / D; l < (late + 1) * S::kQLoads / D; ++l) load_q(l, step + NSQ, qb);
+            }
+          } else if constexpr (more) {
+            constexpr int n = SLOTS - D;
+#pragma unroll
+            for (int l = 0; l < S::kPLoads; ++l)
+              if (l * n / S::kPLoads == k) load_p(l, step - 1 + NSP, before(pb));
           }
 #pragma unroll
-          for (int i = 0; i < TP; ++i)
-#pragma unroll
-            for (int j = 0; j < TQ; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[i], qf[j], acc[i][j], 0, 0, 0);
+          for (int j = 0; j < TQ; ++j)
+            acc[k % TP][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[k % RING], qf[k / TP][j], acc[k % TP][j], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
         }
-      } else {
+        if constexpr (!more && !last) issue_q(step + NSQ, qb);
+      };
+      constexpr std::true_type yes{};
+      constexpr std::false_type no{};
+      const int whole = nk - (ragged_end ? 1 : 0);                    // steps of 128 whole bytes
+      constexpr int ahead = NSP - 1 > NSQ ? NSP - 1 : NSQ;
+      for (; step + ahead < whole; ++step) body(yes, no);
+      for (; step + 1 < nk; ++step) body(no, no);
+      body(no, yes);
+    } else {
+      for (; step < nk; ++step) {
+        const uint32_t pat = p_at(pbuf), qat = q_at(qbuf);
+        issue_p(step - 1 + NSP, before(pbuf));
         i32x8 qf[TQ];
 #pragma unroll
         for (int j = 0; j < TQ; ++j) {
           struct { i32x4 lo, hi; } t;
-          t.lo = lds_read<i32x4>(st + qa[0] + j * 16 * kStepBytes);
-          t.hi = lds_read<i32x4>(st + qa[1] + j * 16 * kStepBytes);
+          t.lo = lds_read<i32x4>(qat + qa[0] + j * 16 * kStepBytes);
+          t.hi = lds_read<i32x4>(qat + qa[1] + j * 16 * kStepBytes);
           qf[j] = __builtin_bit_cast(i32x8, t);
         }
         // fp32 scales multiply each 128-channel block's fp32 sum; power-of-two
         // scales go into the MFMA as their exponent bytes
-        const uint32_t sat = st + S::kPBytes + S::kQBytes;
-        const uint32_t pat = sat + S::kQScales * 4 + wp * 16 * TP / 128 * 4;
+        const uint32_t sat = qat + S::kQBytes;
+        const uint32_t psat = sat + S::kQScales * 4 + wp * 16 * TP / 128 * 4;
         float s[TQ];
         int e[TQ], ep = 0;
         if constexpr (EL == kGemmFp8) {
-          const float sp = lds_read<float>(pat);
+          const float sp = lds_read<float>(psat);
 #pragma unroll
           for (int j = 0; j < TQ; ++j) s[j] = sp * lds_read<float>(sat + ((wq * TQ + j) * 16 + m) * 4);
         } else {
-          ep = lds_read<int>(pat);
+          ep = lds_read<int>(psat);
 #pragma unroll
           for (int j = 0; j < TQ; ++j) e[j] = lds_read<int>(sat + ((wq * TQ + j) * 16 + m) * 4);
         }
 #pragma unroll
         for (int i = 0; i < TP; ++i) {
           struct { i32x4 lo, hi; } t;
-          t.lo = lds_read<i32x4>(st + pa[0] + i * 4 * kStepBytes);
-          t.hi = lds_read<i32x4>(st + pa[1] + i * 4 * kStepBytes);
+          t.lo = lds_read<i32x4>(pat + pa[0] + i * 4 * kStepBytes);
+          t.hi = lds_read<i32x4>(pat + pa[1] + i * 4 * kStepBytes);
           const i32x8 pf = __builtin_bit_cast(i32x8, t);
 #pragma unroll
           for (int j = 0; j < TQ; ++j) {
@@ -292,6 +408,11 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
             }
           }
         }
+        if (step + 1 < nk) {
+          publish(step);
+          issue_q(step + NSQ, qbuf);
+        }
+        next_buffers();
       }
     }
 
@@ -327,7 +448,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
   }
 }
 
-template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NST>
+template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
 hipError_t launch_rows_tile(GemmRowsArgs a, hipStream_t st) {
   const int64_t per = (a.NO + BP - 1) / BP;
   const int64_t most = ((a.g.limit + BQ - 1) / BQ + a.g.G) * per;     // disjoint groups have no more tiles
@@ -335,21 +456,22 @@ hipError_t launch_rows_tile(GemmRowsArgs a, hipStream_t st) {
   a.max_tiles = static_cast<int>(most);
   int per_cu = 0;
   // resident workgroups: by LDS (160 KiB a CU) and two wavefronts a SIMD
-  per_cu = 163840 / (NST * RowsTile<EL, PT, GATHER, BP, BQ, WP, WQ, NST>::kStage);
+  per_cu = 163840 / RowsTile<EL, PT, GATHER, BP, BQ, WP, WQ, NSP, NSQ>::kLds;
   const int by_waves = 8 / (WP * WQ);
   per_cu = per_cu < by_waves ? per_cu : by_waves;
   int64_t grid = 256ll * (per_cu > 0 ? per_cu : 1);
   if (grid > (most + 7) / 8 * 8) grid = (most + 7) / 8 * 8;
-  gemm_rows_kernel<EL, PT, GATHER, BP, BQ, WP, WQ, NST><<<static_cast<unsigned>(grid), WP * WQ * kWave, 0, st>>>(a);
+  gemm_rows_kernel<EL, PT, GATHER, BP, BQ, WP, WQ, NSP, NSQ><<<static_cast<unsigned>(grid), WP * WQ * kWave, 0, st>>>(a);
   return hipGetLastError();
 }
 
 template <int EL, bool PT, bool GATHER>
 hipError_t launch_rows(const GemmRowsArgs& a, hipStream_t st) {
-  if (a.expected <= 32) return launch_rows_tile<EL, PT, GATHER, 128, 32, 4, 1, EL == kGemmBf16 ? 4 : 3>(a, st);
-  if (a.expected <= 64) return launch_rows_tile<EL, PT, GATHER, 128, 64, 2, 2, 3>(a, st);
-  if (a.expected <= 128) return launch_rows_tile<EL, PT, GATHER, 256, 128, 4, 2, 3>(a, st);
-  return launch_rows_tile<EL, PT, GATHER, 256, 256, 2, 4, 2>(a, st);
+  constexpr bool F8 = EL != kGemmBf16;
+  if (a.expected <= 32) return launch_rows_tile<EL, PT, GATHER, 128, 32, 4, 1, F8 ? 3 : 4, F8 ? 3 : 4>(a, st);
+  if (a.expected <= 64) return launch_rows_tile<EL, PT, GATHER, 128, 64, 2, 2, 3, 3>(a, st);
+  if (a.expected <= 128) return launch_rows_tile<EL, PT, GATHER, 256, 128, 4, 2, F8 ? 3 : 4, F8 ? 3 : 2>(a, st);
+  return launch_rows_tile<EL, PT, GATHER, 256, 256, 2, 4, F8 ? 2 : 3, 2>(a, st);
 }
 
 }  // namespace miep
