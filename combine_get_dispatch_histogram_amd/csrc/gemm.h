@@ -6,8 +6,8 @@
 // the rows of the 16 x 16 result (four consecutive ones to a lane), Q its
 // columns (one to a lane).  The result of a rows kernel is out[q][p]: with the
 // weights as P and the tokens as Q a lane holds consecutive output channels of
-// one token, so results go to memory as wide row-contiguous vectors without a
-// transposition, and a token's scale is one value a lane.
+// one token, so results go to memory as row-contiguous vectors without a trip
+// through LDS, and a token's scale is one value a lane.
 #pragma once
 
 #include "device.h"
@@ -67,6 +67,22 @@ __device__ __forceinline__ T lds_read(uint32_t at) {
 __device__ __forceinline__ i16x4 lds_read_tr(uint32_t at) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) i16x4*>(at));
 }
+
+// Two 16 x 16 results of neighbouring P tiles (four consecutive p to a lane,
+// four lanes 16 apart to a tile's 16) as 8 consecutive p to a lane: lanes of
+// the even quarters take the first tile's p from 4 * quarter on, those of the
+// odd ones the second's from 4 * (quarter - 1) on, so that a store of 16 bytes
+// a lane writes 64 whole bytes of each of 16 rows.
+__device__ __forceinline__ v4u pack_pair(const f32x4& a, const f32x4& b) {
+  const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16x2(a[0], a[1]), pack_bf16x2(b[0], b[1]), false, false);
+  const auto y = __builtin_amdgcn_permlane16_swap(pack_bf16x2(a[2], a[3]), pack_bf16x2(b[2], b[3]), false, false);
+  return v4u{static_cast<uint32_t>(x[0]), static_cast<uint32_t>(y[0]), static_cast<uint32_t>(x[1]), static_cast<uint32_t>(y[1])};
+}
+
+// Keeps the arithmetic that makes v where it is written: left alone, the
+// compiler moves the multiplications by FP8 scales behind a step's branches
+// and holds every MFMA's result until then.
+__device__ __forceinline__ void pin(f32x4& v) { asm volatile("" : "+v"(v)); }
 
 // ---- the groups' rows, never trusted: a group reads as the part of
 // [begin, begin + rows) inside [0, limit).

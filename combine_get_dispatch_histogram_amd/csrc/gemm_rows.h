@@ -5,7 +5,7 @@
 //   out[i][p] = sum_c Q[src(i)][c] * P_g[p][c]        for the rows i of group g
 //
 // A workgroup computes BQ rows x BP output channels.  Each 128-byte step of
-// the contraction comes to LDS by asynchronous 16-byte loads, NST buffers deep,
+// the contraction comes to LDS by asynchronous 16-byte loads, several buffers deep,
 // with one barrier a step; wavefront (wp, wq) multiplies its BP/WP x BQ/WQ part
 // with 16x16 MFMAs.
 #pragma once
@@ -41,17 +41,11 @@ struct RowsTile {
   static_assert(!(PT && kFp8), "the transposed operand is bf16");
 };
 
-// Swizzles: the 16-byte chunk c of a tile row is kept at chunk c ^ s(row), so
-// that the 16 rows of one operand read lie in 16 different 16-byte banks
-// groups of the 256-byte LDS line (rows are 128 bytes: their parity is one
-// bit of the place, s the other three).  Q reads 16 consecutive rows; P reads
-// rows 4*TP*(m/4) + 4*i + m%4 (m = lane % 16), which gives a lane the 4*TP
-// consecutive output channels of its results.
-__device__ __forceinline__ int swz_q(int row) { return (row >> 1) & 7; }
-template <int TP>
-__device__ __forceinline__ int swz_p(int row) {
-  return ((row >> 1) & 1) | (((row / (4 * TP)) & 3) << 1);
-}
+// Swizzle: the 16-byte chunk c of a tile row is kept at chunk c ^ s(row), so
+// that the 16 consecutive rows of one operand read lie in 16 different 16-byte
+// places of the 256-byte LDS line (rows are 128 bytes: their parity is one bit
+// of the place, s the other three).
+__device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 // A transposed tile has 64 contraction rows of BP channels.  A transposing
 // read takes 32 bytes of each of 4 rows a 16-lane group: rows 0-3, 8-11 (then
 // 4-7, 12-15) by half wavefront; f spreads those 8 rows over the line.
@@ -120,7 +114,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
         poff[i] = static_cast<uint32_t>(row * ldp + col);
       } else {
         int row = l * 8 + lane / 8;
-        const int c = (lane & 7) ^ swz_p<TP>(row);
+        const int c = (lane & 7) ^ swz(row);
         if (p0 + row >= NO) row = NO - 1 - p0;
         poff[i] = static_cast<uint32_t>(row * ldp + c * 16);
       }
@@ -135,7 +129,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
 #pragma unroll
     for (int i = 0; i < QL; ++i) {
       int row = (i * S::kWaves + wave) * 8 + lane / 8;
-      const int c = (lane & 7) ^ swz_q(row);
+      const int c = (lane & 7) ^ swz(row);
       row = min(row, live - 1);
       if constexpr (GATHER) {
         const int64_t src = a.row_index[row0 + row];
@@ -208,7 +202,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
         const int l = i * S::kWaves + wave;
         bool in;
         if constexpr (PT) in = step * KE + l * (64 / (BP * 2 / 16)) + ln / (BP * 2 / 16) < C;
-        else in = step * kStepBytes + ((ln & 7) ^ swz_p<TP>(l * 8 + ln / 8)) * 16 < cbytes;
+        else in = step * kStepBytes + ((ln & 7) ^ swz(l * 8 + ln / 8)) * 16 < cbytes;
         dma16(in ? static_cast<const void*>(pb + poff[i]) : static_cast<const void*>(g_zero16), p_at(buf) + l * 1024);
       }
     };
@@ -224,7 +218,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
 #pragma unroll
       for (int q = 0; q < QL; ++q) {
         const int l = q * S::kWaves + wave;
-        const bool in = step * kStepBytes + ((ln & 7) ^ swz_q(l * 8 + ln / 8)) * 16 < cbytes;
+        const bool in = step * kStepBytes + ((ln & 7) ^ swz(l * 8 + ln / 8)) * 16 < cbytes;
         const uint8_t* src;
         if constexpr (GATHER) src = ((lost >> q) & 1 ? pg : qbase) + (static_cast<uint64_t>(qoff[q]) << 4);
         else src = qbase + qoff[q];
@@ -250,13 +244,13 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
         pa[i] = row * (2 * BP) + (ch ^ swz_t(row)) * 16 + (m & 1) * 8;
       }
     } else {
-      const int row = wp * 16 * TP + (m / 4) * 4 * TP + (m & 3);
-      pa[0] = row * kStepBytes + (quarter ^ swz_p<TP>(row)) * 16;
+      const int row = wp * 16 * TP + m;
+      pa[0] = row * kStepBytes + (quarter ^ swz(row)) * 16;
       pa[1] = pa[0] ^ 64;
     }
     {
       const int row = wq * 16 * TQ + m;
-      qa[0] = row * kStepBytes + (quarter ^ swz_q(row)) * 16;
+      qa[0] = row * kStepBytes + (quarter ^ swz(row)) * 16;
       qa[1] = qa[0] ^ 64;
     }
 
@@ -312,7 +306,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
           t.hi = lds_read_tr(at + pa[i] + (h * 32 + 4) * 2 * BP);
           pf[k % RING] = __builtin_bit_cast(bf16x8, t);
         } else {
-          pf[k % RING] = lds_read<bf16x8>(at + pa[h] + i * 4 * kStepBytes);
+          pf[k % RING] = lds_read<bf16x8>(at + pa[h] + i * 16 * kStepBytes);
         }
       };
 #pragma unroll
@@ -364,56 +358,101 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
       for (; step + 1 < nk; ++step) body(no, no);
       body(no, yes);
     } else {
-      for (; step < nk; ++step) {
-        const uint32_t pat = p_at(pbuf), qat = q_at(qbuf);
-        issue_p(step - 1 + NSP, before(pbuf));
-        i32x8 qf[TQ];
-#pragma unroll
-        for (int j = 0; j < TQ; ++j) {
-          struct { i32x4 lo, hi; } t;
-          t.lo = lds_read<i32x4>(qat + qa[0] + j * 16 * kStepBytes);
-          t.hi = lds_read<i32x4>(qat + qa[1] + j * 16 * kStepBytes);
-          qf[j] = __builtin_bit_cast(i32x8, t);
-        }
-        // fp32 scales multiply each 128-channel block's fp32 sum; power-of-two
-        // scales go into the MFMA as their exponent bytes
-        const uint32_t sat = qat + S::kQBytes;
-        const uint32_t psat = sat + S::kQScales * 4 + wp * 16 * TP / 128 * 4;
-        float s[TQ];
-        int e[TQ], ep = 0;
+      // A step is TP slots: slot i multiplies P's operand i (128 channels, 32
+      // bytes a lane) with all of Q's.  P's operands come a slot ahead through
+      // a ring of two; Q's are held over the step and each replaced by the
+      // next step's behind its last use, so the barrier lies before the last
+      // slot.  fp32 scales multiply each block's fp32 sum into the result (the
+      // MFMAs start from zero); power-of-two scales go into the MFMAs as their
+      // exponent bytes.
+      i32x8 pf[2], qf[TQ];
+      float s[TQ];
+      int e[TQ], ep = 0;
+      auto operand = [&](uint32_t at0, uint32_t at1) {
+        struct { i32x4 lo, hi; } t;
+        t.lo = lds_read<i32x4>(at0);
+        t.hi = lds_read<i32x4>(at1);
+        return __builtin_bit_cast(i32x8, t);
+      };
+      auto read_p = [&](int i, uint32_t at) {
+        pf[i & 1] = operand(at + pa[0] + i * 16 * kStepBytes, at + pa[1] + i * 16 * kStepBytes);
+      };
+      auto read_q = [&](int j, uint32_t at) {
+        qf[j] = operand(at + qa[0] + j * 16 * kStepBytes, at + qa[1] + j * 16 * kStepBytes);
+      };
+      const uint32_t psat = S::kQBytes + S::kQScales * 4 + wp * 16 * TP / 128 * 4;
+      auto read_scales = [&](uint32_t at) {
         if constexpr (EL == kGemmFp8) {
-          const float sp = lds_read<float>(psat);
+          const float sp = lds_read<float>(at + psat);
 #pragma unroll
-          for (int j = 0; j < TQ; ++j) s[j] = sp * lds_read<float>(sat + ((wq * TQ + j) * 16 + m) * 4);
+          for (int j = 0; j < TQ; ++j) s[j] = sp * lds_read<float>(at + S::kQBytes + ((wq * TQ + j) * 16 + m) * 4);
         } else {
-          ep = lds_read<int>(psat);
+          ep = lds_read<int>(at + psat);
 #pragma unroll
-          for (int j = 0; j < TQ; ++j) e[j] = lds_read<int>(sat + ((wq * TQ + j) * 16 + m) * 4);
+          for (int j = 0; j < TQ; ++j) e[j] = lds_read<int>(at + S::kQBytes + ((wq * TQ + j) * 16 + m) * 4);
         }
+      };
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) read_q(j, q_at(0));
+      read_p(0, p_at(0));
+      read_scales(q_at(0));
+      auto body = [&](auto more, auto last) {
+        const int pb = pbuf, qb = qbuf;
+        next_buffers();
+        if constexpr (!more) issue_p(step - 1 + NSP, before(pb));
 #pragma unroll
         for (int i = 0; i < TP; ++i) {
-          struct { i32x4 lo, hi; } t;
-          t.lo = lds_read<i32x4>(pat + pa[0] + i * 4 * kStepBytes);
-          t.hi = lds_read<i32x4>(pat + pa[1] + i * 4 * kStepBytes);
-          const i32x8 pf = __builtin_bit_cast(i32x8, t);
+          const bool end = i == TP - 1;
+          if constexpr (!last)
+            if (end) publish(step);
+          if (!end) read_p(i + 1, p_at(pb));
+          else if constexpr (!last) read_p(0, p_at(pbuf));
+          if constexpr (more) {
+            if (end) {
+#pragma unroll
+              for (int l = 0; l < S::kQLoads; ++l) load_q(l, step + NSQ, qb);
+            } else {
+#pragma unroll
+              for (int l = 0; l < S::kPLoads; ++l)
+                if (l * (TP - 1) / S::kPLoads == i) load_p(l, step - 1 + NSP, before(pb));
+            }
+          }
+          f32x4 d[TQ];
 #pragma unroll
           for (int j = 0; j < TQ; ++j) {
             if constexpr (EL == kGemmFp8) {
               const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-              const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf, qf[j], z, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[r], s[j], acc[i][j][r]);
+              d[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf[i & 1], qf[j], z, 0, 0, 0, 0, 0, 0);
             } else {
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf, qf[j], acc[i][j], 0, 0, 0, ep, 0, e[j]);
+              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf[i & 1], qf[j], acc[i][j], 0, 0, 0, ep, 0, e[j]);
+            }
+            if constexpr (!last) {
+              if (end) {
+                __builtin_amdgcn_sched_barrier(0);
+                read_q(j, q_at(qbuf));
+              }
             }
           }
+          if constexpr (EL == kGemmFp8) {
+#pragma unroll
+            for (int j = 0; j < TQ; ++j)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[j][r], s[j], acc[i][j][r]);
+          }
+#pragma unroll
+          for (int j = 0; j < TQ; ++j) pin(acc[i][j]);
+          if constexpr (!last)
+            if (end) read_scales(q_at(qbuf));
+          __builtin_amdgcn_sched_barrier(0);
         }
-        if (step + 1 < nk) {
-          publish(step);
-          issue_q(step + NSQ, qbuf);
-        }
-        next_buffers();
-      }
+        if constexpr (!more && !last) issue_q(step + NSQ, qb);
+      };
+      constexpr std::true_type yes{};
+      constexpr std::false_type no{};
+      constexpr int ahead = NSP - 1 > NSQ ? NSP - 1 : NSQ;
+      for (; step + ahead < nk; ++step) body(yes, no);
+      for (; step + 1 < nk; ++step) body(no, no);
+      body(no, yes);
     }
 
     if (!busy) continue;
@@ -427,22 +466,12 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
         none = src < 0 || src >= a.q_rows;
       }
       uint16_t* o = a.out + (row0 + row) * NO;
-      if constexpr (PT) {
 #pragma unroll
-        for (int i = 0; i < TP; ++i) {
-          const int p = p0 + (wp * TP + i) * 16 + quarter * 4;
-          v2u v{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
-          if (p < NO) *reinterpret_cast<v2u*>(o + p) = v;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < TP; i += 2) {
-          const int p = p0 + wp * 16 * TP + quarter * 4 * TP + i * 4;
-          v4u v{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]),
-                pack_bf16x2(acc[i + 1][j][0], acc[i + 1][j][1]), pack_bf16x2(acc[i + 1][j][2], acc[i + 1][j][3])};
-          if (none) v = v4u{0u, 0u, 0u, 0u};
-          if (p < NO) *reinterpret_cast<v4u*>(o + p) = v;
-        }
+      for (int i = 0; i < TP; i += 2) {
+        const int p = p0 + (wp * TP + i + (quarter & 1)) * 16 + (quarter >> 1) * 8;
+        v4u v = pack_pair(acc[i][j], acc[i + 1][j]);
+        if (none) v = v4u{0u, 0u, 0u, 0u};
+        if (p < NO) *reinterpret_cast<v4u*>(o + p) = v;
       }
     }
   }

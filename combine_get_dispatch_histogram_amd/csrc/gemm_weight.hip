@@ -174,9 +174,9 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
     const int64_t o = (static_cast<int64_t>(group) * a.N + n) * a.K;
 #pragma unroll
     for (int i = 0; i < TP; ++i) {
-      const int k = p0 + (wp * TP + i) * 16 + quarter * 4;
-      if (k >= a.K) continue;
       if constexpr (F32) {
+        const int k = p0 + (wp * TP + i) * 16 + quarter * 4;
+        if (k >= a.K) continue;
         f32x4* at = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o + k);
         f32x4 v = acc[i][j];
         if (a.accumulate) {
@@ -184,9 +184,10 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
           v = f32x4{old[0] + v[0], old[1] + v[1], old[2] + v[2], old[3] + v[3]};
         }
         *at = v;
-      } else {
-        const v2u v{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
-        *reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.out) + o + k) = v;
+      } else if ((i & 1) == 0) {
+        const int kk = p0 + (wp * TP + i + (quarter & 1)) * 16 + (quarter >> 1) * 8;
+        const v4u v = pack_pair(acc[i][j], acc[i + 1][j]);
+        if (kk < a.K) *reinterpret_cast<v4u*>(static_cast<uint16_t*>(a.out) + o + kk) = v;
       }
     }
   }
