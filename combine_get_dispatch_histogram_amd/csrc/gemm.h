@@ -51,6 +51,11 @@ __device__ __forceinline__ void dma1(const void* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" ::"s"(lds), "v"(src) : "memory");
 }
 
+// A transposed tile has 64 contraction rows of BP channels.  A transposing
+// read takes 32 bytes of each of 4 rows a 16-lane group: rows 0-3, 8-11 (then
+// 4-7, 12-15) by half wavefront; f spreads those 8 rows over the line.
+__device__ __forceinline__ int swz_t(int row) { return ((row & 3) | ((row >> 1) & 4)) << 1; }
+
 // Waits until at most N vector memory operations of this wavefront are in
 // flight and its LDS reads have returned, then for the workgroup: tiles whose
 // loads every wavefront has waited for may be read, and tiles that every

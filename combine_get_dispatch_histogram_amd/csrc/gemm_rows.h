@@ -46,11 +46,6 @@ struct RowsTile {
 // places of the 256-byte LDS line (rows are 128 bytes: their parity is one bit
 // of the place, s the other three).
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
-// A transposed tile has 64 contraction rows of BP channels.  A transposing
-// read takes 32 bytes of each of 4 rows a 16-lane group: rows 0-3, 8-11 (then
-// 4-7, 12-15) by half wavefront; f spreads those 8 rows over the line.
-__device__ __forceinline__ int swz_t(int row) { return ((row & 3) | ((row >> 1) & 4)) << 1; }
-
 template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
 __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsArgs a) {
   using S = RowsTile<EL, PT, GATHER, BP, BQ, WP, WQ, NSP, NSQ>;

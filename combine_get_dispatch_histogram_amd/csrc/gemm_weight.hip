@@ -5,29 +5,37 @@
 // The contraction runs over rows, so both operands are read through LDS's
 // transposing loads: tiles of 64 rows come in as they lie in memory (rows of
 // 512 or 256 bytes) and a lane reads 4 rows of one channel at a time.  X gives
-// the MFMA's rows, so that a lane holds 4 consecutive k of one n.
+// the MFMA's rows (P), so that a lane holds 4 consecutive k of one n.
+//
+// With few rows a group the fp32 result is most of the traffic (4 N K bytes a
+// group), so it leaves in whole 128-byte lines (see the stores).
+#include <type_traits>
+
 #include "gemm.h"
 
 namespace miep {
 
-template <int BP, int BQ, int WP, int WQ, int NST>
+template <bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
 struct WeightTile {
-  static constexpr int kRows = 64;                                   // contraction rows of a stage
+  static constexpr int kRows = 64;                                   // contraction rows of a step
   static constexpr int kWaves = WP * WQ;
   static constexpr int kTP = BP / WP / 16, kTQ = BQ / WQ / 16;
   static constexpr int kPBytes = BP * 2 * kRows, kQBytes = BQ * 2 * kRows;
-  static constexpr int kStage = kPBytes + kQBytes;
-  static constexpr int kPLoads = kPBytes / 1024 / kWaves, kQLoads = kQBytes / 1024 / kWaves;
-  static constexpr int kLoads = kPLoads + kQLoads;
+  static constexpr int kIndexBytes = GATHER ? 4 * kRows : 0;         // source rows that come with a step of Q
+  static constexpr int kLds = NSP * kPBytes + NSQ * (kQBytes + kIndexBytes);
+  static constexpr int kPLoads = kPBytes / 1024 / kWaves, kQLoads = kQBytes / 1024 / kWaves + (GATHER ? 1 : 0);
   static constexpr int kPChunks = BP / 8, kQChunks = BQ / 8;         // 16-byte chunks of a tile row
-  static_assert(kPChunks >= 16 && kQChunks >= 16 && kLoads * (NST - 1) < 64, "tile shape");
+  // loads in flight behind the tile that a barrier publishes, as in the rows kernel
+  static constexpr int kBehind = (NSP > NSQ ? NSQ - 1 : NSQ - 2) * kPLoads + (NSQ - 2) * kQLoads;
+  static_assert(kPChunks >= 16 && kQChunks >= 16 && NSQ >= 2 && NSP >= NSQ && kLds <= 163840, "tile shape");
+  static_assert(!GATHER || (NSP == 2 && NSQ == 2), "indices come two steps ahead");
 };
 
-template <bool GATHER, bool F32, int BP, int BQ, int WP, int WQ, int NST>
+template <bool GATHER, bool F32, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
 __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWeightArgs a) {
-  using S = WeightTile<BP, BQ, WP, WQ, NST>;
+  using S = WeightTile<GATHER, BP, BQ, WP, WQ, NSP, NSQ>;
   constexpr int TP = S::kTP, TQ = S::kTQ;
-  __shared__ __align__(1024) uint8_t lds_mem[NST * S::kStage];
+  __shared__ __align__(1024) uint8_t lds_mem[S::kLds];
   const uint32_t lds = (uint32_t)(uintptr_t)(lds_byte*)lds_mem;
 
   const int lane = lane_id();
@@ -35,15 +43,22 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
   const int wp = wave % WP, wq = wave / WP;
   const int m = lane & 15, quarter = lane >> 4;
 
-  // XCD x takes the x-th eighth of the tiles: neighbours share dY or X columns in its L2
+  // Groups differ in rows, so every XCD (workgroups go to the 8 in turn) takes
+  // an eighth of each group's tiles, in order, so that they share dY's and
+  // X's columns in its L2; groups of few tiles are dealt out one by one.
   const int ptiles = (a.K + BP - 1) / BP, qtiles = (a.N + BQ - 1) / BQ;
-  const int64_t total = static_cast<int64_t>(ptiles) * qtiles * a.g.G;
-  const int64_t chunk = (total + 7) / 8;
-  const int64_t t = (blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
-  if ((blockIdx.x >> 3) >= chunk || t >= total) return;
-  const int group = static_cast<int>(t / (ptiles * qtiles));
-  const int in_group = static_cast<int>(t - static_cast<int64_t>(group) * (ptiles * qtiles));
-  const int q0 = in_group / ptiles * BQ, p0 = in_group % ptiles * BP;
+  const int per_group = ptiles * qtiles;
+  int group, tile;
+  if (per_group >= 64) {
+    const int part = (per_group + 7) / 8, at = blockIdx.x >> 3;
+    group = at / part;
+    tile = (blockIdx.x & 7) * part + at % part;
+  } else {
+    group = blockIdx.x / per_group;
+    tile = blockIdx.x - group * per_group;
+  }
+  if (group >= a.g.G || tile >= per_group) return;
+  const int q0 = tile / ptiles * BQ, p0 = tile % ptiles * BP;
 
   int64_t begin;
   int rows;
@@ -53,58 +68,81 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
   rows = __builtin_amdgcn_readfirstlane(rows);
   if (rows == 0 && a.accumulate) return;
   const int nk = (rows + S::kRows - 1) / S::kRows;
+  const bool ragged_end = rows % S::kRows != 0;
 
   const int64_t ldq = 2 * static_cast<int64_t>(a.N), ldp = 2 * static_cast<int64_t>(a.K);
   const uint8_t* qbase = reinterpret_cast<const uint8_t*>(a.q) + begin * ldq + 2 * static_cast<int64_t>(q0);
   const uint8_t* pbase = reinterpret_cast<const uint8_t*>(a.p) + (GATHER ? 0 : begin * ldp) + 2 * static_cast<int64_t>(p0);
-  int prow[S::kPLoads], pcol[S::kPLoads], qrow[S::kQLoads], qcol[S::kQLoads];
+  // Of load i of a step: the lane's row of the tile (rows of load i + 1 lie
+  // 64 / chunks * waves further) and its 16 bytes of that row.
+  constexpr int QL = S::kQBytes / 1024 / S::kWaves;
+  constexpr int PR = 64 / S::kPChunks * S::kWaves, QR = 64 / S::kQChunks * S::kWaves;
+  const int prow = wave * (64 / S::kPChunks) + lane / S::kPChunks, qrow = wave * (64 / S::kQChunks) + lane / S::kQChunks;
+  uint32_t poff[S::kPLoads], qoff[QL];
 #pragma unroll
   for (int i = 0; i < S::kPLoads; ++i) {
-    prow[i] = (i * S::kWaves + wave) * (64 / S::kPChunks) + lane / S::kPChunks;
-    pcol[i] = ((lane % S::kPChunks) ^ ((prow[i] & 3) | ((prow[i] >> 1) & 4)) << 1) * 16;
-    if (p0 + pcol[i] / 2 >= a.K) pcol[i] = 0;
+    const int row = prow + i * PR;
+    int col = ((lane % S::kPChunks) ^ swz_t(row)) * 16;
+    if (p0 + col / 2 >= a.K) col = 0;
+    poff[i] = static_cast<uint32_t>((GATHER ? 0 : row * ldp) + col);
   }
 #pragma unroll
-  for (int i = 0; i < S::kQLoads; ++i) {
-    qrow[i] = (i * S::kWaves + wave) * (64 / S::kQChunks) + lane / S::kQChunks;
-    qcol[i] = ((lane % S::kQChunks) ^ ((qrow[i] & 3) | ((qrow[i] >> 1) & 4)) << 1) * 16;
-    if (q0 + qcol[i] / 2 >= a.N) qcol[i] = 0;
+  for (int i = 0; i < QL; ++i) {
+    const int row = qrow + i * QR;
+    int col = ((lane % S::kQChunks) ^ swz_t(row)) * 16;
+    if (q0 + col / 2 >= a.N) col = 0;
+    qoff[i] = static_cast<uint32_t>(row * ldq + col);
   }
-  // gathered rows' sources, read one stage ahead of the loads that use them
-  int src[GATHER ? S::kPLoads : 1];
-  auto sources = [&](int step) {
+  auto p_at = [&](int buf) { return lds + buf * S::kPBytes; };
+  auto q_at = [&](int buf) { return lds + NSP * S::kPBytes + buf * (S::kQBytes + S::kIndexBytes); };
+  // A gathered row's address; a row behind the group's last, or without a
+  // source, reads zeros.
+  auto gathered = [&](int i, int step, int src) {
+    const bool in = step * S::kRows + prow + i * PR < rows && src >= 0 && src < a.p_rows;
+    return in ? static_cast<const void*>(pbase + src * ldp + poff[i]) : static_cast<const void*>(g_zero16);
+  };
+  // Load i of a step of 64 whole rows (gathered: of any).  The indices of a
+  // gathered step come with the Q loads two steps before its own loads, those
+  // of step u + 1 in the place behind Q's step u.
+  auto load_p = [&](int i, int step, int buf) {
+    const uint32_t to = p_at(buf) + (i * S::kWaves + wave) * 1024;
     if constexpr (GATHER) {
+      const int src = lds_read<int>(q_at((step - 1) & 1) + S::kQBytes + (prow + i * PR) * 4);
+      dma16(gathered(i, step, src), to);
+    } else {
+      dma16s(pbase + static_cast<int64_t>(step) * S::kRows * ldp, poff[i], to);
+    }
+  };
+  auto load_q = [&](int i, int step, int buf) {
+    if (i < QL) dma16s(qbase + static_cast<int64_t>(step) * S::kRows * ldq, qoff[i], q_at(buf) + (i * S::kWaves + wave) * 1024);
+    else if constexpr (GATHER)
+      dma4(a.row_index + begin + min((step + 1) * S::kRows + lane, rows - 1), q_at(buf) + S::kQBytes);
+  };
+  // A step's loads, if there is such a step; the last one may have fewer rows.
+  auto issue_p = [&](int step, int buf) {
+    if (step >= nk) return;
 #pragma unroll
-      for (int i = 0; i < S::kPLoads; ++i) {
-        const int r = step * S::kRows + prow[i];
-        src[i] = r < rows ? a.row_index[begin + r] : -1;
+    for (int i = 0; i < S::kPLoads; ++i) {
+      if (GATHER || !ragged_end || step != nk - 1) {
+        load_p(i, step, buf);
+      } else {
+        const uint8_t* src = pbase + static_cast<int64_t>(step) * S::kRows * ldp + poff[i];
+        dma16(step * S::kRows + prow + i * PR < rows ? static_cast<const void*>(src) : static_cast<const void*>(g_zero16),
+              p_at(buf) + (i * S::kWaves + wave) * 1024);
       }
     }
   };
-  auto issue = [&](int step, int buf) {
-    const uint32_t st = lds + buf * S::kStage;
-    const int r0 = step * S::kRows;
-    const bool tail = rows - r0 < S::kRows;
-#pragma unroll
-    for (int i = 0; i < S::kPLoads; ++i) {
-      const uint32_t to = st + (i * S::kWaves + wave) * 1024;
-      if constexpr (GATHER) {
-        const bool in = src[i] >= 0 && src[i] < a.p_rows;
-        dma16(in ? static_cast<const void*>(pbase + src[i] * ldp + pcol[i]) : static_cast<const void*>(g_zero16), to);
-      } else {
-        const uint32_t off = static_cast<uint32_t>(prow[i] * ldp + pcol[i]);
-        const uint8_t* pb = pbase + r0 * ldp;
-        if (!tail) dma16s(pb, off, to);
-        else dma16(r0 + prow[i] < rows ? static_cast<const void*>(pb + off) : static_cast<const void*>(g_zero16), to);
-      }
-    }
+  auto issue_q = [&](int step, int buf) {
+    if (step >= nk) return;
 #pragma unroll
     for (int i = 0; i < S::kQLoads; ++i) {
-      const uint32_t to = st + S::kPBytes + (i * S::kWaves + wave) * 1024;
-      const uint32_t off = static_cast<uint32_t>(qrow[i] * ldq + qcol[i]);
-      const uint8_t* qb = qbase + r0 * ldq;
-      if (!tail) dma16s(qb, off, to);
-      else dma16(r0 + qrow[i] < rows ? static_cast<const void*>(qb + off) : static_cast<const void*>(g_zero16), to);
+      if (i >= QL || !ragged_end || step != nk - 1) {
+        load_q(i, step, buf);
+      } else {
+        const uint8_t* src = qbase + static_cast<int64_t>(step) * S::kRows * ldq + qoff[i];
+        dma16(step * S::kRows + qrow + i * QR < rows ? static_cast<const void*>(src) : static_cast<const void*>(g_zero16),
+              q_at(buf) + (i * S::kWaves + wave) * 1024);
+      }
     }
   };
 
@@ -114,103 +152,169 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
 #pragma unroll
     for (int j = 0; j < TQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  uint32_t pa[TP], qa[TQ];
-  {
-    const int row = quarter * 8 + m / 4;
-    const int s = ((row & 3) | ((row >> 1) & 4)) << 1;
-#pragma unroll
-    for (int i = 0; i < TP; ++i)
-      pa[i] = row * (2 * BP) + ((wp * 2 * TP + i * 2 + (m & 3) / 2) ^ s) * 16 + (m & 1) * 8;
-#pragma unroll
-    for (int j = 0; j < TQ; ++j)
-      qa[j] = S::kPBytes + row * (2 * BQ) + ((wq * 2 * TQ + j * 2 + (m & 3) / 2) ^ s) * 16 + (m & 1) * 8;
-  }
-
-#pragma unroll
-  for (int s = 0; s < NST - 1; ++s)
-    if (s < nk) {
-      sources(s);
-      issue(s, s);
-    }
-  sources(NST - 1);
-  int buf = 0;
-  for (int step = 0; step < nk; ++step) {
-    if (!GATHER && step + NST - 2 < nk) wait_tiles<(NST - 2) * S::kLoads>();
-    else wait_tiles<0>();
-    const int ahead = step + NST - 1;
-    if (ahead < nk) issue(ahead, buf == 0 ? NST - 1 : buf - 1);
-    sources(ahead + 1);
-    const uint32_t st = lds + buf * S::kStage;
-    buf = buf == NST - 1 ? 0 : buf + 1;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      bf16x8 pf[TP], qf[TQ];
-#pragma unroll
-      for (int j = 0; j < TQ; ++j) {
-        struct { i16x4 lo, hi; } v;
-        v.lo = lds_read_tr(st + qa[j] + h * 32 * 2 * BQ);
-        v.hi = lds_read_tr(st + qa[j] + (h * 32 + 4) * 2 * BQ);
-        qf[j] = __builtin_bit_cast(bf16x8, v);
-      }
-#pragma unroll
-      for (int i = 0; i < TP; ++i) {
-        struct { i16x4 lo, hi; } v;
-        v.lo = lds_read_tr(st + pa[i] + h * 32 * 2 * BP);
-        v.hi = lds_read_tr(st + pa[i] + (h * 32 + 4) * 2 * BP);
-        pf[i] = __builtin_bit_cast(bf16x8, v);
-      }
+  if (nk > 0) {
+    uint32_t pa[TP], qa[TQ];
+    {
+      const int row = quarter * 8 + m / 4;
 #pragma unroll
       for (int i = 0; i < TP; ++i)
+        pa[i] = row * (2 * BP) + ((wp * 2 * TP + i * 2 + (m & 3) / 2) ^ swz_t(row)) * 16 + (m & 1) * 8;
+#pragma unroll
+      for (int j = 0; j < TQ; ++j)
+        qa[j] = row * (2 * BQ) + ((wq * 2 * TQ + j * 2 + (m & 3) / 2) ^ swz_t(row)) * 16 + (m & 1) * 8;
+    }
+
+    // The order of loads, waits and barriers is the rows kernel's: step t
+    // issues P's step t - 1 + NSP over its MFMAs and, behind its barrier, Q's
+    // step t + NSQ.
+#pragma unroll
+    for (int t = -NSP; t < 0; ++t) {
+      if (t - 1 + NSP >= 0) {
+        if constexpr (GATHER) {                                       // step 0: its indices straight from memory
+#pragma unroll
+          for (int i = 0; i < S::kPLoads; ++i)
+            dma16(gathered(i, 0, a.row_index[begin + min(prow + i * PR, rows - 1)]), p_at(0) + (i * S::kWaves + wave) * 1024);
+        } else {
+          issue_p(t - 1 + NSP, t - 1 + NSP);
+        }
+      }
+      if (t + NSQ >= 0) issue_q(t + NSQ, t + NSQ);
+    }
+    if (nk >= NSP) wait_tiles<S::kBehind + S::kQLoads>();
+    else wait_tiles<0>();
+    auto publish = [&](int step) {
+      if (step - 1 + NSP < nk) wait_tiles<S::kBehind>();
+      else wait_tiles<0>();
+    };
+    int step = 0, pbuf = 0, qbuf = 0;
+    auto before = [&](int buf) { return buf == 0 ? NSP - 1 : buf - 1; };
+
+    // Slots, operand ring and barrier as in the rows kernel; halves are 32 rows.
+    constexpr int SLOTS = 2 * TP, D = 3, RING = 4;
+    static_assert(SLOTS % RING == 0 && TQ <= SLOTS - D && D <= TP, "operand ring");
+    bf16x8 pf[RING], qf[2][TQ];
+    auto operand = [&](uint32_t at, int row_bytes) {
+      struct { i16x4 lo, hi; } t;
+      t.lo = lds_read_tr(at);
+      t.hi = lds_read_tr(at + 4 * row_bytes);
+      return __builtin_bit_cast(bf16x8, t);
+    };
+    auto read_q = [&](int h, uint32_t at, int j) { qf[h][j] = operand(at + qa[j] + h * 32 * 2 * BQ, 2 * BQ); };
+    auto read_p = [&](int k, uint32_t at) { pf[k % RING] = operand(at + pa[k % TP] + k / TP * 32 * 2 * BP, 2 * BP); };
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) read_q(0, q_at(0), j);
+#pragma unroll
+    for (int k = 0; k < D; ++k) read_p(k, p_at(0));
+    auto body = [&](auto more, auto last) {
+      const int pb = pbuf, qb = qbuf;
+      pbuf = pbuf == NSP - 1 ? 0 : pbuf + 1;
+      qbuf = qbuf == NSQ - 1 ? 0 : qbuf + 1;
+      if constexpr (!more) issue_p(step - 1 + NSP, before(pb));
+#pragma unroll
+      for (int k = 0; k < SLOTS; ++k) {
+        const int late = k - (SLOTS - D);
+        if constexpr (!last)
+          if (late == 0) publish(step);
+        if (k + D < SLOTS) read_p(k + D, p_at(pb));
+        else if constexpr (!last) read_p(k + D - SLOTS, p_at(pbuf));
+        if (k < TP) {
+#pragma unroll
+          for (int j = k * TQ / TP; j < (k + 1) * TQ / TP; ++j) read_q(1, q_at(qb), j);
+        }
+        if (late >= 0) {
+          if constexpr (!last) {
+#pragma unroll
+            for (int j = late * TQ / D; j < (late + 1) * TQ / D; ++j) read_q(0, q_at(qbuf), j);
+          }
+          if constexpr (more) {
+#pragma unroll
+            for (int l = late * S::kQLoads / D; l < (late + 1) * S::kQLoads / D; ++l) load_q(l, step + NSQ, qb);
+          }
+        } else if constexpr (more) {
+          constexpr int n = SLOTS - D;
+#pragma unroll
+          for (int l = 0; l < S::kPLoads; ++l)
+            if (l * n / S::kPLoads == k) load_p(l, step - 1 + NSP, before(pb));
+        }
 #pragma unroll
         for (int j = 0; j < TQ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[i], qf[j], acc[i][j], 0, 0, 0);
-    }
+          acc[k % TP][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[k % RING], qf[k / TP][j], acc[k % TP][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (!more && !last) issue_q(step + NSQ, qb);
+    };
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    const int whole = nk - (ragged_end ? 1 : 0);
+    constexpr int ahead = NSP - 1 > NSQ ? NSP - 1 : NSQ;
+    for (; step + ahead < whole; ++step) body(yes, no);
+    for (; step + 1 < nk; ++step) body(no, no);
+    body(no, yes);
   }
 
+  // Stores.  fp32: lanes of even and odd m exchange halves of two neighbouring
+  // tiles, so that 8 lanes write 128 consecutive bytes of one n: half lines,
+  // written in pieces, took 930 us where whole ones take 690 (32 groups of 256
+  // rows, 7168 x 2048).  Results larger than half the last-level cache leave
+  // it alone (870 us without).
+  const bool odd = m & 1;
 #pragma unroll
   for (int j = 0; j < TQ; ++j) {
-    const int n = q0 + (wq * TQ + j) * 16 + m;
-    if (n >= a.N) continue;
-    const int64_t o = (static_cast<int64_t>(group) * a.N + n) * a.K;
 #pragma unroll
-    for (int i = 0; i < TP; ++i) {
+    for (int i = 0; i < TP; i += 2) {
       if constexpr (F32) {
-        const int k = p0 + (wp * TP + i) * 16 + quarter * 4;
-        if (k >= a.K) continue;
-        f32x4* at = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o + k);
-        f32x4 v = acc[i][j];
-        if (a.accumulate) {
-          const f32x4 old = *at;
-          v = f32x4{old[0] + v[0], old[1] + v[1], old[2] + v[2], old[3] + v[3]};
+        const int k = p0 + (wp * TP + i + (m & 1)) * 16 + quarter * 4;
+        f32x4 v[2];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float x = acc[i][j][r], y = acc[i + 1][j][r];
+          const float other = dpp_f32<0xB1>(odd ? x : y);             // quad_perm [1,0,3,2]
+          v[0][r] = odd ? other : x;
+          v[1][r] = odd ? y : other;
         }
-        *at = v;
-      } else if ((i & 1) == 0) {
-        const int kk = p0 + (wp * TP + i + (quarter & 1)) * 16 + (quarter >> 1) * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n = q0 + (wq * TQ + j) * 16 + (m & ~1) + h;
+          if (n >= a.N || k >= a.K) continue;
+          f32x4* at = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + (static_cast<int64_t>(group) * a.N + n) * a.K + k);
+          if (a.accumulate) {
+            const f32x4 old = *at;
+            v[h] = f32x4{old[0] + v[h][0], old[1] + v[h][1], old[2] + v[h][2], old[3] + v[h][3]};
+          }
+          if (a.stream) __builtin_nontemporal_store(v[h], at);
+          else *at = v[h];
+        }
+      } else {
+        const int n = q0 + (wq * TQ + j) * 16 + m;
+        const int k = p0 + (wp * TP + i + (quarter & 1)) * 16 + (quarter >> 1) * 8;
         const v4u v = pack_pair(acc[i][j], acc[i + 1][j]);
-        if (kk < a.K) *reinterpret_cast<v4u*>(static_cast<uint16_t*>(a.out) + o + kk) = v;
+        if (n < a.N && k < a.K)
+          *reinterpret_cast<v4u*>(static_cast<uint16_t*>(a.out) + (static_cast<int64_t>(group) * a.N + n) * a.K + k) = v;
       }
     }
   }
 }
 
-template <bool GATHER, bool F32, int BP, int BQ, int WP, int WQ, int NST>
+template <bool GATHER, bool F32, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
 hipError_t launch_weight_tile(const GemmWeightArgs& a, hipStream_t st) {
-  const int64_t tiles = static_cast<int64_t>((a.K + BP - 1) / BP) * ((a.N + BQ - 1) / BQ) * a.g.G;
-  const int64_t grid = (tiles + 7) / 8 * 8;
-  if (grid > max_blocks(WP * WQ * kWave)) return hipErrorInvalidConfiguration;
-  gemm_weight_kernel<GATHER, F32, BP, BQ, WP, WQ, NST><<<static_cast<unsigned>(grid), WP * WQ * kWave, 0, st>>>(a);
+  const int64_t per_group = static_cast<int64_t>((a.K + BP - 1) / BP) * ((a.N + BQ - 1) / BQ);
+  const int64_t grid = per_group >= 64 ? (per_group + 7) / 8 * 8 * a.g.G : per_group * a.g.G;
+  if (grid > max_blocks(WP * WQ * kWave) || grid > (1ll << 31) - 1) return hipErrorInvalidConfiguration;
+  gemm_weight_kernel<GATHER, F32, BP, BQ, WP, WQ, NSP, NSQ><<<static_cast<unsigned>(grid), WP * WQ * kWave, 0, st>>>(a);
   return hipGetLastError();
 }
 
 template <bool GATHER, bool F32>
 hipError_t launch_weight(const GemmWeightArgs& a, hipStream_t st) {
   const int64_t big = static_cast<int64_t>((a.K + 255) / 256) * ((a.N + 255) / 256) * a.g.G;
-  if (big < 256) return launch_weight_tile<GATHER, F32, 128, 128, 2, 2, 2>(a, st);
-  return launch_weight_tile<GATHER, F32, 256, 256, 2, 4, 2>(a, st);
+  if (big < 256) return launch_weight_tile<GATHER, F32, 128, 128, 2, 2, 2, 2>(a, st);
+  return launch_weight_tile<GATHER, F32, 256, 256, 2, 4, GATHER ? 2 : 3, 2>(a, st);
 }
 
-hipError_t launch_gemm_weight(const GemmWeightArgs& a, hipStream_t st) {
+hipError_t launch_gemm_weight(const GemmWeightArgs& args, hipStream_t st) {
+  GemmWeightArgs a = args;
   if (a.g.G == 0) return hipSuccess;
+  a.stream = 4ll * a.g.G * a.N * a.K > (128ll << 20);
   if (a.row_index) return a.out_f32 ? launch_weight<true, true>(a, st) : launch_weight<true, false>(a, st);
   return a.out_f32 ? launch_weight<false, true>(a, st) : launch_weight<false, false>(a, st);
 }
