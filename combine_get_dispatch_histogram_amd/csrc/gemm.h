@@ -23,6 +23,10 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
+// The kernels' lambdas: one that is called instead of inlined keeps what it
+// captures in scratch memory.
+#define MIEP_INLINE __attribute__((always_inline))
+
 // A tile's K extent is 128 bytes a row in every type (64 bf16, 128 E4M3).
 constexpr int kStepBytes = 128;
 
@@ -84,6 +88,9 @@ __device__ __forceinline__ v4u pack_pair(const f32x4& a, const f32x4& b) {
   return v4u{static_cast<uint32_t>(x[0]), static_cast<uint32_t>(y[0]), static_cast<uint32_t>(x[1]), static_cast<uint32_t>(y[1])};
 }
 
+// Waits until every wavefront's LDS reads have returned.
+__device__ __forceinline__ void all_read() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // Keeps the arithmetic that makes v where it is written: left alone, the
 // compiler moves the multiplications by FP8 scales behind a step's branches
 // and holds every MFMA's result until then.
@@ -103,27 +110,38 @@ __device__ __forceinline__ void group_range(const GroupArgs& g, int i, int64_t* 
 
 struct TileAt {
   int group;       // -1: past the last tile
-  int first;       // the tile's place among the group's (ceil(rows / bq) * per) tiles
+  int first;       // the tile's place among the group's tiles of its kind
+  int half;        // at most `half` rows: the group's last tile
   int64_t begin;
   int rows;
 };
 
-// Tile t of the sequence in which group i has ceil(rows / bq) * per tiles.
+// Row tiles of n rows: the whole ones of bq rows, and a last one where it has
+// more than `half` rows (the others are the half tile, one at most; half 0:
+// there is none).
+__device__ __forceinline__ int full_tiles(int n, int bq, int half) { return (n + bq - 1 - half) / bq; }
+__device__ __forceinline__ int tiles_of(int n, int bq, int half, bool halves) {
+  const int full = full_tiles(n, bq, half);
+  return halves ? (n > full * bq ? 1 : 0) : full;
+}
+
+// Tile t of the sequence in which group i has tiles_of(rows) * per tiles.
 // Every wavefront walks for itself: one load a lane for each 64 groups and a
-// scan of the lane counts.  *total (when wanted) is the number of tiles.
-__device__ __forceinline__ TileAt find_tile(const GroupArgs& g, int bq, int per, int t) {
+// scan of the lane counts.
+__device__ __forceinline__ TileAt find_tile(const GroupArgs& g, int bq, int per, int half, bool halves, int t) {
   const int lane = lane_id();
   int before = 0;
   TileAt r;
   r.group = -1;
   r.first = 0;
+  r.half = halves;
   r.begin = 0;
   r.rows = 0;
   for (int g0 = 0; g0 < g.G; g0 += kWave) {
     int64_t b = 0;
     int n = 0;
     if (g0 + lane < g.G) group_range(g, g0 + lane, &b, &n);
-    const int tiles = (n + bq - 1) / bq * per;
+    const int tiles = tiles_of(n, bq, half, halves) * per;
     const int inc = wave_inclusive_scan(tiles);
     const uint64_t past = ballot(before + inc > t);
     if (past != 0) {
@@ -140,16 +158,18 @@ __device__ __forceinline__ TileAt find_tile(const GroupArgs& g, int bq, int per,
   return r;
 }
 
-__device__ __forceinline__ int count_tiles(const GroupArgs& g, int bq, int per) {
+// How many they are; at most `most`, whatever overlapping groups would add up to.
+__device__ __forceinline__ int count_tiles(const GroupArgs& g, int bq, int per, int half, bool halves, int most) {
   const int lane = lane_id();
-  int total = 0;
+  int64_t total = 0;
   for (int g0 = 0; g0 < g.G; g0 += kWave) {
     int64_t b = 0;
     int n = 0;
     if (g0 + lane < g.G) group_range(g, g0 + lane, &b, &n);
-    total += readlane(wave_inclusive_scan((n + bq - 1) / bq * per), 63);
+    const int sum = readlane(wave_inclusive_scan(tiles_of(n, bq, half, halves) * per), 63);
+    total += sum < 0 ? most : sum;
   }
-  return total;
+  return static_cast<int>(total < most ? total : most);
 }
 
 }  // namespace miep

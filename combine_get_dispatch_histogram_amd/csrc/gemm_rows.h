@@ -70,34 +70,64 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
   const bool ragged_end = C % KE != 0;
   const int64_t kb = C / kFp8Group;                                       // scale blocks of a row (FP8)
 
-  int total = count_tiles(a.g, BQ, ntiles);
-  if (total < 0 || total > a.max_tiles) total = a.max_tiles;
-  // Workgroups go to the 8 XCDs in turn: XCD x walks the x-th eighth of the
-  // tiles, so tiles that share weights or rows meet in one L2.
-  const int chunk = (total + 7) / 8;
-  const int xcd = blockIdx.x & 7;
-  const int end = min(total, (xcd + 1) * chunk);
+  // Tiles with at most half their rows, on which half the wavefronts idle, come
+  // after all others, so that the last round of workgroups is filled up with
+  // them.  Workgroups go to the 8 XCDs in turn: XCD x walks the x-th eighth of
+  // either kind, so tiles that share weights or rows meet in one L2.
+  constexpr int kHalf = WQ > 1 ? BQ / 2 : 0;
+  const int xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
+  int64_t full0, full1, half0 = 0, half1 = 0;
+  {
+    const int64_t n = count_tiles(a.g, BQ, ntiles, kHalf, false, a.max_tiles);
+    full0 = n * xcd / 8;
+    full1 = n * (xcd + 1) / 8;
+    if constexpr (kHalf > 0) {
+      const int64_t h = count_tiles(a.g, BQ, ntiles, kHalf, true, a.max_tiles);
+      half0 = h * xcd / 8;
+      half1 = h * (xcd + 1) / 8;
+    }
+  }
+  int turn = blockIdx.x >> 3;
+  auto next_tile = [&]() MIEP_INLINE {
+    TileAt r;
+    r.group = -1;
+    const int64_t full = full1 - full0, at = turn;
+    if (at < full) r = find_tile(a.g, BQ, ntiles, kHalf, false, static_cast<int>(full0 + at));
+    else if (kHalf > 0 && at - full < half1 - half0) r = find_tile(a.g, BQ, ntiles, kHalf, true, static_cast<int>(half0 + at - full));
+    turn += stride;
+    return r;
+  };
 
-  for (int t = xcd * chunk + (blockIdx.x >> 3); t < end; t += gridDim.x >> 3) {
-    const TileAt at = find_tile(a.g, BQ, ntiles, t);
-    if (at.group < 0) break;
-    const int mtiles = (at.rows + BQ - 1) / BQ;
-    const int first = min(max(at.first, 0), mtiles * ntiles - 1);
+  // The tile that is being loaded and multiplied; the previous one's results
+  // are stored while its first loads are under way.
+  int p0, live;
+  int64_t row0;
+  const uint8_t *pg, *pbase, *qbase;
+  uint32_t poff[S::kPLoads];
+  constexpr int QL = S::kQBytes / 1024 / S::kWaves;
+  uint32_t qoff[QL];
+  uint32_t lost;                                                      // bit i: load i's row has no source
+  constexpr int SB = EL == kGemmFp8 ? 4 : 1;                          // bytes of an FP8 scale
+  const uint8_t* sptr;
+  uint32_t sto;
+  auto set_tile = [&](const TileAt& at) MIEP_INLINE {
     // bands of kBand row tiles, in a band the row tiles of one column of tiles
     // after the other: the 32 tiles that an XCD works on at a time share 8
     // tiles of rows and 4 of weights
     constexpr int kBand = 8;
+    const int mtiles = at.half ? 1 : max(full_tiles(at.rows, BQ, kHalf), 1);
+    const int first = min(max(at.first, 0), mtiles * ntiles - 1);
     const int band = first / (kBand * ntiles), in_band = first - band * (kBand * ntiles);
     const int bh = min(kBand, mtiles - band * kBand);
-    const int pt = in_band / bh, qt = band * kBand + in_band - pt * bh;
-    const int p0 = pt * BP, q0 = qt * BQ;
-    const int live = min(BQ, at.rows - q0);                           // rows of this tile
-    const int64_t row0 = at.begin + q0;
-    const uint8_t* pg = static_cast<const uint8_t*>(a.p) + static_cast<int64_t>(at.group) * NO * C * EB;
+    const int pt = in_band / bh, qt = at.half ? at.rows / BQ : band * kBand + in_band - pt * bh;
+    const int q0 = qt * BQ;
+    p0 = pt * BP;
+    live = min(BQ, at.rows - q0);                                     // rows of this tile
+    row0 = at.begin + q0;
+    pg = static_cast<const uint8_t*>(a.p) + static_cast<int64_t>(at.group) * NO * C * EB;
 
     // Sources of this lane's 16 bytes of every load of a stage.
-    const uint8_t* pbase = pg + (PT ? static_cast<int64_t>(p0) * EB : static_cast<int64_t>(p0) * ldp);
-    uint32_t poff[S::kPLoads];
+    pbase = pg + (PT ? static_cast<int64_t>(p0) * EB : static_cast<int64_t>(p0) * ldp);
 #pragma unroll
     for (int i = 0; i < S::kPLoads; ++i) {
       const int l = i * S::kWaves + wave;
@@ -117,10 +147,8 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
     // Q's rows: at a fixed stride, or anywhere in the gathered source (its
     // offsets in 16-byte units, so that 32 bits reach 64 GiB).  A row without
     // a source reads row 0 of the weights, and stores zeros.
-    const uint8_t* qbase = static_cast<const uint8_t*>(a.q) + (GATHER ? 0 : row0 * ldq);
-    constexpr int QL = S::kQBytes / 1024 / S::kWaves;
-    uint32_t qoff[QL];
-    uint32_t lost = 0;                                                // bit i: load i's row has no source
+    qbase = static_cast<const uint8_t*>(a.q) + (GATHER ? 0 : row0 * ldq);
+    lost = 0;
 #pragma unroll
     for (int i = 0; i < QL; ++i) {
       int row = (i * S::kWaves + wave) * 8 + lane / 8;
@@ -137,9 +165,6 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
     }
     // FP8: this wavefront's one load of a stage's scales -- 64 rows of Q's, or
     // the P blocks' (every further wavefront repeats those)
-    constexpr int SB = EL == kGemmFp8 ? 4 : 1;                        // bytes of a scale
-    const uint8_t* sptr = nullptr;
-    uint32_t sto = 0;
     if constexpr (S::kFp8) {
       constexpr int SL = S::kQScales / kWave;
       const int64_t pb = static_cast<int64_t>(at.group) * ((NO + 127) / 128);
@@ -157,14 +182,16 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
       sto = S::kQBytes + min(wave, SL) * 256;
     }
 
-    auto p_at = [&](int buf) { return lds + buf * S::kPBytes; };
-    auto q_at = [&](int buf) { return lds + NSP * S::kPBytes + buf * S::kQStage; };
+  };
+
+    auto p_at = [&](int buf) MIEP_INLINE { return lds + buf * S::kPBytes; };
+    auto q_at = [&](int buf) MIEP_INLINE { return lds + NSP * S::kPBytes + buf * S::kQStage; };
     // Load i of this wavefront's loads of a step of 128 whole bytes.
-    auto load_p = [&](int i, int step, int buf) {
+    auto load_p = [&](int i, int step, int buf) MIEP_INLINE {
       dma16s(pbase + static_cast<int64_t>(step) * (PT ? (kStepBytes / 2) * ldp : kStepBytes), poff[i],
              p_at(buf) + (i * S::kWaves + wave) * 1024);
     };
-    auto load_q = [&](int i, int step, int buf) {
+    auto load_q = [&](int i, int step, int buf) MIEP_INLINE {
       if (i < QL) {
         const uint32_t to = q_at(buf) + (i * S::kWaves + wave) * 1024;
         if constexpr (GATHER) {
@@ -182,7 +209,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
     // contraction that is not whole reads zeros behind its end.  (Its lane
     // constants are computed anew: kept through the loop they would cost it
     // registers.)
-    auto issue_p = [&](int step, int buf) {
+    auto issue_p = [&](int step, int buf) MIEP_INLINE {
       if (step >= nk) return;
       if (S::kFp8 || !ragged_end || step != nk - 1) {
 #pragma unroll
@@ -201,7 +228,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
         dma16(in ? static_cast<const void*>(pb + poff[i]) : static_cast<const void*>(g_zero16), p_at(buf) + l * 1024);
       }
     };
-    auto issue_q = [&](int step, int buf) {
+    auto issue_q = [&](int step, int buf) MIEP_INLINE {
       if (step >= nk) return;
       if (S::kFp8 || !ragged_end || step != nk - 1) {
 #pragma unroll
@@ -222,13 +249,6 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
       }
     };
 
-    f32x4 acc[TP][TQ];
-#pragma unroll
-    for (int i = 0; i < TP; ++i)
-#pragma unroll
-      for (int j = 0; j < TQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    const bool busy = wq * 16 * TQ < live;
     // lane addresses of the operand reads, within a buffer
     uint32_t pa[PT ? TP : 2], qa[2];
     if constexpr (PT) {
@@ -249,29 +269,43 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
       qa[1] = qa[0] ^ 64;
     }
 
-    wait_tiles<0>();                                                  // the previous tile's reads
     // P's buffers may be deeper than Q's: the weights stream from memory, the
     // rows mostly come from L2.  Step t issues the loads of P's step t - 1 +
     // NSP, spread over its MFMAs, and behind its barrier those of Q's step t +
     // NSQ; before the first step come those that steps before it would have
     // issued, in that order.
+    auto issue_first = [&]() MIEP_INLINE {
 #pragma unroll
-    for (int t = -NSP; t < 0; ++t) {
-      if (t - 1 + NSP >= 0) issue_p(t - 1 + NSP, t - 1 + NSP);
-      if (t + NSQ >= 0) issue_q(t + NSQ, t + NSQ);
-    }
+      for (int t = -NSP; t < 0; ++t) {
+        if (t - 1 + NSP >= 0) issue_p(t - 1 + NSP, t - 1 + NSP);
+        if (t + NSQ >= 0) issue_q(t + NSQ, t + NSQ);
+      }
+    };
+
+    f32x4 acc[TP][TQ];
+    TileAt at = next_tile();
+    if (at.group < 0) return;
+    set_tile(at);
+    issue_first();
+    while (true) {
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const bool busy = wq * 16 * TQ < live;
+    at = next_tile();
     if (nk >= NSP) wait_tiles<S::kBehind + S::kQLoads>();
     else wait_tiles<0>();
     // The barrier of a step: the next step's tile has come (while the loads
     // behind it may be in flight; at the contraction's end there are fewer),
     // and every wavefront has read this step's.
-    auto publish = [&](int step) {
+    auto publish = [&](int step) MIEP_INLINE {
       if (step - 1 + NSP < nk) wait_tiles<S::kBehind>();
       else wait_tiles<0>();
     };
     int step = 0, pbuf = 0, qbuf = 0;
-    auto before = [&](int buf) { return buf == 0 ? NSP - 1 : buf - 1; };
-    auto next_buffers = [&]() {
+    auto before = [&](int buf) MIEP_INLINE { return buf == 0 ? NSP - 1 : buf - 1; };
+    auto next_buffers = [&]() MIEP_INLINE {
       pbuf = pbuf == NSP - 1 ? 0 : pbuf + 1;
       qbuf = qbuf == NSQ - 1 ? 0 : qbuf + 1;
     };
@@ -292,8 +326,8 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
       constexpr int SLOTS = 2 * TP, D = TP < 3 ? TP : 3, RING = 4;
       static_assert(SLOTS % RING == 0 && D < RING && TQ <= SLOTS - D && D <= TP, "operand ring");
       bf16x8 pf[RING], qf[2][TQ];
-      auto read_q = [&](int h, uint32_t at, int j) { qf[h][j] = lds_read<bf16x8>(at + qa[h] + j * 16 * kStepBytes); };
-      auto read_p = [&](int k, uint32_t at) {
+      auto read_q = [&](int h, uint32_t at, int j) MIEP_INLINE { qf[h][j] = lds_read<bf16x8>(at + qa[h] + j * 16 * kStepBytes); };
+      auto read_p = [&](int k, uint32_t at) MIEP_INLINE {
         const int h = k / TP, i = k % TP;
         if constexpr (PT) {
           struct { i16x4 lo, hi; } t;
@@ -308,7 +342,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
       for (int j = 0; j < TQ; ++j) read_q(0, q_at(0), j);
 #pragma unroll
       for (int k = 0; k < D; ++k) read_p(k, p_at(0));
-      auto body = [&](auto more, auto last) {
+      auto body = [&](auto more, auto last) MIEP_INLINE {
         const int pb = pbuf, qb = qbuf;
         next_buffers();
         if constexpr (!more) issue_p(step - 1 + NSP, before(pb));
@@ -363,20 +397,20 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
       i32x8 pf[2], qf[TQ];
       float s[TQ];
       int e[TQ], ep = 0;
-      auto operand = [&](uint32_t at0, uint32_t at1) {
+      auto operand = [&](uint32_t at0, uint32_t at1) MIEP_INLINE {
         struct { i32x4 lo, hi; } t;
         t.lo = lds_read<i32x4>(at0);
         t.hi = lds_read<i32x4>(at1);
         return __builtin_bit_cast(i32x8, t);
       };
-      auto read_p = [&](int i, uint32_t at) {
+      auto read_p = [&](int i, uint32_t at) MIEP_INLINE {
         pf[i & 1] = operand(at + pa[0] + i * 16 * kStepBytes, at + pa[1] + i * 16 * kStepBytes);
       };
-      auto read_q = [&](int j, uint32_t at) {
+      auto read_q = [&](int j, uint32_t at) MIEP_INLINE {
         qf[j] = operand(at + qa[0] + j * 16 * kStepBytes, at + qa[1] + j * 16 * kStepBytes);
       };
       const uint32_t psat = S::kQBytes + S::kQScales * 4 + wp * 16 * TP / 128 * 4;
-      auto read_scales = [&](uint32_t at) {
+      auto read_scales = [&](uint32_t at) MIEP_INLINE {
         if constexpr (EL == kGemmFp8) {
           const float sp = lds_read<float>(at + psat);
 #pragma unroll
@@ -391,7 +425,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
       for (int j = 0; j < TQ; ++j) read_q(j, q_at(0));
       read_p(0, p_at(0));
       read_scales(q_at(0));
-      auto body = [&](auto more, auto last) {
+      auto body = [&](auto more, auto last) MIEP_INLINE {
         const int pb = pbuf, qb = qbuf;
         next_buffers();
         if constexpr (!more) issue_p(step - 1 + NSP, before(pb));
@@ -409,7 +443,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
             } else {
 #pragma unroll
               for (int l = 0; l < S::kPLoads; ++l)
-                if (l * (TP - 1) / S::kPLoads == i) load_p(l, step - 1 + NSP, before(pb));
+                if (i == (l / 2 < TP - 2 ? l / 2 : TP - 2)) load_p(l, step - 1 + NSP, before(pb));
             }
           }
           f32x4 d[TQ];
@@ -450,25 +484,34 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
       body(no, yes);
     }
 
-    if (!busy) continue;
+    const int out_p0 = p0, out_live = live;
+    const int64_t out_row0 = row0;
+    if (at.group >= 0) {
+      all_read();                                                     // this tile's last buffers
+      set_tile(at);
+      issue_first();
+    }
+    if (busy) {
 #pragma unroll
-    for (int j = 0; j < TQ; ++j) {
-      const int row = (wq * TQ + j) * 16 + m;
-      if (row >= live) continue;
-      bool none = false;
-      if constexpr (GATHER) {
-        const int src = a.row_index[row0 + row];
-        none = src < 0 || src >= a.q_rows;
-      }
-      uint16_t* o = a.out + (row0 + row) * NO;
+      for (int j = 0; j < TQ; ++j) {
+        const int row = (wq * TQ + j) * 16 + m;
+        if (row >= out_live) continue;
+        bool none = false;
+        if constexpr (GATHER) {
+          const int src = a.row_index[out_row0 + row];
+          none = src < 0 || src >= a.q_rows;
+        }
+        uint16_t* o = a.out + (out_row0 + row) * NO;
 #pragma unroll
-      for (int i = 0; i < TP; i += 2) {
-        const int p = p0 + (wp * TP + i + (quarter & 1)) * 16 + (quarter >> 1) * 8;
-        v4u v = pack_pair(acc[i][j], acc[i + 1][j]);
-        if (none) v = v4u{0u, 0u, 0u, 0u};
-        if (p < NO) *reinterpret_cast<v4u*>(o + p) = v;
+        for (int i = 0; i < TP; i += 2) {
+          const int p = out_p0 + (wp * TP + i + (quarter & 1)) * 16 + (quarter >> 1) * 8;
+          v4u v = pack_pair(acc[i][j], acc[i + 1][j]);
+          if (none) v = v4u{0u, 0u, 0u, 0u};
+          if (p < NO) *reinterpret_cast<v4u*>(o + p) = v;
+        }
       }
     }
+    if (at.group < 0) return;
   }
 }
 

@@ -93,18 +93,18 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
     if (q0 + col / 2 >= a.N) col = 0;
     qoff[i] = static_cast<uint32_t>(row * ldq + col);
   }
-  auto p_at = [&](int buf) { return lds + buf * S::kPBytes; };
-  auto q_at = [&](int buf) { return lds + NSP * S::kPBytes + buf * (S::kQBytes + S::kIndexBytes); };
+  auto p_at = [&](int buf) MIEP_INLINE { return lds + buf * S::kPBytes; };
+  auto q_at = [&](int buf) MIEP_INLINE { return lds + NSP * S::kPBytes + buf * (S::kQBytes + S::kIndexBytes); };
   // A gathered row's address; a row behind the group's last, or without a
   // source, reads zeros.
-  auto gathered = [&](int i, int step, int src) {
+  auto gathered = [&](int i, int step, int src) MIEP_INLINE {
     const bool in = step * S::kRows + prow + i * PR < rows && src >= 0 && src < a.p_rows;
     return in ? static_cast<const void*>(pbase + src * ldp + poff[i]) : static_cast<const void*>(g_zero16);
   };
   // Load i of a step of 64 whole rows (gathered: of any).  The indices of a
   // gathered step come with the Q loads two steps before its own loads, those
   // of step u + 1 in the place behind Q's step u.
-  auto load_p = [&](int i, int step, int buf) {
+  auto load_p = [&](int i, int step, int buf) MIEP_INLINE {
     const uint32_t to = p_at(buf) + (i * S::kWaves + wave) * 1024;
     if constexpr (GATHER) {
       const int src = lds_read<int>(q_at((step - 1) & 1) + S::kQBytes + (prow + i * PR) * 4);
@@ -113,13 +113,13 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
       dma16s(pbase + static_cast<int64_t>(step) * S::kRows * ldp, poff[i], to);
     }
   };
-  auto load_q = [&](int i, int step, int buf) {
+  auto load_q = [&](int i, int step, int buf) MIEP_INLINE {
     if (i < QL) dma16s(qbase + static_cast<int64_t>(step) * S::kRows * ldq, qoff[i], q_at(buf) + (i * S::kWaves + wave) * 1024);
     else if constexpr (GATHER)
       dma4(a.row_index + begin + min((step + 1) * S::kRows + lane, rows - 1), q_at(buf) + S::kQBytes);
   };
   // A step's loads, if there is such a step; the last one may have fewer rows.
-  auto issue_p = [&](int step, int buf) {
+  auto issue_p = [&](int step, int buf) MIEP_INLINE {
     if (step >= nk) return;
 #pragma unroll
     for (int i = 0; i < S::kPLoads; ++i) {
@@ -132,7 +132,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
       }
     }
   };
-  auto issue_q = [&](int step, int buf) {
+  auto issue_q = [&](int step, int buf) MIEP_INLINE {
     if (step >= nk) return;
 #pragma unroll
     for (int i = 0; i < S::kQLoads; ++i) {
@@ -182,30 +182,30 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
     }
     if (nk >= NSP) wait_tiles<S::kBehind + S::kQLoads>();
     else wait_tiles<0>();
-    auto publish = [&](int step) {
+    auto publish = [&](int step) MIEP_INLINE {
       if (step - 1 + NSP < nk) wait_tiles<S::kBehind>();
       else wait_tiles<0>();
     };
     int step = 0, pbuf = 0, qbuf = 0;
-    auto before = [&](int buf) { return buf == 0 ? NSP - 1 : buf - 1; };
+    auto before = [&](int buf) MIEP_INLINE { return buf == 0 ? NSP - 1 : buf - 1; };
 
     // Slots, operand ring and barrier as in the rows kernel; halves are 32 rows.
     constexpr int SLOTS = 2 * TP, D = 3, RING = 4;
     static_assert(SLOTS % RING == 0 && TQ <= SLOTS - D && D <= TP, "operand ring");
     bf16x8 pf[RING], qf[2][TQ];
-    auto operand = [&](uint32_t at, int row_bytes) {
+    auto operand = [&](uint32_t at, int row_bytes) MIEP_INLINE {
       struct { i16x4 lo, hi; } t;
       t.lo = lds_read_tr(at);
       t.hi = lds_read_tr(at + 4 * row_bytes);
       return __builtin_bit_cast(bf16x8, t);
     };
-    auto read_q = [&](int h, uint32_t at, int j) { qf[h][j] = operand(at + qa[j] + h * 32 * 2 * BQ, 2 * BQ); };
-    auto read_p = [&](int k, uint32_t at) { pf[k % RING] = operand(at + pa[k % TP] + k / TP * 32 * 2 * BP, 2 * BP); };
+    auto read_q = [&](int h, uint32_t at, int j) MIEP_INLINE { qf[h][j] = operand(at + qa[j] + h * 32 * 2 * BQ, 2 * BQ); };
+    auto read_p = [&](int k, uint32_t at) MIEP_INLINE { pf[k % RING] = operand(at + pa[k % TP] + k / TP * 32 * 2 * BP, 2 * BP); };
 #pragma unroll
     for (int j = 0; j < TQ; ++j) read_q(0, q_at(0), j);
 #pragma unroll
     for (int k = 0; k < D; ++k) read_p(k, p_at(0));
-    auto body = [&](auto more, auto last) {
+    auto body = [&](auto more, auto last) MIEP_INLINE {
       const int pb = pbuf, qb = qbuf;
       pbuf = pbuf == NSP - 1 ? 0 : pbuf + 1;
       qbuf = qbuf == NSQ - 1 ? 0 : qbuf + 1;

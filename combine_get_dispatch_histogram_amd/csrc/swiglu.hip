@@ -35,11 +35,10 @@ __device__ __forceinline__ v4u narrow(const float (&f)[8]) {
 
 template <int KIND>
 __global__ __launch_bounds__(256) void swiglu_kernel(SwigluArgs a) {
-  int total = count_tiles(a.g, a.rows_per_tile, 1);
-  if (total < 0 || total > a.max_tiles) total = a.max_tiles;
+  const int total = count_tiles(a.g, a.rows_per_tile, 1, 0, false, a.max_tiles);
   const int per_row = a.I / 8;
   for (int t = blockIdx.x; t < total; t += gridDim.x) {
-    const TileAt at = find_tile(a.g, a.rows_per_tile, 1, t);
+    const TileAt at = find_tile(a.g, a.rows_per_tile, 1, 0, false, t);
     if (at.group < 0) return;
     const int r0 = max(at.first, 0) * a.rows_per_tile;
     const int n = min(a.rows_per_tile, at.rows - r0);

@@ -242,9 +242,10 @@ def test_grouped_gemm_wgrad(name, N, K, gather):
 
 
 @pytest.mark.parametrize("gather", [False, True])
-def test_wgrad_large_tiles(gather):
-    """Enough tiles for the large tile: 64 groups of a few rows each, 264 x 272 weights (edges in both)."""
-    rows = [(7 * i) % 70 for i in range(64)]
+@pytest.mark.parametrize("most", [70, 400])
+def test_wgrad_large_tiles(most, gather):
+    """Enough tiles for the large tile: 64 groups of up to ``most`` rows, 264 x 272 weights (edges in both)."""
+    rows = [(37 * i) % most for i in range(64)]
     begin = np.cumsum([0] + rows[:-1]).tolist()
     total, N, K = sum(rows), 264, 272
     g = gen(5)
@@ -254,7 +255,7 @@ def test_wgrad_large_tiles(gather):
     want, mag = _wgrad_want(dy, x, rows, begin, index)
     dw = miep.grouped_gemm_wgrad(dy.to(DEV), x.to(DEV), groups_of(rows, begin),
                                  row_index=index.to(DEV) if gather else None)
-    close(dw, want, 71 * ULP * mag)
+    close(dw, want, (most + 1) * ULP * mag)
 
 
 def test_product_gradients_match_differences():
