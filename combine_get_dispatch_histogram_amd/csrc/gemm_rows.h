@@ -324,7 +324,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
       // wavefront holds the last operands of this step's buffers, and the next
       // step's first operands are read under the last MFMAs.
       constexpr int SLOTS = 2 * TP, D = TP < 3 ? TP : 3, RING = 4;
-      static_assert(SLOTS % RING == 0 && D < RING && TQ <= SLOTS - D && D <= TP, "operand ring");
+      static_assert(SLOTS % RING == 0 && D < RING && D <= TP, "operand ring");
       bf16x8 pf[RING], qf[2][TQ];
       auto read_q = [&](int h, uint32_t at, int j) MIEP_INLINE { qf[h][j] = lds_read<bf16x8>(at + qa[h] + j * 16 * kStepBytes); };
       auto read_p = [&](int k, uint32_t at) MIEP_INLINE {
@@ -535,10 +535,33 @@ hipError_t launch_rows_tile(GemmRowsArgs a, hipStream_t st) {
 template <int EL, bool PT, bool GATHER>
 hipError_t launch_rows(const GemmRowsArgs& a, hipStream_t st) {
   constexpr bool F8 = EL != kGemmBf16;
-  if (a.expected <= 32) return launch_rows_tile<EL, PT, GATHER, 128, 32, 4, 1, F8 ? 3 : 4, F8 ? 3 : 4>(a, st);
-  if (a.expected <= 64) return launch_rows_tile<EL, PT, GATHER, 128, 64, 2, 2, 3, 3>(a, st);
-  if (a.expected <= 128) return launch_rows_tile<EL, PT, GATHER, 256, 128, 4, 2, F8 ? 3 : 4, F8 ? 3 : 2>(a, st);
-  return launch_rows_tile<EL, PT, GATHER, 256, 256, 2, 4, F8 ? 2 : 3, 2>(a, st);
+  // Rows that most groups stay under when e are expected and chance spreads
+  // them (a binomial count's deviation is at most sqrt(e)).
+  int64_t e = a.expected, root = 0;
+  while ((root + 1) * (root + 1) <= e) ++root;
+  e += root;
+  // Measured in us on 8 experts of 4096 x 7168 weights unless said otherwise,
+  // bf16, tiles written channels x rows.
+  //   A few rows: the weights stream past them.  128 x 32, two workgroups a
+  //   CU, against 128 x 128: 16 rows 86 / 86, 4 rows 81 / 82, 16 rows of
+  //   7168 x 2048 37 / 38.5, E4M3 21.6 / 24.6.
+  if (e <= 24) return launch_rows_tile<EL, PT, GATHER, 128, 32, 4, 1, F8 ? 3 : 4, F8 ? 3 : 4>(a, st);
+  const int64_t wide = (a.NO + 255) / 256, narrow = (a.NO + 127) / 128;
+  if (a.g.G * wide * ((e + 255) / 256) >= 192) {
+    //   Enough tiles of 256 channels for the GPU's 256 CUs.  256 x 192 where
+    //   it takes no more row tiles than 256 x 256 (32 experts: 128 rows 359 /
+    //   378, 16 of 4096 x 2048 with 300 rows 88 / 126), else 256 x 256 (400
+    //   rows 881 / 757, 4096 rows 827 / 736).
+    if (e <= 192 || (e > 256 && e <= 384)) return launch_rows_tile<EL, PT, GATHER, 256, 192, 2, 4, 3, 2>(a, st);
+    return launch_rows_tile<EL, PT, GATHER, 256, 256, 2, 4, F8 ? 2 : 3, 2>(a, st);
+  }
+  //   Fewer: 128 channels, as many rows as a group needs: 128 x 128 / 192 /
+  //   256 at 64 rows 89 / - / 94, at 128 rows 151 / 107 / 110, at 180 rows
+  //   190 / 158 / 121.
+  if (e <= 108 || a.g.G * narrow * ((e + 127) / 128) <= 256)
+    return launch_rows_tile<EL, PT, GATHER, 128, 128, 2, 4, F8 ? 4 : 5, F8 ? 4 : 5>(a, st);
+  if (e <= 192) return launch_rows_tile<EL, PT, GATHER, 128, 192, 2, 4, F8 ? 3 : 4, F8 ? 3 : 4>(a, st);
+  return launch_rows_tile<EL, PT, GATHER, 128, 256, 2, 4, 3, 3>(a, st);
 }
 
 }  // namespace miep
