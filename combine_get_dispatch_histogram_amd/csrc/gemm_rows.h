@@ -32,9 +32,13 @@ struct RowsTile {
   static constexpr int kLds = NSP * kPBytes + NSQ * kQStage;
   static constexpr int kPLoads = kPBytes / 1024 / kWaves;            // a wavefront's loads of a step
   static constexpr int kQLoads = kQBytes / 1024 / kWaves + (kFp8 ? 1 : 0);
+  // Few results a wavefront (so registers to spare) and equally deep buffers:
+  // a whole step's operands are read a step ahead.
+  static constexpr bool kShort = kTP <= 4;
   // Loads that may be in flight behind the tile that a barrier publishes (see
   // `publish`): the buffers that are deeper than the two of every tile.
   static constexpr int kBehind = (NSP > NSQ ? NSQ - 1 : NSQ - 2) * kPLoads + (NSQ - 2) * kQLoads;
+  static_assert(!kShort || NSP == NSQ, "short steps load both operands at once");
   static_assert(kPLoads * kWaves * 1024 == kPBytes && kQBytes % (kWaves * 1024) == 0, "whole loads a wavefront");
   static_assert(kTP % 2 == 0 && kTQ >= 1 && NSQ >= 2 && NSP >= NSQ && kLds <= 163840, "tile shape");
   static_assert(kBehind + kPLoads + kQLoads < 64, "loads in flight");
@@ -273,11 +277,13 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
     // rows mostly come from L2.  Step t issues the loads of P's step t - 1 +
     // NSP, spread over its MFMAs, and behind its barrier those of Q's step t +
     // NSQ; before the first step come those that steps before it would have
-    // issued, in that order.
+    // issued, in that order.  (Short steps issue both behind the barrier, P's
+    // of step t + NSP.)
     auto issue_first = [&]() MIEP_INLINE {
 #pragma unroll
       for (int t = -NSP; t < 0; ++t) {
-        if (t - 1 + NSP >= 0) issue_p(t - 1 + NSP, t - 1 + NSP);
+        if constexpr (S::kShort) issue_p(t + NSP, t + NSP);
+        else if (t - 1 + NSP >= 0) issue_p(t - 1 + NSP, t - 1 + NSP);
         if (t + NSQ >= 0) issue_q(t + NSQ, t + NSQ);
       }
     };
@@ -294,7 +300,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
       for (int j = 0; j < TQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     const bool busy = wq * 16 * TQ < live;
     at = next_tile();
-    if (nk >= NSP) wait_tiles<S::kBehind + S::kQLoads>();
+    if (nk >= NSP) wait_tiles<S::kBehind + S::kQLoads + (S::kShort ? S::kPLoads : 0)>();
     else wait_tiles<0>();
     // The barrier of a step: the next step's tile has come (while the loads
     // behind it may be in flight; at the contraction's end there are fewer),
@@ -311,10 +317,121 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
     };
     if (!busy) {
       for (; step + 1 < nk; ++step) {
-        issue_p(step - 1 + NSP, before(pbuf));
+        if constexpr (!S::kShort) issue_p(step - 1 + NSP, before(pbuf));
         publish(step);
+        if constexpr (S::kShort) issue_p(step + NSP, pbuf);
         issue_q(step + NSQ, qbuf);
         next_buffers();
+      }
+    } else if constexpr (S::kShort) {
+      // All operands of a step (32 bytes a lane each: 64 bf16 channels in two
+      // halves, or 128 E4M3) are in registers when it begins; its barrier comes
+      // first, and the next step's operands are read under its MFMAs, into
+      // the other of two sets.
+      i32x8 pf[2][TP], qf[2][TQ];
+      float s[2][TQ];
+      int e[2][TQ], ep[2] = {0, 0};
+      auto read_p = [&](int set, int i, uint32_t at) MIEP_INLINE {
+        if constexpr (PT) {
+          struct { i16x4 v[4]; } t;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) t.v[r] = lds_read_tr(at + pa[i] + (r / 2 * 32 + r % 2 * 4) * 2 * BP);
+          pf[set][i] = __builtin_bit_cast(i32x8, t);
+        } else {
+          struct { i32x4 lo, hi; } t;
+          t.lo = lds_read<i32x4>(at + pa[0] + i * 16 * kStepBytes);
+          t.hi = lds_read<i32x4>(at + pa[1] + i * 16 * kStepBytes);
+          pf[set][i] = __builtin_bit_cast(i32x8, t);
+        }
+      };
+      auto read_q = [&](int set, int j, uint32_t at) MIEP_INLINE {
+        struct { i32x4 lo, hi; } t;
+        t.lo = lds_read<i32x4>(at + qa[0] + j * 16 * kStepBytes);
+        t.hi = lds_read<i32x4>(at + qa[1] + j * 16 * kStepBytes);
+        qf[set][j] = __builtin_bit_cast(i32x8, t);
+      };
+      auto read_scales = [&](int set, uint32_t at) MIEP_INLINE {
+        const uint32_t psat = at + S::kQBytes + S::kQScales * 4 + wp * 16 * TP / 128 * 4;
+        if constexpr (EL == kGemmFp8) {
+          const float sp = lds_read<float>(psat);
+#pragma unroll
+          for (int j = 0; j < TQ; ++j) s[set][j] = sp * lds_read<float>(at + S::kQBytes + ((wq * TQ + j) * 16 + m) * 4);
+        } else if constexpr (S::kFp8) {
+          ep[set] = lds_read<int>(psat);
+#pragma unroll
+          for (int j = 0; j < TQ; ++j) e[set][j] = lds_read<int>(at + S::kQBytes + ((wq * TQ + j) * 16 + m) * 4);
+        }
+      };
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) read_q(0, j, q_at(0));
+#pragma unroll
+      for (int i = 0; i < TP; ++i) read_p(0, i, p_at(0));
+      read_scales(0, q_at(0));
+      const int whole = nk - (ragged_end ? 1 : 0);                    // steps of 128 whole bytes
+      auto body = [&](auto parity, auto more, auto last) MIEP_INLINE {
+        constexpr int now = parity, then = 1 - parity;
+        const int pb = pbuf, qb = qbuf;
+        if constexpr (!last) publish(step);
+        if constexpr (!more && !last) {
+          issue_p(step + NSP, pb);
+          issue_q(step + NSQ, qb);
+        }
+        next_buffers();
+#pragma unroll
+        for (int i = 0; i < TP; ++i) {
+          if constexpr (!last) {
+            if (i == 0) read_scales(then, q_at(qbuf));
+#pragma unroll
+            for (int j = i * TQ / TP; j < (i + 1) * TQ / TP; ++j) read_q(then, j, q_at(qbuf));
+            read_p(then, i, p_at(pbuf));
+          }
+          if constexpr (more) {
+            constexpr int all = S::kPLoads + S::kQLoads;
+#pragma unroll
+            for (int l = i * all / TP; l < (i + 1) * all / TP; ++l) {
+              if (l < S::kQLoads) load_q(l, step + NSQ, qb);
+              else load_p(l - S::kQLoads, step + NSP, pb);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < TQ; ++j) {
+            if constexpr (EL == kGemmBf16) {
+              struct operand { bf16x8 lo, hi; };
+              const operand p = __builtin_bit_cast(operand, pf[now][i]), q = __builtin_bit_cast(operand, qf[now][j]);
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p.lo, q.lo, acc[i][j], 0, 0, 0);
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p.hi, q.hi, acc[i][j], 0, 0, 0);
+            } else if constexpr (EL == kGemmFp8) {
+              const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+              const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf[now][i], qf[now][j], z, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[r], s[now][j], acc[i][j][r]);
+            } else {
+              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf[now][i], qf[now][j], acc[i][j], 0, 0, 0, ep[now], 0, e[now][j]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < TQ; ++j) pin(acc[i][j]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        ++step;
+      };
+      constexpr std::true_type yes{};
+      constexpr std::false_type no{};
+      constexpr std::integral_constant<int, 0> even{};
+      constexpr std::integral_constant<int, 1> odd{};
+      while (step + 1 + NSP < whole) {
+        body(even, yes, no);
+        body(odd, yes, no);
+      }
+      while (step + 2 < nk) {
+        body(even, no, no);
+        body(odd, no, no);
+      }
+      if (step + 1 < nk) {
+        body(even, no, no);
+        body(odd, no, yes);
+      } else {
+        body(even, no, yes);
       }
     } else if constexpr (!S::kFp8) {
       // A step is 2 * TP slots: slot k multiplies P's operand k % TP of the
