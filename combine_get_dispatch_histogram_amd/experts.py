@@ -46,7 +46,7 @@ class RowGroups:
             raise ValueError("groups.rows must be [num_groups]")
         _want(self.begin, "groups.begin", torch.int32, tuple(self.rows.shape))
         rows, begin = a.p(self.rows), a.p(self.begin)
-        return _lib.RowGroupsC(begin.value if begin else None, rows.value, num_rows, self.rows.numel(), int(self.stride))
+        return _lib.RowGroupsC(begin, rows, num_rows, self.rows.numel(), int(self.stride))
 
 
 @dataclass
