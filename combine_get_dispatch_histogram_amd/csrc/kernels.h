@@ -265,6 +265,7 @@ constexpr int kMaxLocalExperts = 2048;   // LDS counters of one rank
 struct OrderArgs {
   int64_t rows;              // receive rows allocated
   int K, E, R, L, align, parts;
+  FastDiv Kdiv;              // set by the launcher
   int64_t slots;             // slots allocated
   const int64_t* topk;       // [rows][K] local expert of each entry, or -1
   const int32_t* off;        // [R+1]

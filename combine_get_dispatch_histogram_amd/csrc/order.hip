@@ -13,7 +13,12 @@
 
 namespace miep {
 
-constexpr int kOrderWaves = 4;
+constexpr int kOrderWaves = 8;                 // wavefronts of a part in the placing kernel
+constexpr int kOrderThreads = kOrderWaves * kWave;
+// A lane keeps this many entries in registers: their loads are in flight
+// together, and a wavefront whose share fits reads it only once (one load at a
+// time, twice, the placing of 16384 tokens' top-8 over 64 ranks took 15.6 us).
+constexpr int kOrderHold = 8;
 
 // Rows [first, last) of part p of rank r, inside the allocated rows whatever
 // the offsets hold.
@@ -25,66 +30,85 @@ __device__ __forceinline__ void part_rows(const OrderArgs& a, int r, int p, int6
   *last = lo + (hi - lo) * (p + 1) / a.parts;
 }
 
-__global__ __launch_bounds__(256) void order_count_kernel(OrderArgs a) {
+// Entries i0 + lane, + 64, ...: the lane's local experts of kOrderHold of them, -1
+// where there is none.
+__device__ __forceinline__ void hold(const OrderArgs& a, int64_t i0, int64_t i1, int step, int (&e)[kOrderHold]) {
+  int64_t v[kOrderHold];
+#pragma unroll
+  for (int k = 0; k < kOrderHold; ++k) {
+    v[k] = -1;
+    if (i0 + k * step < i1) v[k] = a.topk[i0 + k * step];
+  }
+#pragma unroll
+  for (int k = 0; k < kOrderHold; ++k) e[k] = v[k] >= 0 && v[k] < a.L ? static_cast<int>(v[k]) : -1;
+}
+
+__global__ __launch_bounds__(kOrderThreads) void order_count_kernel(OrderArgs a) {
   __shared__ int count[kMaxLocalExperts];
   const int r = blockIdx.x / a.parts, p = blockIdx.x - r * a.parts;
-  for (int l = threadIdx.x; l < a.L; l += 256) count[l] = 0;
+  for (int l = threadIdx.x; l < a.L; l += kOrderThreads) count[l] = 0;
   __syncthreads();
   int64_t first, last;
   part_rows(a, r, p, &first, &last);
-  for (int64_t i = first * a.K + threadIdx.x; i < last * a.K; i += 256) {
-    const int64_t e = a.topk[i];
-    if (e >= 0 && e < a.L) atomicAdd(&count[e], 1);
+  for (int64_t i = first * a.K + threadIdx.x; i < last * a.K; i += kOrderHold * kOrderThreads) {
+    int e[kOrderHold];
+    hold(a, i, last * a.K, kOrderThreads, e);
+#pragma unroll
+    for (int k = 0; k < kOrderHold; ++k)
+      if (e[k] >= 0) atomicAdd(&count[e[k]], 1);
   }
   __syncthreads();
   int32_t* out = a.counts + static_cast<int64_t>(p) * a.E + r * a.L;
-  for (int l = threadIdx.x; l < a.L; l += 256) out[l] = count[l];
+  for (int l = threadIdx.x; l < a.L; l += kOrderThreads) out[l] = count[l];
 }
 
-__global__ __launch_bounds__(256) void order_place_kernel(OrderArgs a) {
+__global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs a) {
   __shared__ int next[kOrderWaves][kMaxLocalExperts];   // each wavefront's next slot per expert
-  __shared__ int sums[256], waves[kOrderWaves];
+  __shared__ int sums[512], waves[kOrderWaves];
   const int tid = threadIdx.x, lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r = blockIdx.x / a.parts, p = blockIdx.x - r * a.parts;
   int64_t first, last;
   part_rows(a, r, p, &first, &last);
-  // this wavefront's entries
+  // this wavefront's entries, in blocks of what its lanes hold
+  constexpr int kBlock = kOrderHold * kWave;
   const int64_t entries = (last - first) * a.K;
   const int64_t i0 = first * a.K + entries * wave / kOrderWaves, i1 = first * a.K + entries * (wave + 1) / kOrderWaves;
+  int held[kOrderHold];
+  hold(a, i0 + lane, i1, kWave, held);
 
-  for (int l = tid; l < kOrderWaves * a.L; l += 256) next[l / a.L][l % a.L] = 0;
+  for (int l = tid; l < kOrderWaves * a.L; l += kOrderThreads) next[l / a.L][l % a.L] = 0;
   __syncthreads();
-  for (int64_t i = i0 + lane; i < i1; i += kWave) {
-    const int64_t e = a.topk[i];
-    if (e >= 0 && e < a.L) atomicAdd(&next[wave][e], 1);
+  for (int64_t i = i0; i < i1; i += kBlock) {
+    if (i != i0) hold(a, i + lane, i1, kWave, held);
+#pragma unroll
+    for (int k = 0; k < kOrderHold; ++k)
+      if (held[k] >= 0) atomicAdd(&next[wave][held[k]], 1);
   }
   __syncthreads();
 
-  // first slots: prefix of the experts' aligned totals, 256 experts at a time
-  // (fewer experts: several threads add up the parts of one)
+  // first slots: prefix of the experts' aligned totals, 512 experts at a time
+  // (up to 256 experts: several threads add up the parts of one)
   int64_t slots = 0;
-  int width = 256;
+  int width = kOrderThreads;
   while (width / 2 >= a.E) width /= 2;
-  for (int e0 = 0; e0 < a.E; e0 += 256) {
+  for (int e0 = 0; e0 < a.E; e0 += kOrderThreads) {
     const int e = e0 + (tid & (width - 1));
     int all = 0, before = 0;
     if (e < a.E)
-      for (int q = tid / width; q < a.parts; q += 256 / width) {
+      for (int q = tid / width; q < a.parts; q += kOrderThreads / width) {
         const int c = a.counts[static_cast<int64_t>(q) * a.E + e];
         all += c;
         before += q < p ? c : 0;
       }
-    if (width < 256) {
-      __syncthreads();
-      if (tid < width) sums[tid] = 0;
-      if (tid >= 128 && width <= 128) sums[tid] = 0;
+    if (width < kOrderThreads) {
+      sums[tid] = 0;
       __syncthreads();
       atomicAdd(&sums[tid & (width - 1)], all);
-      atomicAdd(&sums[128 + (tid & (width - 1))], before);
+      atomicAdd(&sums[256 + (tid & (width - 1))], before);
       __syncthreads();
       all = tid < width ? sums[tid] : 0;
-      before = tid < width ? sums[128 + tid] : 0;
+      before = tid < width ? sums[256 + tid] : 0;
     }
     const bool mine = e < a.E && tid < width;
     const int padded = mine ? (all + a.align - 1) / a.align * a.align : 0;
@@ -119,45 +143,49 @@ __global__ __launch_bounds__(256) void order_place_kernel(OrderArgs a) {
 
   int bits = 0;
   while ((1 << bits) < a.L) ++bits;
-  for (int64_t i = i0; i < i1; i += kWave) {
-    const bool in = i + lane < i1;
-    const int64_t e64 = in ? a.topk[i + lane] : -1;
-    const bool named = e64 >= 0 && e64 < a.L;
-    const int e = named ? static_cast<int>(e64) : 0;
-    uint64_t same = ballot(named);
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t set = ballot((e >> b) & 1);
-      same &= ((e >> b) & 1) ? set : ~set;
+  for (int64_t i = i0; i < i1; i += kBlock) {
+    if (i1 - i0 > kBlock) hold(a, i + lane, i1, kWave, held);         // longer shares: read again
+#pragma unroll
+    for (int k = 0; k < kOrderHold; ++k) {
+      const int64_t n = i + k * kWave + lane;
+      if (n - lane >= i1) break;
+      const int e = max(held[k], 0);
+      uint64_t same = ballot(held[k] >= 0);
+      for (int b = 0; b < bits; ++b) {
+        const uint64_t set = ballot((e >> b) & 1);
+        same &= ((e >> b) & 1) ? set : ~set;
+      }
+      int slot = -1;
+      if (held[k] >= 0) {
+        slot = next[wave][e] + __popcll(same & lanemask_lt());
+        if ((same >> lane) == 1) next[wave][e] = slot + 1;            // the last of the equal ones
+        if (slot < a.slots) a.slot_row[slot] = fdiv(static_cast<int>(n), a.Kdiv);
+        else slot = -1;
+      }
+      if (n < i1) a.row_slot[n] = slot;
     }
-    int slot = -1;
-    if (named) {
-      const int base = next[wave][e];
-      slot = base + __popcll(same & lanemask_lt());
-      if ((same >> lane) == 1) next[wave][e] = slot + 1;              // the last of the equal ones
-      if (slot < a.slots) a.slot_row[slot] = static_cast<int>((i + lane) / a.K);
-      else slot = -1;
-    }
-    if (in) a.row_slot[i + lane] = slot;
   }
 
   // slots behind the last expert's, and rows behind the last received one
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
-  for (int64_t s = slots + blockIdx.x * 256ll + tid; s < a.slots; s += step) a.slot_row[s] = -1;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kOrderThreads;
+  for (int64_t s = slots + blockIdx.x * static_cast<int64_t>(kOrderThreads) + tid; s < a.slots; s += step) a.slot_row[s] = -1;
   int64_t end = a.off[a.R];
   end = end < 0 ? 0 : end > a.rows ? a.rows : end;
-  for (int64_t i = end * a.K + blockIdx.x * 256ll + tid; i < a.rows * a.K; i += step) a.row_slot[i] = -1;
+  for (int64_t i = end * a.K + blockIdx.x * static_cast<int64_t>(kOrderThreads) + tid; i < a.rows * a.K; i += step) a.row_slot[i] = -1;
   if (a.status && blockIdx.x == 0 && tid == 0) *a.status = slots > a.slots ? kStatusCapacity : 0;
 }
 
 hipError_t launch_order(const OrderArgs& args, hipStream_t st) {
   OrderArgs a = args;
-  // a part is worth about 2048 entries (8 a lane): fewer leave more to sum up than to sort
-  const int64_t want = (a.rows * a.K / a.R + 2047) / 2048;
+  a.Kdiv = make_fastdiv(a.K);                                        // entries stay below 2^31, K <= 64
+  // a part is worth the entries that its lanes hold: fewer leave more to sum up than to sort
+  constexpr int kPart = kOrderHold * kOrderThreads;
+  const int64_t want = (a.rows * a.K / a.R + kPart - 1) / kPart;
   if (want < a.parts) a.parts = want < 1 ? 1 : static_cast<int>(want);
   const int64_t grid = static_cast<int64_t>(a.parts) * a.R;
-  if (grid > max_blocks(256)) return hipErrorInvalidConfiguration;
-  order_count_kernel<<<static_cast<unsigned>(grid), 256, 0, st>>>(a);
-  order_place_kernel<<<static_cast<unsigned>(grid), 256, 0, st>>>(a);
+  if (grid > max_blocks(kOrderThreads)) return hipErrorInvalidConfiguration;
+  order_count_kernel<<<static_cast<unsigned>(grid), kOrderThreads, 0, st>>>(a);
+  order_place_kernel<<<static_cast<unsigned>(grid), kOrderThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -218,9 +246,20 @@ __global__ __launch_bounds__(256) void reduce_kernel(ReduceArgs a) {
   }
 }
 
+// 16 bytes of rows that are used once.
+__device__ __forceinline__ v4u ld16_once(const void* p) {
+  const u32x4 t = __builtin_nontemporal_load(static_cast<const u32x4*>(p));
+  return v4u{t.x, t.y, t.z, t.w};
+}
+__device__ __forceinline__ void st16_once(void* p, const v4u& v) {
+  const u32x4 t = {v.x, v.y, v.z, v.w};
+  __builtin_nontemporal_store(t, static_cast<u32x4*>(p));
+}
+
 // Gradient: dz[slot(row, k)] = w[row][k] * dy[row], dw[row][k] = <dy[row],
 // z[slot(row, k)]>.  Eight entries at a time share one read of dy's row; the
 // dot products are summed over lanes, then wavefronts, in a fixed order.
+template <bool STREAM>
 __global__ __launch_bounds__(256) void reduce_backward_kernel(ReduceArgs a) {
   constexpr int NB = 8;
   __shared__ float part[4][NB];
@@ -266,7 +305,7 @@ __global__ __launch_bounds__(256) void reduce_backward_kernel(ReduceArgs a) {
         if (a.dw) {
 #pragma unroll
           for (int q = 0; q < NB; ++q)
-            if (q < n) d[q] = ld16(a.z + at[q] + v * 8);
+            if (q < n) d[q] = STREAM ? ld16_once(a.z + at[q] + v * 8) : ld16(a.z + at[q] + v * 8);
         }
 #pragma unroll
         for (int q = 0; q < NB; ++q)
@@ -274,7 +313,8 @@ __global__ __launch_bounds__(256) void reduce_backward_kernel(ReduceArgs a) {
             float o[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[k] = g[q] * dy[k];
-            *reinterpret_cast<v4u*>(a.out + at[q] + v * 8) = narrow(o);
+            if constexpr (STREAM) st16_once(a.out + at[q] + v * 8, narrow(o));
+            else *reinterpret_cast<v4u*>(a.out + at[q] + v * 8) = narrow(o);
             if (a.dw) {
               float f[8];
               widen(d[q], f);
@@ -312,7 +352,10 @@ hipError_t launch_reduce(const ReduceArgs& a, hipStream_t st) {
 hipError_t launch_reduce_backward(const ReduceArgs& a, hipStream_t st) {
   if (a.rows == 0) return hipSuccess;
   const unsigned grid = static_cast<unsigned>(a.rows < 65536 ? a.rows : 65536);
-  reduce_backward_kernel<<<grid, 256, 0, st>>>(a);
+  // Slots of half the 256 MiB last-level cache or more pass it by (32768 slots
+  // of 7168: 203 -> 187 us).
+  if (2 * a.slots * a.H >= (128ll << 20)) reduce_backward_kernel<true><<<grid, 256, 0, st>>>(a);
+  else reduce_backward_kernel<false><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -646,3 +646,110 @@ def test_expert_reduce_and_backward(H, K, weighted):
         e[5, 0] = 1e-3
         f = lambda v: float((zz * v.unsqueeze(2)).sum(1)[:n].mul(dy[:n].double()).sum())  # noqa: E731
         assert abs((f(w64 + e) - f(w64 - e)) / 2e-3 - float(prod.sum(2)[5, 0])) < 1e-6
+
+
+# ------------------------------------------------------------------ results that pass the caches by (128 MiB and more)
+def test_large_swiglu_and_its_gradient():
+    rows, I = 8200, 8200
+    g = torch.Generator(device=DEV).manual_seed(4)
+    h = torch.randn((rows, 2 * I), generator=g, device=DEV).to(BF)
+    da = torch.randn((rows, I), generator=g, device=DEV).to(BF)
+    grp = groups_of([8000, 0, 150], [0, 9, 8010])
+    a = torch.full((rows, I), MARK, dtype=BF, device=DEV)
+    dh = torch.full((rows, 2 * I), MARK, dtype=BF, device=DEV)
+    miep.swiglu_into(h, grp, a)
+    miep.swiglu_backward_into(da, h, grp, dh)
+    at = [0, 1, 77, 4095, 7999, 8010, 8159]
+    want = swiglu64(h[at].cpu())
+    gate, up = factors(h[at].cpu())
+    close(a[at], want, (BF_HALF + SIG) * want.abs() + TINY * (1 + gate * up))
+    hd, d = h[at].cpu().double(), da[at].cpu().double()
+    s = torch.sigmoid(hd[:, :I])
+    dup = d * hd[:, :I] * s
+    close(dh[at][:, I:], dup, (BF_HALF + SIG) * dup.abs() + TINY * (1 + d.abs() * gate), "up")
+    dgate = d * hd[:, I:] * s * (1 + hd[:, :I] * (1 - s))
+    close(dh[at][:, :I], dgate, BF_HALF * dgate.abs() + d.abs() * up * s * (2 + gate) * SIG + TINY * (1 + d.abs() * up * (1 + gate)), "gate")
+    out = [8000, 8009, 8160, 8199]
+    assert bool((a[out] == MARK).all()) and bool((dh[out] == MARK).all())
+
+
+def test_large_reduce_backward():
+    cap, K, H = 4200, 4, 8200
+    g = torch.Generator(device=DEV).manual_seed(6)
+    topk = torch.randint(0, 8, (cap, K), generator=g, device=DEV)
+    order = miep.expert_order(topk, i32([0, cap - 3]), 8)
+    z = torch.randn((order.num_slots, H), generator=g, device=DEV).to(BF)
+    dy = torch.randn((cap, H), generator=g, device=DEV).to(BF)
+    w = torch.rand((cap, K), generator=g, device=DEV)
+    dz, dw = torch.full_like(z, MARK), torch.full_like(w, MARK)
+    miep.expert_reduce_backward_into(dy, z, order, dz, w, dw)
+    rs = order.row_slot.cpu().long()
+    for r in (0, 1, 2000, cap - 4):
+        want = d64(dy[r]) * d64(w[r]).unsqueeze(1)
+        close(dz[rs[r]], want, (BF_HALF + ULP) * want.abs())
+        prod = d64(z[rs[r]]) * d64(dy[r])
+        close(dw[r], prod.sum(1), (H + 8) * ULP * prod.abs().sum(1))
+    assert bool((dw[cap - 3:] == MARK).all())
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+def test_rows_past_four_gigabytes():
+    """Source rows and results whose byte offsets pass 2^32, and an E4M3 source as large."""
+    K, rows = 8192, 270000
+    g = torch.Generator(device=DEV).manual_seed(8)
+    x = torch.zeros((rows, K), dtype=BF, device=DEV)          # 4.4 GB
+    at = [0, 131071, 262144, 269999]
+    x[at] = torch.randn((4, K), generator=g, device=DEV).to(BF)
+    w = torch.randn((2, 16, K), generator=g, device=DEV).to(BF)
+    xs, ws = x[at].cpu().double(), w.cpu().double()
+    tol = lambda a, b: BF_HALF * (a @ b.T).abs() + K * ULP * (a.abs() @ b.abs().T)  # noqa: E731
+    y = miep.grouped_gemm(x, w, groups_of([3, 1], [0, 3]), row_index=i32([at[3], at[2], at[1], at[3]]))
+    close(y[:3], xs[[3, 2, 1]] @ ws[0].T, tol(xs[[3, 2, 1]], ws[0]))
+    close(y[3:], xs[[3]] @ ws[1].T, tol(xs[[3]], ws[1]))
+    y = torch.full((rows, 16), MARK, dtype=BF, device=DEV)
+    miep.grouped_gemm_into(x, w, groups_of([1, 2], [262144, 269998]), y, expected_rows=2)
+    close(y[[262144, 269999]], torch.cat([xs[[2]] @ ws[0].T, xs[[3]] @ ws[1].T]), torch.cat([tol(xs[[2]], ws[0]), tol(xs[[3]], ws[1])]))
+    assert bool((y[:262144] == MARK).all())
+    dy = torch.randn((rows, 16), generator=g, device=DEV).to(BF)
+    miep.grouped_gemm_dgrad_into(dy, w, groups_of([1, 2], [262144, 269998]), x, expected_rows=2)
+    ds = dy[[262144, 269999]].cpu().double()
+    want = torch.cat([ds[:1] @ ws[0], ds[1:] @ ws[1]])
+    close(x[[262144, 269999]], want, BF_HALF * want.abs() + 16 * ULP * torch.cat([ds[:1].abs() @ ws[0].abs(), ds[1:].abs() @ ws[1].abs()]))
+    dw = miep.grouped_gemm_wgrad(dy, x, groups_of([1, 2], [262144, 269998]))
+    d, v = dy[269998:].cpu().double(), x[269998:].cpu().double()
+    close(dw[1], d.T @ v, 3 * ULP * (d.abs().T @ v.abs()))
+
+
+# ------------------------------------------------------------------ the same results every time, on any stream
+def _problem(seed=0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rows, begin, total = layout("ragged")
+    x = torch.randn((total, 264), generator=g, device=DEV).to(BF)
+    w = torch.randn((len(rows), 136, 264), generator=g, device=DEV).to(BF)
+    dy = torch.randn((total, 136), generator=g, device=DEV).to(BF)
+    return groups_of(rows, begin), x, w, dy
+
+
+def test_results_do_not_depend_on_timing():
+    grp, x, w, dy = _problem()
+    live = members(*layout("ragged")).to(DEV)
+    first = [miep.grouped_gemm(x, w, grp)[live], miep.grouped_gemm_dgrad(dy, w, grp)[live], miep.grouped_gemm_wgrad(dy, x, grp)]
+    for _ in range(20):
+        again = [miep.grouped_gemm(x, w, grp)[live], miep.grouped_gemm_dgrad(dy, w, grp)[live], miep.grouped_gemm_wgrad(dy, x, grp)]
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def test_two_streams_at_once():
+    problems = [_problem(s) for s in (1, 2)]
+    live = members(*layout("ragged")).to(DEV)
+    want = [miep.grouped_gemm(x, w, grp)[live] for grp, x, w, _ in problems]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(DEV) for _ in problems]
+    outs = [[], []]
+    for _ in range(10):
+        for i, (st, (grp, x, w, dy)) in enumerate(zip(streams, problems)):
+            with torch.cuda.stream(st):
+                outs[i].append(miep.grouped_gemm(x, w, grp))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y[live], want[i]) for y in outs[i])
