@@ -295,6 +295,160 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
   }
 }
 
+// Few tiles under many rows: the rows are split.  A workgroup computes 64 x 64
+// of dW; its 8 wavefronts take every eighth step of 32 rows each, through
+// buffers of their own (so without barriers), and their sums are added up in
+// wavefront order in LDS at the end.
+struct SplitTile {
+  static constexpr int kRows = 32, kWaves = 8, kSide = 64, kT = kSide / 16;
+  static constexpr int kBytes = kSide * 2 * kRows;                   // of one operand's step
+  static constexpr int kLoads = kBytes / 1024;
+  static constexpr int kPitch = kSide + 4;                           // of a wavefront's sums, floats: rows in different banks
+  static constexpr int kSums = kSide * kPitch * 4;
+  static constexpr int kLds = kWaves * (kSums > 4 * kBytes ? kSums : 4 * kBytes);
+  static_assert(kLds <= 163840, "buffers");
+};
+
+// Rows of 128 bytes: the 8 rows of a half wavefront's transposing read (0-3 and
+// 8-11) differ in parity, bit 1 and bit 3.
+__device__ __forceinline__ int swz_t64(int row) { return (((row >> 1) & 1) | ((row >> 2) & 2)) << 1; }
+
+template <bool GATHER, bool F32>
+__global__ __launch_bounds__(512, 2) void gemm_weight_split_kernel(GemmWeightArgs a) {
+  using S = SplitTile;
+  __shared__ __align__(1024) uint8_t lds_mem[S::kLds];
+  const uint32_t lds = (uint32_t)(uintptr_t)(lds_byte*)lds_mem;
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+  const int m = lane & 15, quarter = lane >> 4;
+  const int ptiles = (a.K + S::kSide - 1) / S::kSide, qtiles = (a.N + S::kSide - 1) / S::kSide;
+  const int group = blockIdx.x / (ptiles * qtiles), tile = blockIdx.x - group * (ptiles * qtiles);
+  const int q0 = tile / ptiles * S::kSide, p0 = tile % ptiles * S::kSide;
+
+  int64_t begin;
+  int rows;
+  group_range(a.g, group, &begin, &rows);
+  begin = (static_cast<int64_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(begin >> 32))) << 32) |
+          static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(begin)));
+  rows = __builtin_amdgcn_readfirstlane(rows);
+  if (rows == 0 && a.accumulate) return;
+
+  const int64_t ldq = 2 * static_cast<int64_t>(a.N), ldp = 2 * static_cast<int64_t>(a.K);
+  const uint8_t* qbase = reinterpret_cast<const uint8_t*>(a.q) + begin * ldq + 2 * static_cast<int64_t>(q0);
+  const uint8_t* pbase = reinterpret_cast<const uint8_t*>(a.p) + (GATHER ? 0 : begin * ldp) + 2 * static_cast<int64_t>(p0);
+  const uint32_t mine = lds + wave * 4 * S::kBytes;                  // [buffer][P, Q]
+  int src[GATHER ? S::kLoads : 1];
+  auto sources = [&](int step) MIEP_INLINE {
+    if constexpr (GATHER) {
+#pragma unroll
+      for (int i = 0; i < S::kLoads; ++i) {
+        const int r = step * S::kRows + i * 8 + lane / 8;
+        src[i] = r < rows ? a.row_index[begin + r] : -1;
+      }
+    }
+  };
+  auto issue = [&](int step, int buf) MIEP_INLINE {
+#pragma unroll
+    for (int i = 0; i < S::kLoads; ++i) {
+      const int row = i * 8 + lane / 8, r = step * S::kRows + row;
+      int pc = ((lane & 7) ^ swz_t64(row)) * 16, qc = pc;
+      if (p0 + pc / 2 >= a.K) pc = 0;
+      if (q0 + qc / 2 >= a.N) qc = 0;
+      bool in = r < rows;
+      const uint8_t* q = qbase + r * ldq + qc;
+      dma16(in ? static_cast<const void*>(q) : static_cast<const void*>(g_zero16), mine + (2 * buf + 1) * S::kBytes + i * 1024);
+      const uint8_t* p;
+      if constexpr (GATHER) {
+        in = in && src[i] >= 0 && src[i] < a.p_rows;
+        p = pbase + src[i] * ldp + pc;
+      } else {
+        p = pbase + r * ldp + pc;
+      }
+      dma16(in ? static_cast<const void*>(p) : static_cast<const void*>(g_zero16), mine + 2 * buf * S::kBytes + i * 1024);
+    }
+  };
+
+  f32x4 acc[S::kT][S::kT];
+#pragma unroll
+  for (int i = 0; i < S::kT; ++i)
+#pragma unroll
+    for (int j = 0; j < S::kT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  uint32_t at[S::kT];
+  {
+    const int row = quarter * 8 + m / 4;
+#pragma unroll
+    for (int i = 0; i < S::kT; ++i) at[i] = row * 128 + ((i * 2 + (m & 3) / 2) ^ swz_t64(row)) * 16 + (m & 1) * 8;
+  }
+  auto operand = [&](uint32_t from) MIEP_INLINE {
+    struct { i16x4 lo, hi; } t;
+    t.lo = lds_read_tr(from);
+    t.hi = lds_read_tr(from + 4 * 128);
+    return __builtin_bit_cast(bf16x8, t);
+  };
+
+  const int nk = (rows + S::kRows - 1) / S::kRows;
+  int buf = 0;
+  if (wave < nk) {
+    sources(wave);
+    issue(wave, 0);
+    sources(wave + S::kWaves);
+  }
+  for (int step = wave; step < nk; step += S::kWaves, buf ^= 1) {
+    if (step + S::kWaves < nk) {
+      issue(step + S::kWaves, buf ^ 1);
+      sources(step + 2 * S::kWaves);
+      // (gathered: the sources' own loads are behind these, so all have come when they are used)
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * S::kLoads) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    bf16x8 pf[S::kT], qf[S::kT];
+#pragma unroll
+    for (int i = 0; i < S::kT; ++i) {
+      pf[i] = operand(mine + 2 * buf * S::kBytes + at[i]);
+      qf[i] = operand(mine + (2 * buf + 1) * S::kBytes + at[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < S::kT; ++i)
+#pragma unroll
+      for (int j = 0; j < S::kT; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[i], qf[j], acc[i][j], 0, 0, 0);
+    // the operands have left this buffer before the next turn loads into it
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+
+  all_read();
+  float* sums = reinterpret_cast<float*>(lds_mem);
+#pragma unroll
+  for (int j = 0; j < S::kT; ++j)
+#pragma unroll
+    for (int i = 0; i < S::kT; ++i)
+      *reinterpret_cast<f32x4*>(sums + wave * (S::kSums / 4) + (j * 16 + m) * S::kPitch + i * 16 + quarter * 4) = acc[i][j];
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int x = threadIdx.x + h * 512, n = x / 16, k = x % 16 * 4;
+    f32x4 v = *reinterpret_cast<const f32x4*>(sums + n * S::kPitch + k);
+#pragma unroll
+    for (int w = 1; w < S::kWaves; ++w) {
+      const f32x4 u = *reinterpret_cast<const f32x4*>(sums + w * (S::kSums / 4) + n * S::kPitch + k);
+      v = f32x4{v[0] + u[0], v[1] + u[1], v[2] + u[2], v[3] + u[3]};
+    }
+    if (q0 + n >= a.N || p0 + k >= a.K) continue;
+    const int64_t o = (static_cast<int64_t>(group) * a.N + q0 + n) * a.K + p0 + k;
+    if constexpr (F32) {
+      f32x4* to = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o);
+      if (a.accumulate) {
+        const f32x4 old = *to;
+        v = f32x4{old[0] + v[0], old[1] + v[1], old[2] + v[2], old[3] + v[3]};
+      }
+      *to = v;
+    } else {
+      *reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.out) + o) = v2u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    }
+  }
+}
+
 template <bool GATHER, bool F32, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
 hipError_t launch_weight_tile(const GemmWeightArgs& a, hipStream_t st) {
   const int64_t per_group = static_cast<int64_t>((a.K + BP - 1) / BP) * ((a.N + BQ - 1) / BQ);
@@ -307,6 +461,14 @@ hipError_t launch_weight_tile(const GemmWeightArgs& a, hipStream_t st) {
 template <bool GATHER, bool F32>
 hipError_t launch_weight(const GemmWeightArgs& a, hipStream_t st) {
   const int64_t big = static_cast<int64_t>((a.K + 255) / 256) * ((a.N + 255) / 256) * a.g.G;
+  const int64_t small = static_cast<int64_t>((a.K + 63) / 64) * ((a.N + 63) / 64) * a.g.G;
+  // Splitting the rows: 8000 rows of 512 x 512 89 -> 35 us, of 1024 x 1024 92
+  // -> 37; but of 2048 x 2048 103 -> 118, 8 groups of 1000 of 512 x 512 18.5
+  // -> 20, and 500 rows of 512 x 512 the same 11.
+  if (small <= 256 && a.g.limit / a.g.G >= 512) {
+    gemm_weight_split_kernel<GATHER, F32><<<static_cast<unsigned>(small), 512, 0, st>>>(a);
+    return hipGetLastError();
+  }
   if (big < 256) return launch_weight_tile<GATHER, F32, 128, 128, 2, 2, 2, 2>(a, st);
   return launch_weight_tile<GATHER, F32, 256, 256, 2, 4, GATHER ? 2 : 3, 2>(a, st);
 }

@@ -258,6 +258,28 @@ def test_wgrad_large_tiles(most, gather):
     close(dw, want, (most + 1) * ULP * mag)
 
 
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("N,K", [(8, 8), (136, 72), (192, 520)])
+def test_wgrad_of_many_rows(N, K, gather):
+    """Many rows under few tiles: the rows are split over wavefronts; groups of none, one, a few and many steps."""
+    say("wgrad split", N, K, gather)
+    rows = [0, 2600, 1, 33, 0, 1217]
+    begin = np.cumsum([0] + rows[:-1]).tolist()
+    total = sum(rows) + 5
+    g = gen(N * K)
+    dy = poison(torch.randn((total, N), generator=g), members(rows, begin, total)).to(BF)
+    x = torch.randn((900, K) if gather else (total, K), generator=g).to(BF)
+    index = torch.randint(-1, 901, (total,), generator=g, dtype=torch.int32) if gather else None
+    want, mag = _wgrad_want(dy, x, rows, begin, index)
+    grp, kw = groups_of(rows, begin), dict(row_index=index.to(DEV)) if gather else {}
+    close(miep.grouped_gemm_wgrad(dy.to(DEV), x.to(DEV), grp, **kw), want, 2601 * ULP * mag)
+    close(miep.grouped_gemm_wgrad(dy.to(DEV), x.to(DEV), grp, dtype=BF, **kw), want, BF_HALF * want.abs() + 2 * 2601 * ULP * mag)
+    old = torch.randn(want.shape, generator=g)
+    acc = old.to(DEV)
+    miep.grouped_gemm_wgrad_into(dy.to(DEV), x.to(DEV), grp, acc, accumulate=True, **kw)
+    close(acc, want + old.double(), 2602 * ULP * (mag + old.double().abs()))
+
+
 def test_product_gradients_match_differences():
     """The formulas the gradients are held to, against central differences of the 64-bit product (linear: exact)."""
     g = gen(9)
