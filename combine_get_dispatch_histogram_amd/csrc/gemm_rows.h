@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "gemm.h"
+#include "gemm_rows_split.h"
 
 namespace miep {
 
@@ -652,6 +653,12 @@ hipError_t launch_rows_tile(GemmRowsArgs a, hipStream_t st) {
 template <int EL, bool PT, bool GATHER>
 hipError_t launch_rows(const GemmRowsArgs& a, hipStream_t st) {
   constexpr bool F8 = EL != kGemmBf16;
+  // Few tiles over a long contraction: split it (bf16, us against the tiles
+  // below: 16 rows of 1 x 4096 x 7168 28 -> 15, 100 rows of 1 x 256 x 7168 46 ->
+  // 13, 16 rows of 2 x 4096 x 7168 28 -> 22; of 4 x 4096 x 7168 37 -> 38, and
+  // 16 steps only, 100 rows of 1 x 256 x 1024, 13 -> 14.5).
+  const int64_t tiles32 = a.g.G * ((static_cast<int64_t>(a.expected) + 31) / 32) * ((a.NO + 31) / 32);
+  if (tiles32 <= 256 && a.C / (F8 ? 128 : 64) >= 24) return launch_rows_split<EL, PT, GATHER>(a, st);
   // Rows that most groups stay under when e are expected and chance spreads
   // them (a binomial count's deviation is at most sqrt(e)).
   int64_t e = a.expected, root = 0;

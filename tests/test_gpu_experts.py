@@ -405,6 +405,45 @@ def test_every_tile(kind, expected):
         close(y[b:b + n], want, fp8_tol(want, mag, K), "group %d" % i)
 
 
+@pytest.mark.parametrize("rows", [[1], [0, 33, 5], [70, 0, 1, 32]])
+@pytest.mark.parametrize("kind", ["gemm", "gather", "dgrad", "fp8", "fp8 gather", "ue8m0", "ue8m0 gather"])
+def test_few_tiles_over_a_long_contraction(kind, rows):
+    """The contraction split over wavefronts: more than 24 steps of it, the last one short where the type allows."""
+    say("split", kind, rows)
+    begin = np.cumsum([1] + [n + 2 for n in rows])[:-1].tolist()
+    total, G, N = begin[-1] + rows[-1] + 3, len(rows), 72
+    g, live, grp = gen(len(kind)), members(rows, begin, total), groups_of(rows, begin)
+    gather = "gather" in kind
+    src = 50 if gather else total
+    index = torch.randint(-1, src + 1, (total,), generator=g, dtype=torch.int32) if gather else None
+    kw = dict(row_index=index.to(DEV)) if gather else {}
+    y = torch.full((total, N), MARK, dtype=BF, device=DEV)
+    if kind in ("gemm", "gather", "dgrad"):
+        K = 1608
+        x = torch.randn((src, K), generator=g)
+        x = (x if gather else poison(x, live)).to(BF)
+        w = torch.randn((G, K, N) if kind == "dgrad" else (G, N, K), generator=g).to(BF)
+        if kind == "dgrad":
+            miep.grouped_gemm_dgrad_into(x.to(DEV), w.to(DEV), grp, y, expected_rows=4)
+        else:
+            miep.grouped_gemm_into(x.to(DEV), w.to(DEV), grp, y, expected_rows=4, **kw)
+        xd, wd = x.double(), [(t if kind == "dgrad" else t.T).double() for t in w]
+    else:
+        K, pow2 = 3200, "ue8m0" in kind
+        x, xs = quant_rows(torch.randn((src, K), generator=g), pow2)
+        w, ws = quant_blocks(torch.randn((G, N, K), generator=g), pow2)
+        byte = (lambda s: (torch.log2(s) + 127).to(torch.uint8)) if pow2 else (lambda s: s)
+        miep.grouped_gemm_fp8_into(x.to(DEV), byte(xs).to(DEV), w.to(DEV), byte(ws).to(DEV), grp, y, expected_rows=4, **kw)
+        xd, wd = expand_x(x, xs), [expand_w(w[i], ws[i]).T for i in range(G)]
+    y = y.cpu()
+    assert bool((y[~live] == MARK).all())
+    for i, (n, b) in enumerate(zip(rows, begin)):
+        a = xd[b:b + n] if not gather else torch.where(((index[b:b + n] >= 0) & (index[b:b + n] < src)).unsqueeze(1),
+                                                       xd[index[b:b + n].long().clamp(0, src - 1)], 0.0)
+        want, mag = a @ wd[i], a.abs() @ wd[i].abs()
+        close(y[b:b + n], want, fp8_tol(want, mag, K), "group %d" % i)
+
+
 def test_fp8_codes_as_bytes():
     """uint8 codes are the same call as float8_e4m3fn ones."""
     g = gen(1)
