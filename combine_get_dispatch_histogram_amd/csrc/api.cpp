@@ -235,12 +235,16 @@ miep_status check_gemm(const miep_row_groups* g, int32_t n, int32_t k, int32_t e
   return MIEP_OK;
 }
 
-// The rows operand of a grouped product: in layout rows, or gathered.
-miep_status check_source(const miep_row_groups* g, const void* x, int64_t x_rows, const int32_t* row_index) {
+// The rows operand of a grouped product: in layout rows, or gathered (its rows'
+// offsets are 32-bit counts of 16 bytes).
+miep_status check_source(const miep_row_groups* g, const void* x, int64_t x_rows, int64_t row_bytes,
+                         const int32_t* row_index) {
   if (x_rows < 0 || x_rows > kMaxRowsI32) return fail(MIEP_EINVAL, "x_rows must be in [0, 2^31-1]");
   if (!row_index && x_rows != g->num_rows)
     return fail(MIEP_EINVAL, "x has %lld rows, the layout %lld (and there is no row_index)",
                 static_cast<long long>(x_rows), static_cast<long long>(g->num_rows));
+  if (row_index && x_rows * row_bytes > (64ll << 30))
+    return fail(MIEP_EUNSUPPORTED, "a gathered x larger than 64 GiB");
   if (x_rows > 0 && !x) return fail(MIEP_EINVAL, "x is NULL");
   if (!aligned16(x)) return fail(MIEP_EUNSUPPORTED, "x must be 16-byte aligned");
   return MIEP_OK;
@@ -896,7 +900,7 @@ miep_status miep_grouped_gemm(const miep_row_groups* g, const uint16_t* x, int64
                               void* stream) {
   miep::GemmRowsArgs a{};
   miep_status st = check_gemm(g, n, k, expected_rows, &a.g);
-  if (st == MIEP_OK) st = check_source(g, x, x_rows, row_index);
+  if (st == MIEP_OK) st = check_source(g, x, x_rows, 2ll * k, row_index);
   if (st == MIEP_OK) st = check_array(w, g->num_groups > 0, "w");
   if (st == MIEP_OK) st = check_array(y, g->num_rows > 0, "y");
   if (st != MIEP_OK) return st;
@@ -938,7 +942,7 @@ miep_status miep_grouped_gemm_wgrad(const miep_row_groups* g, const uint16_t* dy
   miep::GemmWeightArgs a{};
   miep_status st = check_gemm(g, n, k, 0, &a.g);
   if (st == MIEP_OK) st = check_array(dy, g->num_rows > 0, "dy");
-  if (st == MIEP_OK) st = check_source(g, x, x_rows, row_index);
+  if (st == MIEP_OK) st = check_source(g, x, x_rows, 2ll * k, row_index);
   if (st == MIEP_OK) st = check_array(dw, g->num_groups > 0, "dw");
   if (st != MIEP_OK) return st;
   if (accumulate && !dw_f32) return fail(MIEP_EINVAL, "accumulate needs an fp32 dw");
@@ -962,7 +966,7 @@ miep_status miep_grouped_gemm_fp8(const miep_row_groups* g, const uint8_t* x, co
   miep::GemmRowsArgs a{};
   miep_status st = check_gemm(g, n, k, expected_rows, &a.g);
   if (st == MIEP_OK && k % miep::kFp8Group != 0) st = fail(MIEP_EINVAL, "FP8 products need k %% 128 == 0");
-  if (st == MIEP_OK) st = check_source(g, x, x_rows, row_index);
+  if (st == MIEP_OK) st = check_source(g, x, x_rows, k, row_index);
   if (st == MIEP_OK) st = check_array(w, g->num_groups > 0, "w");
   if (st == MIEP_OK) st = check_array(y, g->num_rows > 0, "y");
   if (st != MIEP_OK) return st;

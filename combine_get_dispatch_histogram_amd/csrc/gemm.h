@@ -143,7 +143,7 @@ __device__ __forceinline__ TileAt find_tile(const GroupArgs& g, int bq, int per,
     if (g0 + lane < g.G) group_range(g, g0 + lane, &b, &n);
     const int tiles = tiles_of(n, bq, half, halves) * per;
     const int inc = wave_inclusive_scan(tiles);
-    const uint64_t past = ballot(before + inc > t);
+    const uint64_t past = ballot(before + inc > t && tiles > 0);
     if (past != 0) {
       const int l = __builtin_ctzll(past);
       r.group = g0 + l;

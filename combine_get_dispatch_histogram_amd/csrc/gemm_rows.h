@@ -10,6 +10,7 @@
 // with 16x16 MFMAs.
 #pragma once
 
+#include <cmath>
 #include <type_traits>
 
 #include "gemm.h"
@@ -658,12 +659,11 @@ hipError_t launch_rows(const GemmRowsArgs& a, hipStream_t st) {
   // 13, 16 rows of 2 x 4096 x 7168 28 -> 22; of 4 x 4096 x 7168 37 -> 38, and
   // 16 steps only, 100 rows of 1 x 256 x 1024, 13 -> 14.5).
   const int64_t tiles32 = a.g.G * ((static_cast<int64_t>(a.expected) + 31) / 32) * ((a.NO + 31) / 32);
-  if (tiles32 <= 256 && a.C / (F8 ? 128 : 64) >= 24) return launch_rows_split<EL, PT, GATHER>(a, st);
+  if (tiles32 <= 256 && a.C / (F8 ? 128 : 64) >= 24 && split_tiles(a) <= (1ll << 31) - 1)
+    return launch_rows_split<EL, PT, GATHER>(a, st);
   // Rows that most groups stay under when e are expected and chance spreads
   // them (a binomial count's deviation is at most sqrt(e)).
-  int64_t e = a.expected, root = 0;
-  while ((root + 1) * (root + 1) <= e) ++root;
-  e += root;
+  const int64_t e = a.expected + static_cast<int64_t>(std::sqrt(static_cast<double>(a.expected)));
   // Measured in us on 8 experts of 4096 x 7168 weights unless said otherwise,
   // bf16, tiles written channels x rows.
   //   A few rows: the weights stream past them.  128 x 32, two workgroups a

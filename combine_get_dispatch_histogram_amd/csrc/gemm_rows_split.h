@@ -214,10 +214,14 @@ __global__ __launch_bounds__(512, 2) void gemm_rows_split_kernel(GemmRowsArgs a)
   }
 }
 
+// The most tiles that disjoint groups can have.
+inline int64_t split_tiles(const GemmRowsArgs& a) {
+  return ((a.g.limit + 31) / 32 + a.g.G) * ((static_cast<int64_t>(a.NO) + 31) / 32);
+}
+
 template <int EL, bool PT, bool GATHER>
 hipError_t launch_rows_split(GemmRowsArgs a, hipStream_t st) {
-  const int64_t most = ((a.g.limit + 31) / 32 + a.g.G) * static_cast<int64_t>((a.NO + 31) / 32);
-  if (most > (1ll << 31) - 1) return hipErrorInvalidConfiguration;
+  const int64_t most = split_tiles(a);
   a.max_tiles = static_cast<int>(most);
   gemm_rows_split_kernel<EL, PT, GATHER><<<static_cast<unsigned>(most < 256 ? most : 256), 512, 0, st>>>(a);
   return hipGetLastError();

@@ -403,7 +403,7 @@ typedef struct miep_row_groups {
  *   recv_topk_idx    [num_rows][K] int64 from miep_dispatch (entries outside [0, E/R) have no slot)
  *   recv_rank_offset [R + 1] int32 from the handle
  *   workspace        [parts][E] int32, parts >= 1: the parts a rank's rows may be sorted in
- *                    (256 / R is enough to fill the GPU)
+ *                    (256 / R is enough to fill the GPU); of one call at a time
  *   group_begin      [E] int32 out: first slot of each expert
  *   group_rows       [E] int32 out: its slots (num_recv_tokens_per_expert with expert_alignment 1)
  *   slot_row         [num_slots] int32 out: received row of each slot, -1 where there is none
@@ -446,7 +446,8 @@ miep_status miep_expert_reduce_backward(const uint16_t* dy, const uint16_t* z, i
  * in fp32, rounded once to bf16.
  *   x         [x_rows][K] bf16.  src(i) = i (x_rows == num_rows), or row_index[i]
  *   row_index [num_rows] int32, nullable: source row of each layout row (slot_row of
- *             miep_expert_order); a row whose index is outside [0, x_rows) gives zeros
+ *             miep_expert_order), any of them any number of times; a row whose index is
+ *             outside [0, x_rows) gives zeros.  A gathered x is at most 64 GiB.
  *   w         [num_groups][N][K] bf16;  y [num_rows][N] bf16 out
  *   expected_rows  rows a group is expected to hold, 0 = num_rows / num_groups: chooses the tile,
  *             never the result's meaning.  Give it where the layout is mostly empty (low latency).

@@ -69,6 +69,7 @@ def test_product_arguments(lib):
     assert gemm(x=24) == EUNSUPPORTED and gemm(w=8) == EUNSUPPORTED and gemm(y=18) == EUNSUPPORTED
     assert gemm(rows=99) == EINVAL and b"row_index" in lib.miep_last_error()      # rows of another layout
     assert gemm(rows=-1, idx=16) == EINVAL and gemm(exp=-1) == EINVAL
+    assert gemm(rows=(64 << 30) // 128 + 1, idx=16) == EUNSUPPORTED and b"64 GiB" in lib.miep_last_error()
 
     def wgrad(dw=16, f32=1, acc=0, dy=16):
         return lib.miep_grouped_gemm_wgrad(g, dy, 16, 100, None, 64, 64, f32, acc, dw, None)

@@ -241,6 +241,27 @@ def test_grouped_gemm_wgrad(name, N, K, gather):
     close(acc, want + old.double(), (most + 2) * ULP * (mag + old.double().abs()), "accumulated")
 
 
+@pytest.mark.parametrize("expected", [1, 100, 100000])
+def test_more_groups_than_lanes(expected):
+    """150 groups, most of them empty: the walk over groups passes several blocks of 64."""
+    rows = [(i * 7) % 40 if i % 3 == 0 else 0 for i in range(150)]
+    begin = np.cumsum([0] + rows[:-1]).tolist()
+    total, N, K = sum(rows), 72, 40
+    g = gen(12)
+    x, w = torch.randn((total, K), generator=g).to(BF), torch.randn((150, N, K), generator=g).to(BF)
+    dy, h = torch.randn((total, N), generator=g).to(BF), torch.randn((total, 2 * K), generator=g).to(BF)
+    grp = groups_of(rows, begin)
+    y, dw = miep.grouped_gemm(x.to(DEV), w.to(DEV), grp, expected_rows=expected), miep.grouped_gemm_wgrad(dy.to(DEV), x.to(DEV), grp)
+    a = miep.swiglu(h.to(DEV), grp)
+    for i, (n, b) in enumerate(zip(rows, begin)):
+        xs, ws = x[b:b + n].double(), w[i].double()
+        close(y[b:b + n], xs @ ws.T, BF_HALF * (xs @ ws.T).abs() + K * ULP * (xs.abs() @ ws.abs().T), "group %d" % i)
+        d = dy[b:b + n].double()
+        close(dw[i], d.T @ xs, 41 * ULP * (d.abs().T @ xs.abs()))
+    want = swiglu64(h)
+    close(a, want, (BF_HALF + SIG) * want.abs() + TINY * (1 + factors(h)[0] * factors(h)[1]))
+
+
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("most", [70, 400])
 def test_wgrad_large_tiles(most, gather):
