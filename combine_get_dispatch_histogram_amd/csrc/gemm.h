@@ -111,7 +111,7 @@ __device__ __forceinline__ void group_range(const GroupArgs& g, int i, int64_t* 
 struct TileAt {
   int group;       // -1: past the last tile
   int first;       // the tile's place among the group's tiles of its kind
-  int half;        // at most `half` rows: the group's last tile
+  int half;        // 1: the group's half tile; 2, 3: the first and second half of a whole one
   int64_t begin;
   int rows;
 };

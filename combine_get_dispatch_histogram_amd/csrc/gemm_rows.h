@@ -93,13 +93,26 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
       half1 = h * (xcd + 1) / 8;
     }
   }
+  // Whole tiles that would make a last round of their own, one workgroup each,
+  // are cut in two where their halves and the half tiles then make one round
+  // of half the length (16384 ragged rows, 4.06 rounds of whole tiles: 957 -> 944 us).
+  int64_t cut = 0;
+  if constexpr (kHalf > 0) {
+    cut = (full1 - full0) % stride;
+    if (2 * cut + half1 - half0 > stride) cut = 0;
+  }
   int turn = blockIdx.x >> 3;
   auto next_tile = [&]() MIEP_INLINE {
     TileAt r;
     r.group = -1;
-    const int64_t full = full1 - full0, at = turn;
-    if (at < full) r = find_tile(a.g, BQ, ntiles, kHalf, false, static_cast<int>(full0 + at));
-    else if (kHalf > 0 && at - full < half1 - half0) r = find_tile(a.g, BQ, ntiles, kHalf, true, static_cast<int>(half0 + at - full));
+    const int64_t full = full1 - full0 - cut, at = turn;
+    if (at < full + 2 * cut) {
+      const int64_t k = at - full;
+      r = find_tile(a.g, BQ, ntiles, kHalf, false, static_cast<int>(full0 + (k < 0 ? at : full + k / 2)));
+      if (k >= 0) r.half = 2 + static_cast<int>(k & 1);
+    } else if (kHalf > 0 && at - full - 2 * cut < half1 - half0) {
+      r = find_tile(a.g, BQ, ntiles, kHalf, true, static_cast<int>(half0 + at - full - 2 * cut));
+    }
     turn += stride;
     return r;
   };
@@ -121,14 +134,14 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
     // after the other: the 32 tiles that an XCD works on at a time share 8
     // tiles of rows and 4 of weights
     constexpr int kBand = 8;
-    const int mtiles = at.half ? 1 : max(full_tiles(at.rows, BQ, kHalf), 1);
+    const int mtiles = at.half == 1 ? 1 : max(full_tiles(at.rows, BQ, kHalf), 1);
     const int first = min(max(at.first, 0), mtiles * ntiles - 1);
     const int band = first / (kBand * ntiles), in_band = first - band * (kBand * ntiles);
     const int bh = min(kBand, mtiles - band * kBand);
-    const int pt = in_band / bh, qt = at.half ? at.rows / BQ : band * kBand + in_band - pt * bh;
-    const int q0 = qt * BQ;
+    const int pt = in_band / bh, qt = at.half == 1 ? at.rows / BQ : band * kBand + in_band - pt * bh;
+    const int q0 = qt * BQ + (at.half == 3 ? kHalf : 0);
     p0 = pt * BP;
-    live = min(BQ, at.rows - q0);                                     // rows of this tile
+    live = min(at.half ? kHalf : BQ, at.rows - q0);                   // rows of this tile
     row0 = at.begin + q0;
     pg = static_cast<const uint8_t*>(a.p) + static_cast<int64_t>(at.group) * NO * C * EB;
 
