@@ -41,9 +41,11 @@ __device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0u, 0u, 0u
 __device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
 }
-// The same from a scalar base and a 32-bit lane offset.
+// The same from a scalar base and a 32-bit lane offset.  (A scalar register that
+// a vector instruction wrote, as when a spilled one comes back, may be a vector
+// load's base after five wait states: the pause and the move before it.)
 __device__ __forceinline__ void dma16s(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
 // 4 bytes a lane to lds + 4 * i.
 __device__ __forceinline__ void dma4(const void* src, uint32_t lds) {
@@ -59,6 +61,15 @@ __device__ __forceinline__ void dma1(const void* src, uint32_t lds) {
 // read takes 32 bytes of each of 4 rows a 16-lane group: rows 0-3, 8-11 (then
 // 4-7, 12-15) by half wavefront; f spreads those 8 rows over the line.
 __device__ __forceinline__ int swz_t(int row) { return ((row & 3) | ((row >> 1) & 4)) << 1; }
+
+// One store of 16 bytes a lane, whatever surrounds it: for results that a later
+// wait counts.  (A vector write to the data registers of a store of more than 8
+// bytes may follow it after two wait states; the compiler, which sees to that
+// elsewhere, does not look into the statement.)
+__device__ __forceinline__ void store16(void* p, const v4u& v) {
+  const u32x4 t = {v.x, v.y, v.z, v.w};
+  asm volatile("global_store_dwordx4 %0, %1, off\n\ts_nop 1" ::"v"(p), "v"(t) : "memory");
+}
 
 // Waits until at most N vector memory operations of this wavefront are in
 // flight and its LDS reads have returned, then for the workgroup: tiles whose
