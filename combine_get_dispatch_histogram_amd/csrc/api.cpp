@@ -211,6 +211,7 @@ miep_status check_groups(const miep_row_groups* g, miep::GroupArgs* out) {
   if (g->num_groups < 0 || g->num_rows < 0 || g->num_rows > kMaxRowsI32)
     return fail(MIEP_EINVAL, "num_groups must be >= 0 and num_rows in [0, 2^31-1]");
   if (g->num_groups > miep::kMaxExperts) return fail(MIEP_EUNSUPPORTED, "num_groups > %d", miep::kMaxExperts);
+  if (g->num_rows > miep::kMostRows) return fail(MIEP_EUNSUPPORTED, "num_rows > 2^31 - 2^16");
   if (g->num_groups > 0 && !g->rows) return fail(MIEP_EINVAL, "groups' rows is NULL");
   if (g->num_groups > 0 && !g->begin && g->stride <= 0)
     return fail(MIEP_EINVAL, "groups need begin or a stride > 0");
@@ -230,8 +231,8 @@ miep_status check_gemm(const miep_row_groups* g, int32_t n, int32_t k, int32_t e
   if (n % 8 != 0 || k % 8 != 0) return fail(MIEP_EUNSUPPORTED, "n and k must be multiples of 8 (16-byte rows)");
   if (n > (1 << 21) || k > (1 << 21)) return fail(MIEP_EUNSUPPORTED, "n or k > 2^21");
   const int64_t wide = (n > k ? n : k) / 128 + 1;
-  if ((g->num_rows / 32 + 1 + g->num_groups) * wide > kMaxRowsI32)
-    return fail(MIEP_EUNSUPPORTED, "more than 2^31-1 tiles of rows and columns");
+  if ((g->num_rows / 32 + 1 + g->num_groups) * wide > miep::kMostTiles)
+    return fail(MIEP_EUNSUPPORTED, "more than 2^31 - 2^16 tiles of 32 rows x 128 columns");
   return MIEP_OK;
 }
 

@@ -169,8 +169,10 @@ __device__ __forceinline__ TileAt find_tile(const GroupArgs& g, int bq, int per,
   return r;
 }
 
-// How many they are; at most `most`, whatever overlapping groups would add up to.
-__device__ __forceinline__ int count_tiles(const GroupArgs& g, int bq, int per, int half, bool halves, int most) {
+// How many they are.  Groups that overlap may have more than the layout's rows
+// make; past kMostTiles, where a walk's own steps would overflow, they are not
+// counted.
+__device__ __forceinline__ int count_tiles(const GroupArgs& g, int bq, int per, int half, bool halves) {
   const int lane = lane_id();
   int64_t total = 0;
   for (int g0 = 0; g0 < g.G; g0 += kWave) {
@@ -178,9 +180,9 @@ __device__ __forceinline__ int count_tiles(const GroupArgs& g, int bq, int per, 
     int n = 0;
     if (g0 + lane < g.G) group_range(g, g0 + lane, &b, &n);
     const int sum = readlane(wave_inclusive_scan(tiles_of(n, bq, half, halves) * per), 63);
-    total += sum < 0 ? most : sum;
+    total += sum < 0 ? kMostTiles : sum;
   }
-  return static_cast<int>(total < most ? total : most);
+  return static_cast<int>(total < kMostTiles ? total : kMostTiles);
 }
 
 }  // namespace miep

@@ -84,11 +84,11 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
   const int xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
   int64_t full0, full1, half0 = 0, half1 = 0;
   {
-    const int64_t n = count_tiles(a.g, BQ, ntiles, kHalf, false, a.max_tiles);
+    const int64_t n = count_tiles(a.g, BQ, ntiles, kHalf, false);
     full0 = n * xcd / 8;
     full1 = n * (xcd + 1) / 8;
     if constexpr (kHalf > 0) {
-      const int64_t h = count_tiles(a.g, BQ, ntiles, kHalf, true, a.max_tiles);
+      const int64_t h = count_tiles(a.g, BQ, ntiles, kHalf, true);
       half0 = h * xcd / 8;
       half1 = h * (xcd + 1) / 8;
     }
@@ -674,11 +674,9 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
 }
 
 template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
-hipError_t launch_rows_tile(GemmRowsArgs a, hipStream_t st) {
+hipError_t launch_rows_tile(const GemmRowsArgs& a, hipStream_t st) {
   const int64_t per = (a.NO + BP - 1) / BP;
   const int64_t most = ((a.g.limit + BQ - 1) / BQ + a.g.G) * per;     // disjoint groups have no more tiles
-  if (most > (1ll << 31) - 1) return hipErrorInvalidConfiguration;
-  a.max_tiles = static_cast<int>(most);
   int per_cu = 0;
   // resident workgroups: by LDS (160 KiB a CU) and two wavefronts a SIMD
   per_cu = 163840 / RowsTile<EL, PT, GATHER, BP, BQ, WP, WQ, NSP, NSQ>::kLds;
@@ -698,7 +696,7 @@ hipError_t launch_rows(const GemmRowsArgs& a, hipStream_t st) {
   // 13, 16 rows of 2 x 4096 x 7168 28 -> 22; of 4 x 4096 x 7168 37 -> 38, and
   // 16 steps only, 100 rows of 1 x 256 x 1024, 13 -> 14.5).
   const int64_t tiles32 = a.g.G * ((static_cast<int64_t>(a.expected) + 31) / 32) * ((a.NO + 31) / 32);
-  if (tiles32 <= 256 && a.C / (F8 ? 128 : 64) >= 24 && split_tiles(a) <= (1ll << 31) - 1)
+  if (tiles32 <= 256 && a.C / (F8 ? 128 : 64) >= 24 && split_tiles(a) <= kMostTiles)
     return launch_rows_split<EL, PT, GATHER>(a, st);
   // Rows that most groups stay under when e are expected and chance spreads
   // them (a binomial count's deviation is at most sqrt(e)).

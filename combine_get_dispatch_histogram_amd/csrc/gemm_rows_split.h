@@ -46,7 +46,7 @@ __global__ __launch_bounds__(512, 2) void gemm_rows_split_kernel(GemmRowsArgs a)
   const int64_t kb = C / kFp8Group;
   constexpr int SB = EL == kGemmFp8 ? 4 : 1;
 
-  const int total = count_tiles(a.g, S::kSide, ntiles, 0, false, a.max_tiles);
+  const int total = count_tiles(a.g, S::kSide, ntiles, 0, false);
   for (int t = blockIdx.x; t < total; t += gridDim.x) {
     const TileAt at = find_tile(a.g, S::kSide, ntiles, 0, false, t);
     if (at.group < 0) break;
@@ -220,9 +220,8 @@ inline int64_t split_tiles(const GemmRowsArgs& a) {
 }
 
 template <int EL, bool PT, bool GATHER>
-hipError_t launch_rows_split(GemmRowsArgs a, hipStream_t st) {
+hipError_t launch_rows_split(const GemmRowsArgs& a, hipStream_t st) {
   const int64_t most = split_tiles(a);
-  a.max_tiles = static_cast<int>(most);
   gemm_rows_split_kernel<EL, PT, GATHER><<<static_cast<unsigned>(most < 256 ? most : 256), 512, 0, st>>>(a);
   return hipGetLastError();
 }

@@ -201,7 +201,10 @@ hipError_t launch_copy_i32(const int32_t* src, int32_t* dst, int n, hipStream_t 
 
 // ---- groups of rows of one layout: group i holds rows[i] rows from begin[i]
 // (null: from i * stride, at most stride of them).  Device data, never
-// trusted: kernels read each group as its part inside [0, limit).
+// trusted: kernels read each group as its part inside [0, limit).  Layouts have
+// at most kMostRows rows and walks at most as many tiles, which leaves room for
+// the 32-bit sums of rows and tiles with a tile, a step or a grid.
+constexpr int kMostRows = 0x7fff0000, kMostTiles = kMostRows;
 struct GroupArgs {
   int G;
   int stride;
@@ -225,7 +228,6 @@ struct GemmRowsArgs {
   uint16_t* out;               // [limit][NO]
   int type, transposed;
   int expected;                // rows a group is expected to hold (0: limit / G)
-  int max_tiles;               // set by the launcher
 };
 hipError_t launch_gemm_rows(const GemmRowsArgs& a, hipStream_t st);
 
@@ -254,7 +256,7 @@ struct SwigluArgs {
   void* out;                 // [limit][I] bf16 or E4M3; backward: [limit][2 * I] bf16
   float* scales;             // FP8: [limit][I/128]
   uint8_t* scales_ue8m0;     // FP8: [limit][I/128] or null
-  int rows_per_tile, max_tiles;  // set by the launcher
+  int rows_per_tile;         // set by the launcher
 };
 enum SwigluKind { kSwigluBf16 = 0, kSwigluFp8 = 1, kSwigluBackward = 2 };
 hipError_t launch_swiglu(const SwigluArgs& a, int kind, hipStream_t st);

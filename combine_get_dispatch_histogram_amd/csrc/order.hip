@@ -135,7 +135,7 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs a)
         }
         if (p == 0)
           for (int64_t q = at + all; q < at + padded; ++q)
-            if (q < a.slots) a.slot_row[q] = -1;
+            if (q >= 0 && q < a.slots) a.slot_row[q] = -1;
       }
     }
   }
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs a)
       if (held[k] >= 0) {
         slot = next[wave][e] + __popcll(same & lanemask_lt());
         if ((same >> lane) == 1) next[wave][e] = slot + 1;            // the last of the equal ones
-        if (slot < a.slots) a.slot_row[slot] = fdiv(static_cast<int>(n), a.Kdiv);
+        if (slot >= 0 && slot < a.slots) a.slot_row[slot] = fdiv(static_cast<int>(n), a.Kdiv);
         else slot = -1;
       }
       if (n < i1) a.row_slot[n] = slot;
@@ -167,11 +167,11 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs a)
   }
 
   // slots behind the last expert's, and rows behind the last received one
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kOrderThreads;
-  for (int64_t s = slots + blockIdx.x * static_cast<int64_t>(kOrderThreads) + tid; s < a.slots; s += step) a.slot_row[s] = -1;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kOrderThreads, own = blockIdx.x * static_cast<int64_t>(kOrderThreads) + tid;
+  for (int64_t s = max(slots, static_cast<int64_t>(0)) + own; s < a.slots; s += step) a.slot_row[s] = -1;
   int64_t end = a.off[a.R];
   end = end < 0 ? 0 : end > a.rows ? a.rows : end;
-  for (int64_t i = end * a.K + blockIdx.x * static_cast<int64_t>(kOrderThreads) + tid; i < a.rows * a.K; i += step) a.row_slot[i] = -1;
+  for (int64_t i = end * a.K + own; i < a.rows * a.K; i += step) a.row_slot[i] = -1;
   if (a.status && blockIdx.x == 0 && tid == 0) *a.status = slots > a.slots ? kStatusCapacity : 0;
 }
 

@@ -44,7 +44,7 @@ __device__ __forceinline__ void put(uint16_t* p, const v4u& v) {
 
 template <int KIND, bool STREAM>
 __global__ __launch_bounds__(256) void swiglu_kernel(SwigluArgs a) {
-  const int total = count_tiles(a.g, a.rows_per_tile, 1, 0, false, a.max_tiles);
+  const int total = count_tiles(a.g, a.rows_per_tile, 1, 0, false);
   const int per_row = a.I / 8;
   for (int t = blockIdx.x; t < total; t += gridDim.x) {
     const TileAt at = find_tile(a.g, a.rows_per_tile, 1, 0, false, t);
@@ -105,8 +105,6 @@ hipError_t launch_swiglu(const SwigluArgs& args, int kind, hipStream_t st) {
   // One row a workgroup at a time (16384 rows of 2 x 2048, backward: 61 us; 4 rows 65, 8 rows 72).
   a.rows_per_tile = 1;
   const int64_t most = a.g.limit + a.g.G;
-  if (most > (1ll << 31) - 1) return hipErrorInvalidConfiguration;
-  a.max_tiles = static_cast<int>(most);
   const unsigned grid = static_cast<unsigned>(most < 2048 ? most : 2048);
   // A result of half the 256 MiB last-level cache or more is stored past it:
   // 16384 rows 63 -> 52 us (with a copy that reads it behind, 122 -> 115);

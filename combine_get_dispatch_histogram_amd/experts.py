@@ -384,7 +384,7 @@ def swiglu_fp8(h: torch.Tensor, groups: RowGroups, round_scale: bool = False, us
 
 
 def swiglu_backward_into(da, h, groups: RowGroups, dh) -> None:
-    """swiglu_backward into dh [rows, 2 * inner] (allocates nothing)."""
+    """swiglu_backward into dh [rows, 2 * inner], which may be h itself (allocates nothing)."""
     h, rows, inner = _check_h(h)
     da, out = _flat(da, "da"), _flat(dh, "dh")
     _want(da, "da", torch.bfloat16, (rows, inner))

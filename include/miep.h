@@ -386,12 +386,13 @@ miep_status miep_mask_query(const int32_t* mask_buffer, int32_t num_ranks, int32
  * = R*M).  Both arrays are device data, read when the kernels run; whatever
  * they hold, only rows in [0, num_rows) are touched.  Groups may be empty and
  * need no alignment; groups that overlap leave either one's result in the
- * shared rows.  Rows of an output that lie in no group are left as they were,
- * and rows of an input that lie in no group are never read into a result. */
+ * shared rows (num_rows in the limits below then counts them in each).  Rows
+ * of an output that lie in no group are left as they were, and rows of an
+ * input that lie in no group are never read into a result. */
 typedef struct miep_row_groups {
   const int32_t* begin;  /* [num_groups] first row, or NULL (g * stride)        */
   const int32_t* rows;   /* [num_groups] rows                                   */
-  int64_t num_rows;      /* rows of the layout, 0..2^31-1                       */
+  int64_t num_rows;      /* rows of the layout, 0..2^31-2^16                    */
   int32_t num_groups;    /* 0..8192                                             */
   int32_t stride;        /* rows between group starts where begin is NULL (> 0) */
 } miep_row_groups;
@@ -451,7 +452,8 @@ miep_status miep_expert_reduce_backward(const uint16_t* dy, const uint16_t* z, i
  *   w         [num_groups][N][K] bf16;  y [num_rows][N] bf16 out
  *   expected_rows  rows a group is expected to hold, 0 = num_rows / num_groups: chooses the tile,
  *             never the result's meaning.  Give it where the layout is mostly empty (low latency).
- * x, w, y 16-byte aligned; N % 8 == 0, K % 8 == 0, both at most 2^21.
+ * x, w, y 16-byte aligned; N % 8 == 0, K % 8 == 0, both at most 2^21, and
+ * (num_rows / 32 + 1 + num_groups) * (max(N, K) / 128 + 1) at most 2^31-2^16.
  * Errors: EINVAL for null pointers or sizes, EUNSUPPORTED for the limits above. */
 miep_status miep_grouped_gemm(const miep_row_groups* g, const uint16_t* x, int64_t x_rows, const uint16_t* w,
                               int32_t n, int32_t k, const int32_t* row_index, int32_t expected_rows, uint16_t* y,
@@ -488,7 +490,8 @@ miep_status miep_grouped_gemm_fp8(const miep_row_groups* g, const uint8_t* x, co
  * swiglu_fp8 casts the fp32 value per 128 channels (I % 128 == 0) by the rule
  * of the FP8 dispatch: a E4M3, a_scales [num_rows][I/128] fp32 (powers of two
  * with round_scale), a_scales_ue8m0 their exponent bytes (nullable, needs
- * round_scale).  swiglu_backward: dh [num_rows][2*I] from da [num_rows][I]. */
+ * round_scale).  swiglu_backward: dh [num_rows][2*I] from da [num_rows][I]; dh
+ * may be h itself.  Otherwise no output of these calls overlaps an input. */
 miep_status miep_swiglu(const miep_row_groups* g, const uint16_t* h, int32_t inner, uint16_t* a, void* stream);
 miep_status miep_swiglu_fp8(const miep_row_groups* g, const uint16_t* h, int32_t inner, int32_t round_scale,
                             uint8_t* a, float* a_scales, uint8_t* a_scales_ue8m0, void* stream);

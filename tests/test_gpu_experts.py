@@ -242,6 +242,60 @@ def test_grouped_gemm_wgrad(name, N, K, gather):
 
 
 @pytest.mark.parametrize("expected", [1, 100, 100000])
+@pytest.mark.parametrize("K", [64, 3200])                 # steps in order, and split over wavefronts
+def test_groups_that_overlap(K, expected):
+    """Five groups over the same rows and one behind them: far more tiles than the layout's rows make."""
+    say("overlap", K, expected)
+    rows, begin, total, N = [200] * 5 + [33], [0] * 5 + [200], 240, 136
+    g = gen(21)
+    grp = groups_of(rows, begin)
+    x, w = torch.randn((total, K), generator=g).to(BF), torch.randn((6, N, K), generator=g).to(BF)
+    dy = torch.randn((total, N), generator=g).to(BF)
+    y, dx = torch.full((total, N), MARK, dtype=BF, device=DEV), torch.full((total, K), MARK, dtype=BF, device=DEV)
+    miep.grouped_gemm_into(x.to(DEV), w.to(DEV), grp, y, expected_rows=expected)
+    miep.grouped_gemm_dgrad_into(dy.to(DEV), w.to(DEV), grp, dx, expected_rows=expected)
+    for out, a, b, depth in ((y, x, w.transpose(1, 2), K), (dx, dy, w, N)):
+        a, b = a.double(), b.double()
+        assert bool((out[233:] == MARK).all())
+        got = d64(out)
+        fits = torch.zeros((200, out.shape[1]), dtype=torch.bool)
+        for i in range(5):                                 # a shared row holds, place by place, one group's result
+            want, mag = a[:200] @ b[i], a[:200].abs() @ b[i].abs()
+            fits |= (got[:200] - want).abs() <= BF_HALF * want.abs() + depth * ULP * mag
+        assert bool(fits.all())
+        want, mag = a[200:233] @ b[5], a[200:233].abs() @ b[5].abs()
+        close(out[200:233], want, BF_HALF * want.abs() + depth * ULP * mag)
+    dw = miep.grouped_gemm_wgrad(dy.to(DEV), x.to(DEV), grp)
+    want, mag = _wgrad_want(dy, x, rows, begin)
+    close(dw, want, 201 * ULP * mag)
+    h = _h(total, K, g)
+    act = torch.full((total, K), MARK, dtype=BF, device=DEV)
+    miep.swiglu_into(h.to(DEV), grp, act)
+    want = swiglu64(h[:233])
+    gate, up = factors(h[:233])
+    close(act[:233], want, (BF_HALF + SIG) * want.abs() + TINY * (1 + gate * up))
+    assert bool((act[233:] == MARK).all())
+
+
+def test_layouts_without_rows():
+    """No rows at all: outputs of no rows, weight gradients of zeros, or what they held."""
+    grp = groups_of([3, 0], [0, 0])                        # counts that the layout does not hold
+    x, w = torch.empty((0, 64), dtype=BF, device=DEV), torch.ones((2, 16, 64), dtype=BF, device=DEV)
+    dy = torch.empty((0, 16), dtype=BF, device=DEV)
+    assert miep.grouped_gemm(x, w, grp).shape == (0, 16) and miep.grouped_gemm_dgrad(dy, w, grp).shape == (0, 64)
+    assert miep.swiglu(x, grp).shape == (0, 32) and miep.swiglu_backward(x[:, :32].contiguous(), x, grp).shape == (0, 64)
+    assert not miep.grouped_gemm_wgrad(dy, x, grp).any()
+    kept = torch.ones((2, 16, 64), device=DEV)
+    miep.grouped_gemm_wgrad_into(dy, x, grp, kept, accumulate=True)
+    assert bool((kept == 1).all())
+    none = groups_of([], [])
+    assert miep.grouped_gemm_wgrad(dy, x, none).shape == (0, 16, 64)
+    y = torch.full((4, 16), MARK, dtype=BF, device=DEV)
+    miep.grouped_gemm_into(torch.ones((4, 64), dtype=BF, device=DEV), w[:0], none, y)
+    assert bool((y == MARK).all())
+
+
+@pytest.mark.parametrize("expected", [1, 100, 100000])
 def test_more_groups_than_lanes(expected):
     """150 groups, most of them empty: the walk over groups passes several blocks of 64."""
     rows = [(i * 7) % 40 if i % 3 == 0 else 0 for i in range(150)]
@@ -581,6 +635,16 @@ def test_swiglu_backward(name, I):
         assert bool(((num - dup).abs() <= 1e-8 * (1 + d.abs() * gate.abs() * (1 + up.abs()))).all())
 
 
+def test_swiglu_backward_in_place():
+    rows, begin, total = layout("ragged")
+    g = gen(9)
+    h, da = _h(total, 136, g).to(DEV), torch.randn((total, 136), generator=g).to(BF).to(DEV)
+    want = h.clone()
+    miep.swiglu_backward_into(da, h, groups_of(rows, begin), want)
+    miep.swiglu_backward_into(da, h, groups_of(rows, begin), h)
+    assert torch.equal(h, want)
+
+
 def test_swiglu_of_infinities_and_nan():
     inf = float("inf")
     h = torch.zeros((1, 16))
@@ -680,6 +744,21 @@ def test_expert_order_of_overflowed_receive_rows():
     begin, count, slot_row, row_slot, _ = order_want(topk, off, 8, 1, order.num_slots)
     assert np.array_equal(order.group_rows.cpu().numpy(), count)
     assert np.array_equal(order.row_slot.cpu().numpy(), row_slot)
+
+
+def test_expert_order_of_offsets_out_of_order():
+    """Offsets that no dispatch writes: whatever they hold, only the arrays' own places are written."""
+    topk, _ = received(4, 3, 4, [20, 20, 20, 20], 80, gen(4))
+    room = torch.full((3, 400), -99, dtype=torch.int32, device=DEV)
+    for off in ([60, 0, 80, -7, 30], [2 ** 31 - 1, -2 ** 31, 5, 99, 0], [0, 80, 0, 80, 0]):
+        room.fill_(-99)
+        order = miep.ExpertOrder.allocate(topk.to(DEV), i32(off), 12, 4, 100)
+        order.slot_row, order.row_slot = room[0, 150:250], room[2, 40:360].view(80, 4)
+        miep.expert_order_into(topk.to(DEV), order, 4)
+        assert bool((room[1] == -99).all()) and bool((room[0, :150] == -99).all()) and bool((room[0, 250:] == -99).all())
+        assert bool((room[2, :40] == -99).all()) and bool((room[2, 360:] == -99).all())
+        assert bool((order.slot_row >= -1).all()) and bool((order.slot_row < 80).all())
+        assert bool((order.row_slot >= -1 - 98).all()) and bool((order.row_slot < 100).all())
 
 
 @pytest.mark.parametrize("H,K,weighted", [(8, 1, True), (136, 8, True), (2056, 8, False), (264, 20, True), (7168, 3, True)])
