@@ -13,8 +13,10 @@ class _Args:
     a contiguous device tensor on one and the same GPU, and the call runs with
     that GPU current and on its current stream."""
 
+    __slots__ = ("dev", "index")
+
     def __init__(self):
-        self.dev = None
+        self.dev = self.index = None
 
     def _see(self, t: torch.Tensor) -> None:
         if not t.is_cuda:
@@ -27,7 +29,10 @@ class _Args:
     def p(self, t: Optional[torch.Tensor]):
         if t is None:
             return None
-        self._see(t)
+        index = t.get_device()                             # -1 on the host
+        if index != self.index:
+            self._see(t)
+            self.index = index
         if not t.is_contiguous():
             raise ValueError("miep expects contiguous tensors")
         return t.data_ptr()
@@ -38,20 +43,23 @@ class _Args:
 
 
 # The current stream of a device as an integer, without building a Stream
-# object for every call (10 us a call became 6, more than a small kernel takes).
+# object for every call, and the current device without torch's check that the
+# GPU is set up, as tensors on it show (a small swiglu_fp8 call took 10.1 us, of
+# which its launch is 3.8; 7.4 with the first, 6.8 with both).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _run(a: _Args, name: str, *args) -> None:
     if a.dev is None:
         raise ValueError("miep call without device tensors")
     call = getattr(_lib.load(), name)
-    index = a.dev.index
-    if torch.cuda.current_device() == index:
+    index = a.index
+    if _current_device() == index:
         _lib.check(call(*args, _raw_stream(index)))
     else:
-        with torch.cuda.device(a.dev):
+        with torch.cuda.device(index):
             _lib.check(call(*args, _raw_stream(index)))
 
 
@@ -60,7 +68,7 @@ def _want(t: Optional[torch.Tensor], name: str, dtype, shape=None):
         return
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 

@@ -148,6 +148,12 @@ def _check_reduce(order: ExpertOrder, topk_weights, name="topk_weights"):
     return cap, K
 
 
+def _total_rows(a: _Args, order: ExpertOrder) -> int:
+    """Where the received rows' number is: recv_rank_offset's last entry."""
+    off = order.recv_rank_offset
+    return a.p(off) + 4 * (off.numel() - 1)
+
+
 def expert_reduce_into(z, order: ExpertOrder, y, topk_weights=None) -> None:
     """expert_reduce into y [cap, H] (allocates nothing); rows behind the last received one are left as they were."""
     cap, K = _check_reduce(order, topk_weights)
@@ -156,9 +162,7 @@ def expert_reduce_into(z, order: ExpertOrder, y, topk_weights=None) -> None:
         raise ValueError("z must be [%d, H]" % order.num_slots)
     _want(y, "y", torch.bfloat16, (cap, z.shape[1]))
     a = _Args()
-    off = order.recv_rank_offset
-    a.p(off)
-    _run(a, "miep_expert_reduce", a.p(z), z.shape[0], z.shape[1], a.p(order.row_slot), cap, K, a.p(off[-1:]),
+    _run(a, "miep_expert_reduce", a.p(z), z.shape[0], z.shape[1], a.p(order.row_slot), cap, K, _total_rows(a, order),
          a.p(topk_weights), a.p(y))
 
 
@@ -184,10 +188,8 @@ def expert_reduce_backward_into(dy, z, order: ExpertOrder, dz, topk_weights=None
     if d_topk_weights is not None and z is None:
         raise ValueError("d_topk_weights needs z")
     a = _Args()
-    off = order.recv_rank_offset
-    a.p(off)
     _run(a, "miep_expert_reduce_backward", a.p(dy), a.p(z), order.num_slots, H, a.p(order.row_slot), cap, K,
-         a.p(off[-1:]), a.p(topk_weights), a.p(dz), a.p(d_topk_weights))
+         _total_rows(a, order), a.p(topk_weights), a.p(dz), a.p(d_topk_weights))
 
 
 def expert_reduce_backward(dy: torch.Tensor, z: torch.Tensor, order: ExpertOrder,
