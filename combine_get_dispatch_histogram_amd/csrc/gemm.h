@@ -121,38 +121,29 @@ __device__ __forceinline__ void group_range(const GroupArgs& g, int i, int64_t* 
 
 struct TileAt {
   int group;       // -1: past the last tile
-  int first;       // the tile's place among the group's tiles of its kind
-  int half;        // 1: the group's half tile; 2, 3: the first and second half of a whole one
+  int first;       // the tile's place among the group's tiles
   int64_t begin;
   int rows;
 };
 
-// Row tiles of n rows: the whole ones of bq rows, and a last one where it has
-// more than `half` rows (the others are the half tile, one at most; half 0:
-// there is none).
-__device__ __forceinline__ int full_tiles(int n, int bq, int half) { return (n + bq - 1 - half) / bq; }
-__device__ __forceinline__ int tiles_of(int n, int bq, int half, bool halves) {
-  const int full = full_tiles(n, bq, half);
-  return halves ? (n > full * bq ? 1 : 0) : full;
-}
+__device__ __forceinline__ int row_tiles(int n, int bq) { return (n + bq - 1) / bq; }
 
-// Tile t of the sequence in which group i has tiles_of(rows) * per tiles.
+// Tile t of the sequence in which group i has row_tiles(rows, bq) * per tiles.
 // Every wavefront walks for itself: one load a lane for each 64 groups and a
 // scan of the lane counts.
-__device__ __forceinline__ TileAt find_tile(const GroupArgs& g, int bq, int per, int half, bool halves, int t) {
+__device__ __forceinline__ TileAt find_tile(const GroupArgs& g, int bq, int per, int t) {
   const int lane = lane_id();
   int before = 0;
   TileAt r;
   r.group = -1;
   r.first = 0;
-  r.half = halves;
   r.begin = 0;
   r.rows = 0;
   for (int g0 = 0; g0 < g.G; g0 += kWave) {
     int64_t b = 0;
     int n = 0;
     if (g0 + lane < g.G) group_range(g, g0 + lane, &b, &n);
-    const int tiles = tiles_of(n, bq, half, halves) * per;
+    const int tiles = row_tiles(n, bq) * per;
     const int inc = wave_inclusive_scan(tiles);
     const uint64_t past = ballot(before + inc > t && tiles > 0);
     if (past != 0) {
@@ -172,14 +163,14 @@ __device__ __forceinline__ TileAt find_tile(const GroupArgs& g, int bq, int per,
 // How many they are.  Groups that overlap may have more than the layout's rows
 // make; past kMostTiles, where a walk's own steps would overflow, they are not
 // counted.
-__device__ __forceinline__ int count_tiles(const GroupArgs& g, int bq, int per, int half, bool halves) {
+__device__ __forceinline__ int count_tiles(const GroupArgs& g, int bq, int per) {
   const int lane = lane_id();
   int64_t total = 0;
   for (int g0 = 0; g0 < g.G; g0 += kWave) {
     int64_t b = 0;
     int n = 0;
     if (g0 + lane < g.G) group_range(g, g0 + lane, &b, &n);
-    const int sum = readlane(wave_inclusive_scan(tiles_of(n, bq, half, halves) * per), 63);
+    const int sum = readlane(wave_inclusive_scan(row_tiles(n, bq) * per), 63);
     total += sum < 0 ? kMostTiles : sum;
   }
   return static_cast<int>(total < kMostTiles ? total : kMostTiles);

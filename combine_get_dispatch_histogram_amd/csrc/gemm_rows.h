@@ -52,12 +52,12 @@ struct RowsTile {
 // places of the 256-byte LDS line (rows are 128 bytes: their parity is one bit
 // of the place, s the other three).
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
+
+// One workgroup's tiles, of `total`; its LDS from `lds` on (kLds bytes).
 template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
-__global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsArgs a) {
+__device__ __forceinline__ void rows_tiles(const GemmRowsArgs& a, int total, uint32_t lds) {
   using S = RowsTile<EL, PT, GATHER, BP, BQ, WP, WQ, NSP, NSQ>;
   constexpr int TP = S::kTP, TQ = S::kTQ, EB = S::kEB;
-  __shared__ __align__(1024) uint8_t lds_mem[S::kLds];
-  const uint32_t lds = (uint32_t)(uintptr_t)(lds_byte*)lds_mem;
 
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
@@ -76,43 +76,18 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
   const bool ragged_end = C % KE != 0;
   const int64_t kb = C / kFp8Group;                                       // scale blocks of a row (FP8)
 
-  // Tiles with at most half their rows, on which half the wavefronts idle, come
-  // after all others, so that the last round of workgroups is filled up with
-  // them.  Workgroups go to the 8 XCDs in turn: XCD x walks the x-th eighth of
-  // either kind, so tiles that share weights or rows meet in one L2.
-  constexpr int kHalf = WQ > 1 ? BQ / 2 : 0;
+  // Workgroups go to the 8 XCDs in turn: XCD x walks the x-th eighth of the
+  // tiles, so tiles that share weights or rows meet in one L2.  (The groups'
+  // last, short tiles stay among the others: all at the end, they fill up the
+  // last round but read their weights again, 32 groups of 300 rows, 4096 x 2048
+  // 193 -> 183 us, of about 400 252 -> 225.)
   const int xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
-  int64_t full0, full1, half0 = 0, half1 = 0;
-  {
-    const int64_t n = count_tiles(a.g, BQ, ntiles, kHalf, false);
-    full0 = n * xcd / 8;
-    full1 = n * (xcd + 1) / 8;
-    if constexpr (kHalf > 0) {
-      const int64_t h = count_tiles(a.g, BQ, ntiles, kHalf, true);
-      half0 = h * xcd / 8;
-      half1 = h * (xcd + 1) / 8;
-    }
-  }
-  // Whole tiles that would make a last round of their own, one workgroup each,
-  // are cut in two where their halves and the half tiles then make one round
-  // of half the length (16384 ragged rows, 4.06 rounds of whole tiles: 957 -> 944 us).
-  int64_t cut = 0;
-  if constexpr (kHalf > 0) {
-    cut = (full1 - full0) % stride;
-    if (2 * cut + half1 - half0 > stride) cut = 0;
-  }
-  int turn = blockIdx.x >> 3;
+  const int end = static_cast<int>(static_cast<int64_t>(total) * (xcd + 1) / 8);
+  int turn = static_cast<int>(static_cast<int64_t>(total) * xcd / 8) + (blockIdx.x >> 3);
   auto next_tile = [&]() MIEP_INLINE {
     TileAt r;
     r.group = -1;
-    const int64_t full = full1 - full0 - cut, at = turn;
-    if (at < full + 2 * cut) {
-      const int64_t k = at - full;
-      r = find_tile(a.g, BQ, ntiles, kHalf, false, static_cast<int>(full0 + (k < 0 ? at : full + k / 2)));
-      if (k >= 0) r.half = 2 + static_cast<int>(k & 1);
-    } else if (kHalf > 0 && at - full - 2 * cut < half1 - half0) {
-      r = find_tile(a.g, BQ, ntiles, kHalf, true, static_cast<int>(half0 + at - full - 2 * cut));
-    }
+    if (turn < end) r = find_tile(a.g, BQ, ntiles, turn);
     turn += stride;
     return r;
   };
@@ -135,14 +110,14 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
     // after the other: the 32 tiles that an XCD works on at a time share 8
     // tiles of rows and 4 of weights
     constexpr int kBand = 8;
-    const int mtiles = at.half == 1 ? 1 : max(full_tiles(at.rows, BQ, kHalf), 1);
+    const int mtiles = max(row_tiles(at.rows, BQ), 1);
     const int first = min(max(at.first, 0), mtiles * ntiles - 1);
     const int band = first / (kBand * ntiles), in_band = first - band * (kBand * ntiles);
     const int bh = min(kBand, mtiles - band * kBand);
-    const int pt = in_band / bh, qt = at.half == 1 ? at.rows / BQ : band * kBand + in_band - pt * bh;
-    const int q0 = qt * BQ + (at.half == 3 ? kHalf : 0);
+    const int pt = in_band / bh, qt = band * kBand + in_band - pt * bh;
+    const int q0 = qt * BQ;
     p0 = pt * BP;
-    live = min(at.half ? kHalf : BQ, at.rows - q0);                   // rows of this tile
+    live = min(BQ, at.rows - q0);                                     // rows of this tile
     row0 = at.begin + q0;
     pg = static_cast<const uint8_t*>(a.p) + static_cast<int64_t>(at.group) * NO * C * EB;
 
@@ -674,6 +649,35 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
 }
 
 template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
+__global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsArgs a) {
+  __shared__ __align__(1024) uint8_t lds_mem[RowsTile<EL, PT, GATHER, BP, BQ, WP, WQ, NSP, NSQ>::kLds];
+  rows_tiles<EL, PT, GATHER, BP, BQ, WP, WQ, NSP, NSQ>(a, count_tiles(a.g, BQ, (a.NO + BP - 1) / BP),
+                                                       (uint32_t)(uintptr_t)(lds_byte*)lds_mem);
+}
+
+// Tiles of 256 channels, of 192 or 256 rows by what the groups hold: the one
+// whose rounds of one tile a workgroup are the shorter together, a tile of 192
+// taking 5/6 of the time of one of 256 (both by measurement: 46 and 56 us of
+// 4096 x 2048, 151 and 190 of 7168 x 2048's gradient).  32 groups, bf16: of 256
+// rows each 218 us in 256s and 321 in 192s (gradient of 7168 x 2048); of 300
+// rows 224 and 183 (4096 x 2048).
+template <int EL, bool PT, bool GATHER>
+__global__ __launch_bounds__(8 * kWave, 2) void gemm_rows_wide_kernel(GemmRowsArgs a) {
+  constexpr int NSP = EL == kGemmBf16 ? 3 : 2;
+  constexpr int kLds192 = RowsTile<EL, PT, GATHER, 256, 192, 2, 4, 3, 2>::kLds;
+  constexpr int kLds256 = RowsTile<EL, PT, GATHER, 256, 256, 2, 4, NSP, 2>::kLds;
+  __shared__ __align__(1024) uint8_t lds_mem[kLds192 > kLds256 ? kLds192 : kLds256];
+  const uint32_t lds = (uint32_t)(uintptr_t)(lds_byte*)lds_mem;
+  const int ntiles = (a.NO + 255) / 256;
+  const int t192 = count_tiles(a.g, 192, ntiles), t256 = count_tiles(a.g, 256, ntiles);
+  const int64_t grid = gridDim.x;
+  if ((t192 + grid - 1) / grid * 5 < (t256 + grid - 1) / grid * 6)
+    rows_tiles<EL, PT, GATHER, 256, 192, 2, 4, 3, 2>(a, t192, lds);
+  else
+    rows_tiles<EL, PT, GATHER, 256, 256, 2, 4, NSP, 2>(a, t256, lds);
+}
+
+template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
 hipError_t launch_rows_tile(const GemmRowsArgs& a, hipStream_t st) {
   const int64_t per = (a.NO + BP - 1) / BP;
   const int64_t most = ((a.g.limit + BQ - 1) / BQ + a.g.G) * per;     // disjoint groups have no more tiles
@@ -709,12 +713,9 @@ hipError_t launch_rows(const GemmRowsArgs& a, hipStream_t st) {
   if (e <= 24) return launch_rows_tile<EL, PT, GATHER, 128, 32, 4, 1, F8 ? 3 : 4, F8 ? 3 : 4>(a, st);
   const int64_t wide = (a.NO + 255) / 256, narrow = (a.NO + 127) / 128;
   if (a.g.G * wide * ((e + 255) / 256) >= 192) {
-    //   Enough tiles of 256 channels for the GPU's 256 CUs.  256 x 192 where
-    //   it takes no more row tiles than 256 x 256 (32 experts: 128 rows 359 /
-    //   378, 16 of 4096 x 2048 with 300 rows 88 / 126), else 256 x 256 (400
-    //   rows 881 / 757, 4096 rows 827 / 736).
-    if (e <= 192 || (e > 256 && e <= 384)) return launch_rows_tile<EL, PT, GATHER, 256, 192, 2, 4, 3, 2>(a, st);
-    return launch_rows_tile<EL, PT, GATHER, 256, 256, 2, 4, F8 ? 2 : 3, 2>(a, st);
+    // enough tiles of 256 channels for the GPU's 256 CUs
+    gemm_rows_wide_kernel<EL, PT, GATHER><<<256, 8 * kWave, 0, st>>>(a);
+    return hipGetLastError();
   }
   //   Fewer: 128 channels, as many rows as a group needs: 128 x 128 / 192 /
   //   256 at 64 rows 89 / - / 94, at 128 rows 151 / 107 / 110, at 180 rows

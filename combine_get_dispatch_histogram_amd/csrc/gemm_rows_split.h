@@ -46,11 +46,11 @@ __global__ __launch_bounds__(512, 2) void gemm_rows_split_kernel(GemmRowsArgs a)
   const int64_t kb = C / kFp8Group;
   constexpr int SB = EL == kGemmFp8 ? 4 : 1;
 
-  const int total = count_tiles(a.g, S::kSide, ntiles, 0, false);
+  const int total = count_tiles(a.g, S::kSide, ntiles);
   for (int t = blockIdx.x; t < total; t += gridDim.x) {
-    const TileAt at = find_tile(a.g, S::kSide, ntiles, 0, false, t);
+    const TileAt at = find_tile(a.g, S::kSide, ntiles, t);
     if (at.group < 0) break;
-    const int mtiles = max(full_tiles(at.rows, S::kSide, 0), 1);
+    const int mtiles = max(row_tiles(at.rows, S::kSide), 1);
     const int first = min(max(at.first, 0), mtiles * ntiles - 1);
     const int p0 = first / mtiles * S::kSide, q0 = first % mtiles * S::kSide;
     const int live = min(S::kSide, at.rows - q0);

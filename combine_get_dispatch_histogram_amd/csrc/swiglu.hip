@@ -44,10 +44,10 @@ __device__ __forceinline__ void put(uint16_t* p, const v4u& v) {
 
 template <int KIND, bool STREAM>
 __global__ __launch_bounds__(256) void swiglu_kernel(SwigluArgs a) {
-  const int total = count_tiles(a.g, a.rows_per_tile, 1, 0, false);
+  const int total = count_tiles(a.g, a.rows_per_tile, 1);
   const int per_row = a.I / 8;
   for (int t = blockIdx.x; t < total; t += gridDim.x) {
-    const TileAt at = find_tile(a.g, a.rows_per_tile, 1, 0, false, t);
+    const TileAt at = find_tile(a.g, a.rows_per_tile, 1, t);
     if (at.group < 0) return;
     const int r0 = max(at.first, 0) * a.rows_per_tile;
     const int n = min(a.rows_per_tile, at.rows - r0);

@@ -439,22 +439,21 @@ def test_grouped_gemm_fp8(name, N, K, gather, ue8m0, expected):
         close(y[b:b + n], want, fp8_tol(want, mag, K), "group %d" % i)
 
 
-# 64 groups of 0 to 329 rows under 264 output channels: with these expectations every tile is taken in turn
-@pytest.mark.parametrize("expected", [1, 60, 130, 190, 300, 1000])
-@pytest.mark.parametrize("kind", ["gemm", "gather", "dgrad", "fp8", "fp8 gather", "ue8m0", "ue8m0 gather"])
-def test_every_tile(kind, expected):
-    say("every tile", kind, expected)
-    rows = [(53 * i) % 330 if i % 9 else 0 for i in range(64)]
+KINDS = ["gemm", "gather", "dgrad", "fp8", "fp8 gather", "ue8m0", "ue8m0 gather"]
+
+
+def check_product(kind, rows, N, K, expected):
+    """Groups of these rows with gaps between them, N output channels, contractions of K."""
+    G = len(rows)
     begin = np.cumsum([0] + [n + i % 3 for i, n in enumerate(rows)][:-1]).tolist()
-    total, G, N = begin[-1] + rows[-1] + 2, 64, 264
-    g, live, grp = gen(expected), members(rows, begin, begin[-1] + rows[-1] + 2), groups_of(rows, begin)
+    total = begin[-1] + rows[-1] + 2
+    g, live, grp = gen(expected), members(rows, begin, total), groups_of(rows, begin)
     gather = "gather" in kind
     src = 500 if gather else total
     index = torch.randint(-1, src, (total,), generator=g, dtype=torch.int32) if gather else None
     kw = dict(row_index=index.to(DEV)) if gather else {}
     y = torch.full((total, N), MARK, dtype=BF, device=DEV)
     if kind in ("gemm", "gather", "dgrad"):
-        K = 520
         x = torch.randn((src, K), generator=g).to(BF)
         w = torch.randn((G, K, N) if kind == "dgrad" else (G, N, K), generator=g).to(BF)
         if kind == "dgrad":
@@ -463,7 +462,7 @@ def test_every_tile(kind, expected):
             miep.grouped_gemm_into(x.to(DEV), w.to(DEV), grp, y, expected_rows=expected, **kw)
         xd, wd = x.double(), [(t if kind == "dgrad" else t.T).double() for t in w]
     else:
-        K, pow2 = 640, "ue8m0" in kind
+        pow2 = "ue8m0" in kind
         x, xs = quant_rows(torch.randn((src, K), generator=g), pow2)
         w, ws = quant_blocks(torch.randn((G, N, K), generator=g), pow2)
         byte = (lambda s: (torch.log2(s) + 127).to(torch.uint8)) if pow2 else (lambda s: s)
@@ -478,6 +477,22 @@ def test_every_tile(kind, expected):
             a = torch.where((at >= 0).unsqueeze(1), xd[at.clamp_min(0)], 0.0)
         want, mag = a @ wd[i], a.abs() @ wd[i].abs()
         close(y[b:b + n], want, fp8_tol(want, mag, K), "group %d" % i)
+
+
+# 64 groups of 0 to 329 rows under 264 output channels: with these expectations every tile but 256 x 256 is taken in turn
+@pytest.mark.parametrize("expected", [1, 60, 130, 190, 300, 1000])
+@pytest.mark.parametrize("kind", KINDS)
+def test_every_tile(kind, expected):
+    say("every tile", kind, expected)
+    check_product(kind, [(53 * i) % 330 if i % 9 else 0 for i in range(64)], 264, 640 if "8" in kind else 520, expected)
+
+
+# More tiles of 256 channels than workgroups, some whole and some short: of 256 rows, and of 192
+@pytest.mark.parametrize("most", [256, 192])
+@pytest.mark.parametrize("kind", KINDS)
+def test_rounds_of_wide_tiles(kind, most):
+    say("wide tiles", kind, most)
+    check_product(kind, [most - i % 7 for i in range(70)], 1040, 384 if "8" in kind else 264, 256)
 
 
 @pytest.mark.parametrize("rows", [[1], [0, 33, 5], [70, 0, 1, 32]])
