@@ -8,7 +8,10 @@
 // the MFMA's rows (P), so that a lane holds 4 consecutive k of one n.
 //
 // With few rows a group the fp32 result is most of the traffic (4 N K bytes a
-// group), so it leaves in whole 128-byte lines (see the stores).
+// group), so it leaves in whole 128-byte lines (see the stores): 32 ragged groups
+// of 8192 rows, 7168 x 2048, take 494 us, of which the stores alone 308 and the
+// rest alone 271.  With many rows the MFMAs and their LDS reads bound it: 16384
+// rows over 4 groups 404 us, 1,190 TFLOP/s.
 #include <type_traits>
 
 #include "gemm.h"
@@ -253,10 +256,9 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
   }
 
   // Stores.  fp32: lanes of even and odd m exchange halves of two neighbouring
-  // tiles, so that 8 lanes write 128 consecutive bytes of one n: half lines,
-  // written in pieces, took 930 us where whole ones take 690 (32 groups of 256
-  // rows, 7168 x 2048).  Results larger than half the last-level cache leave
-  // it alone (870 us without).
+  // tiles, so that 8 lanes write 128 consecutive bytes of one n: half lines
+  // take 522 us where whole ones take 488 (32 groups of 256 rows, 7168 x 2048;
+  // stores past the caches the same 488).
   const bool odd = m & 1;
 #pragma unroll
   for (int j = 0; j < TQ; ++j) {
@@ -281,8 +283,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
             const f32x4 old = *at;
             v[h] = f32x4{old[0] + v[h][0], old[1] + v[h][1], old[2] + v[h][2], old[3] + v[h][3]};
           }
-          if (a.stream) __builtin_nontemporal_store(v[h], at);
-          else *at = v[h];
+          *at = v[h];
         }
       } else {
         const int n = q0 + (wq * TQ + j) * 16 + m;
@@ -460,23 +461,25 @@ hipError_t launch_weight_tile(const GemmWeightArgs& a, hipStream_t st) {
 
 template <bool GATHER, bool F32>
 hipError_t launch_weight(const GemmWeightArgs& a, hipStream_t st) {
-  const int64_t big = static_cast<int64_t>((a.K + 255) / 256) * ((a.N + 255) / 256) * a.g.G;
-  const int64_t small = static_cast<int64_t>((a.K + 63) / 64) * ((a.N + 63) / 64) * a.g.G;
+  auto tiles = [&](int64_t side) { return (a.K + side - 1) / side * ((a.N + side - 1) / side) * a.g.G; };
   // Splitting the rows: 8000 rows of 512 x 512 89 -> 35 us, of 1024 x 1024 92
   // -> 37; but of 2048 x 2048 103 -> 118, 8 groups of 1000 of 512 x 512 18.5
   // -> 20, and 500 rows of 512 x 512 the same 11.
-  if (small <= 256 && a.g.limit / a.g.G >= 512) {
-    gemm_weight_split_kernel<GATHER, F32><<<static_cast<unsigned>(small), 512, 0, st>>>(a);
+  if (tiles(64) <= 256 && a.g.limit / a.g.G >= 512) {
+    gemm_weight_split_kernel<GATHER, F32><<<static_cast<unsigned>(tiles(64)), 512, 0, st>>>(a);
     return hipGetLastError();
   }
-  if (big < 256) return launch_weight_tile<GATHER, F32, 128, 128, 2, 2, 2, 2>(a, st);
+  // 128 x 128 tiles, two at a time on a CU, or 256 x 256 ones, one at a time:
+  // whose rounds are the shorter together, one of 128s taking 5/8 of one of 256s
+  // (us in 128s / 256s: 2 groups of 2048 rows, 4096 x 2048, 75 / 63; one of 4096
+  // rows 69 / 95; 4 of 2000, 1408 x 2048, 66 / 54; 8 of 500, 2048 x 1408, 42 / 46).
+  if ((tiles(128) + 511) / 512 * 5 < (tiles(256) + 255) / 256 * 8)
+    return launch_weight_tile<GATHER, F32, 128, 128, 2, 2, 2, 2>(a, st);
   return launch_weight_tile<GATHER, F32, 256, 256, 2, 4, GATHER ? 2 : 3, 2>(a, st);
 }
 
-hipError_t launch_gemm_weight(const GemmWeightArgs& args, hipStream_t st) {
-  GemmWeightArgs a = args;
+hipError_t launch_gemm_weight(const GemmWeightArgs& a, hipStream_t st) {
   if (a.g.G == 0) return hipSuccess;
-  a.stream = 4ll * a.g.G * a.N * a.K > (128ll << 20);
   if (a.row_index) return a.out_f32 ? launch_weight<true, true>(a, st) : launch_weight<true, false>(a, st);
   return a.out_f32 ? launch_weight<false, true>(a, st) : launch_weight<false, false>(a, st);
 }

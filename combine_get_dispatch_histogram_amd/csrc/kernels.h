@@ -242,7 +242,6 @@ struct GemmWeightArgs {
   int N, K;
   void* out;                   // [G][N][K] fp32 or bf16
   int out_f32, accumulate;
-  int stream = 0;              // fp32 results bypass the caches (set by the launcher)
 };
 hipError_t launch_gemm_weight(const GemmWeightArgs& a, hipStream_t st);
 
