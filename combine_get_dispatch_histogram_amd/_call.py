@@ -45,7 +45,7 @@ class _Args:
 # The current stream of a device as an integer, without building a Stream
 # object for every call, and the current device without torch's check that the
 # GPU is set up, as tensors on it show (a small swiglu_fp8 call took 10.1 us, of
-# which its launch is 3.8; 7.4 with the first, 6.8 with both).
+# which its launch is 3.8; 7.4 with the first, 6.4 with both and fewer checks).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device

@@ -41,12 +41,13 @@ class RowGroups:
         return RowGroups(rows=recv["packed_recv_count"], stride=recv["packed_recv_x"].shape[1])
 
     def c(self, a, num_rows: int) -> _lib.RowGroupsC:
-        _want(self.rows, "groups.rows", torch.int32)
-        if self.rows.dim() != 1:
+        rows, begin = self.rows, self.begin
+        _want(rows, "groups.rows", torch.int32)
+        if rows.dim() != 1:
             raise ValueError("groups.rows must be [num_groups]")
-        _want(self.begin, "groups.begin", torch.int32, tuple(self.rows.shape))
-        rows, begin = a.p(self.rows), a.p(self.begin)
-        return _lib.RowGroupsC(begin, rows, num_rows, self.rows.numel(), int(self.stride))
+        if begin is not None:
+            _want(begin, "groups.begin", torch.int32, rows.shape)
+        return _lib.RowGroupsC(a.p(begin), a.p(rows), num_rows, rows.numel(), int(self.stride))
 
 
 @dataclass
@@ -88,11 +89,11 @@ class ExpertOrder:
 
 def _flat(t: torch.Tensor, name: str) -> torch.Tensor:
     """[rows, width], or [blocks, rows, width] seen as its rows."""
+    if t.dim() == 2:
+        return t
     if t.dim() == 3 and t.is_contiguous():
         return t.view(t.shape[0] * t.shape[1], t.shape[2])
-    if t.dim() != 2:
-        raise ValueError("%s must be [rows, width] or contiguous [groups, rows, width]" % name)
-    return t
+    raise ValueError("%s must be [rows, width] or contiguous [groups, rows, width]" % name)
 
 
 # --------------------------------------------------------------------------- expert order
@@ -103,20 +104,22 @@ def expert_order_into(recv_topk_idx, order: ExpertOrder, expert_alignment: int =
     if recv_topk_idx.dim() != 2:
         raise ValueError("recv_topk_idx must be [cap, K]")
     cap, K = recv_topk_idx.shape
+    slots, workspace = order.num_slots, order.workspace
+    parts = workspace.shape[0] if workspace is not None and workspace.dim() == 2 else 0
     E, R = order.group_begin.numel(), order.recv_rank_offset.numel() - 1
     _want(order.group_begin, "group_begin", torch.int32, (E,))
     _want(order.group_rows, "group_rows", torch.int32, (E,))
-    _want(order.slot_row, "slot_row", torch.int32, (order.num_slots,))
+    _want(order.slot_row, "slot_row", torch.int32, (slots,))
     _want(order.row_slot, "row_slot", torch.int32, (cap, K))
     _want(order.recv_rank_offset, "recv_rank_offset", torch.int32, (R + 1,))
     _want(status, "status", torch.int32, (1,))
-    if order.workspace is None or order.workspace.dim() != 2 or order.workspace.shape[0] < 1:
+    if parts < 1:
         raise ValueError("expert_order needs a workspace [parts, %d] int32" % E)
-    _want(order.workspace, "workspace", torch.int32, (order.workspace.shape[0], E))
+    _want(workspace, "workspace", torch.int32, (parts, E))
     a = _Args()
     _run(a, "miep_expert_order", a.p(recv_topk_idx), a.p(order.recv_rank_offset), cap, K, E, R, int(expert_alignment),
-         a.p(order.workspace), order.workspace.shape[0], a.p(order.group_begin), a.p(order.group_rows),
-         a.p(order.slot_row), order.num_slots, a.p(order.row_slot), a.p(status))
+         a.p(workspace), parts, a.p(order.group_begin), a.p(order.group_rows), a.p(order.slot_row), slots,
+         a.p(order.row_slot), a.p(status))
 
 
 def expert_order(recv_topk_idx: torch.Tensor, recv_rank_offset: torch.Tensor, num_experts: int,
@@ -204,27 +207,32 @@ def expert_reduce_backward(dy: torch.Tensor, z: torch.Tensor, order: ExpertOrder
 
 # --------------------------------------------------------------------------- grouped products
 def _check_product(x, w, groups: RowGroups, rows: int, row_index, wide: str):
-    if w.dim() != 3 or w.shape[0] != groups.rows.numel():
+    """(rows of x, N, K) of a product over x's channels, w's N or K."""
+    shape, (x_rows, channels) = w.shape, x.shape
+    if len(shape) != 3 or shape[0] != groups.rows.numel():
         raise ValueError("w must be [%d, N, K]" % groups.rows.numel())
-    if x.shape[1] != (w.shape[2] if wide == "K" else w.shape[1]):
-        raise ValueError("rows of %d channels do not match w %s" % (x.shape[1], tuple(w.shape)))
-    _want(row_index, "row_index", torch.int32, (rows,))
-    if row_index is None and x.shape[0] != rows:
-        raise ValueError("x has %d rows, the output %d (and there is no row_index)" % (x.shape[0], rows))
+    _, N, K = shape
+    if channels != (K if wide == "K" else N):
+        raise ValueError("rows of %d channels do not match w %s" % (channels, tuple(shape)))
+    if row_index is not None:
+        _want(row_index, "row_index", torch.int32, (rows,))
+    elif x_rows != rows:
+        raise ValueError("x has %d rows, the output %d (and there is no row_index)" % (x_rows, rows))
+    return x_rows, N, K
 
 
 def grouped_gemm_into(x, w, groups: RowGroups, y, row_index=None, expected_rows: int = 0) -> None:
     """grouped_gemm into y (allocates nothing)."""
     x, y = _flat(x, "x"), _flat(y, "y")
-    _check_product(x, w, groups, y.shape[0], row_index, "K")
-    for t, name in ((x, "x"), (w, "w"), (y, "y")):
-        _want(t, name, torch.bfloat16)
-    _, N, K = w.shape
-    _want(y, "y", torch.bfloat16, (y.shape[0], N))
+    rows = y.shape[0]
+    x_rows, N, K = _check_product(x, w, groups, rows, row_index, "K")
+    _want(x, "x", torch.bfloat16)
+    _want(w, "w", torch.bfloat16)
+    _want(y, "y", torch.bfloat16, (rows, N))
     a = _Args()
-    g = groups.c(a, y.shape[0])
-    _run(a, "miep_grouped_gemm", ctypes.byref(g), a.p(x), x.shape[0], a.p(w), N, K, a.p(row_index),
-         int(expected_rows), a.p(y))
+    g = groups.c(a, rows)
+    _run(a, "miep_grouped_gemm", ctypes.byref(g), a.p(x), x_rows, a.p(w), N, K, a.p(row_index), int(expected_rows),
+         a.p(y))
 
 
 def grouped_gemm(x: torch.Tensor, w: torch.Tensor, groups: RowGroups, row_index: Optional[torch.Tensor] = None,
@@ -245,12 +253,13 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, groups: RowGroups, row_index:
 def grouped_gemm_dgrad_into(dy, w, groups: RowGroups, dx, expected_rows: int = 0) -> None:
     """grouped_gemm_dgrad into dx (allocates nothing)."""
     dy, dx = _flat(dy, "dy"), _flat(dx, "dx")
-    _check_product(dy, w, groups, dx.shape[0], None, "N")
-    _, N, K = w.shape
-    for t, name, shape in ((dy, "dy", (dx.shape[0], N)), (w, "w", None), (dx, "dx", (dx.shape[0], K))):
-        _want(t, name, torch.bfloat16, shape)
+    rows = dx.shape[0]
+    _, N, K = _check_product(dy, w, groups, rows, None, "N")
+    _want(dy, "dy", torch.bfloat16)
+    _want(w, "w", torch.bfloat16)
+    _want(dx, "dx", torch.bfloat16, (rows, K))
     a = _Args()
-    g = groups.c(a, dx.shape[0])
+    g = groups.c(a, rows)
     _run(a, "miep_grouped_gemm_dgrad", ctypes.byref(g), a.p(dy), a.p(w), N, K, int(expected_rows), a.p(dx))
 
 
@@ -271,12 +280,12 @@ def grouped_gemm_wgrad_into(dy, x, groups: RowGroups, dw, row_index=None, accumu
         raise TypeError("accumulate needs a float32 dw")
     _want(dy, "dy", torch.bfloat16)
     _want(x, "x", torch.bfloat16)
-    _check_product(x, dw, groups, dy.shape[0], row_index, "K")
-    _, N, K = dw.shape
-    _want(dy, "dy", torch.bfloat16, (dy.shape[0], N))
+    rows = dy.shape[0]
+    x_rows, N, K = _check_product(x, dw, groups, rows, row_index, "K")
+    _want(dy, "dy", torch.bfloat16, (rows, N))
     a = _Args()
-    g = groups.c(a, dy.shape[0])
-    _run(a, "miep_grouped_gemm_wgrad", ctypes.byref(g), a.p(dy), a.p(x), x.shape[0], a.p(row_index), N, K,
+    g = groups.c(a, rows)
+    _run(a, "miep_grouped_gemm_wgrad", ctypes.byref(g), a.p(dy), a.p(x), x_rows, a.p(row_index), N, K,
          int(dw.dtype == torch.float32), int(bool(accumulate)), a.p(dw))
 
 
@@ -298,16 +307,16 @@ def grouped_gemm_fp8_into(x, x_scales, w, w_scales, groups: RowGroups, y, row_in
             raise TypeError("%s must be float8_e4m3fn/uint8 codes, got %s" % (name, t.dtype))
     if x_scales.dtype not in (torch.float32, torch.uint8):
         raise TypeError("x_scales must be float32, or uint8 exponent bytes, got %s" % x_scales.dtype)
-    _check_product(x, w, groups, y.shape[0], row_index, "K")
-    G, N, K = w.shape
+    rows = y.shape[0]
+    x_rows, N, K = _check_product(x, w, groups, rows, row_index, "K")
     if K % 128:
         raise ValueError("FP8 products need K % 128 == 0")
-    _want(x_scales, "x_scales", x_scales.dtype, (x.shape[0], K // 128))
-    _want(w_scales, "w_scales", x_scales.dtype, (G, -(-N // 128), K // 128))
-    _want(y, "y", torch.bfloat16, (y.shape[0], N))
+    _want(x_scales, "x_scales", x_scales.dtype, (x_rows, K // 128))
+    _want(w_scales, "w_scales", x_scales.dtype, (w.shape[0], -(-N // 128), K // 128))
+    _want(y, "y", torch.bfloat16, (rows, N))
     a = _Args()
-    g = groups.c(a, y.shape[0])
-    _run(a, "miep_grouped_gemm_fp8", ctypes.byref(g), a.p(x), a.p(x_scales), x.shape[0], a.p(w), a.p(w_scales),
+    g = groups.c(a, rows)
+    _run(a, "miep_grouped_gemm_fp8", ctypes.byref(g), a.p(x), a.p(x_scales), x_rows, a.p(w), a.p(w_scales),
          int(x_scales.dtype == torch.uint8), N, K, a.p(row_index), int(expected_rows), a.p(y))
 
 
