@@ -13,10 +13,10 @@ class _Args:
     a contiguous device tensor on one and the same GPU, and the call runs with
     that GPU current and on its current stream."""
 
-    __slots__ = ("dev", "index")
+    __slots__ = ("dev", "index", "astray")
 
     def __init__(self):
-        self.dev = self.index = None
+        self.dev = self.index = self.astray = None
 
     def _see(self, t: torch.Tensor) -> None:
         if not t.is_cuda:
@@ -37,6 +37,25 @@ class _Args:
             raise ValueError("miep expects contiguous tensors")
         return t.data_ptr()
 
+    def arg(self, t: torch.Tensor, name: str, dtype, shape=None) -> int:
+        """_want and p in one step.  Where the tensor lies is looked at by _run
+        (``astray``), so that wrong types and shapes are reported first."""
+        if t.dtype != dtype or (shape is not None and t.shape != shape):
+            _want(t, name, dtype, shape)
+        index = t.get_device()                             # -1 on the host
+        if index != self.index:
+            if self.index is None and index >= 0:
+                self._see(t)
+                self.index = index
+            elif self.astray is None:
+                self.astray = t
+        if not t.is_contiguous():
+            raise ValueError("miep expects contiguous tensors")
+        return t.data_ptr()
+
+    def opt(self, t: Optional[torch.Tensor], name: str, dtype, shape=None) -> Optional[int]:
+        return None if t is None else self.arg(t, name, dtype, shape)
+
     def handle(self, h) -> None:
         for t in h.tensors():
             self.p(t)
@@ -45,13 +64,15 @@ class _Args:
 # The current stream of a device as an integer, without building a Stream
 # object for every call, and the current device without torch's check that the
 # GPU is set up, as tensors on it show (a small swiglu_fp8 call took 10.1 us, of
-# which its launch is 3.8; 7.4 with the first, 6.4 with both and fewer checks).
+# which its launch is 3.8; 7.4 with the first, 6.8 with both, 6.1 with `arg`).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _run(a: _Args, name: str, *args) -> None:
+    if a.astray is not None:
+        a._see(a.astray)
     if a.dev is None:
         raise ValueError("miep call without device tensors")
     call = getattr(_lib.load(), name)

@@ -20,9 +20,10 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._call import _Args, _run, _want, check_status
+from ._call import _Args, _run, check_status
 
 _FP8 = (torch.float8_e4m3fn, torch.uint8)
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 @dataclass
@@ -42,12 +43,11 @@ class RowGroups:
 
     def c(self, a, num_rows: int) -> _lib.RowGroupsC:
         rows, begin = self.rows, self.begin
-        _want(rows, "groups.rows", torch.int32)
-        if rows.dim() != 1:
+        shape = rows.shape
+        if len(shape) != 1:
             raise ValueError("groups.rows must be [num_groups]")
-        if begin is not None:
-            _want(begin, "groups.begin", torch.int32, rows.shape)
-        return _lib.RowGroupsC(a.p(begin), a.p(rows), num_rows, rows.numel(), int(self.stride))
+        first = None if begin is None else a.arg(begin, "groups.begin", _I32, shape)
+        return _lib.RowGroupsC(first, a.arg(rows, "groups.rows", _I32), num_rows, shape[0], int(self.stride))
 
 
 @dataclass
@@ -100,26 +100,20 @@ def _flat(t: torch.Tensor, name: str) -> torch.Tensor:
 def expert_order_into(recv_topk_idx, order: ExpertOrder, expert_alignment: int = 1, status=None) -> None:
     """expert_order into preallocated arrays (allocates nothing).  ``status`` ([1] int32, optional) receives 0 or
     MIEP_ECAPACITY where the experts need more than the slots given (read it with ``check_status``)."""
-    _want(recv_topk_idx, "recv_topk_idx", torch.int64)
     if recv_topk_idx.dim() != 2:
         raise ValueError("recv_topk_idx must be [cap, K]")
     cap, K = recv_topk_idx.shape
     slots, workspace = order.num_slots, order.workspace
     parts = workspace.shape[0] if workspace is not None and workspace.dim() == 2 else 0
     E, R = order.group_begin.numel(), order.recv_rank_offset.numel() - 1
-    _want(order.group_begin, "group_begin", torch.int32, (E,))
-    _want(order.group_rows, "group_rows", torch.int32, (E,))
-    _want(order.slot_row, "slot_row", torch.int32, (slots,))
-    _want(order.row_slot, "row_slot", torch.int32, (cap, K))
-    _want(order.recv_rank_offset, "recv_rank_offset", torch.int32, (R + 1,))
-    _want(status, "status", torch.int32, (1,))
     if parts < 1:
         raise ValueError("expert_order needs a workspace [parts, %d] int32" % E)
-    _want(workspace, "workspace", torch.int32, (parts, E))
     a = _Args()
-    _run(a, "miep_expert_order", a.p(recv_topk_idx), a.p(order.recv_rank_offset), cap, K, E, R, int(expert_alignment),
-         a.p(workspace), parts, a.p(order.group_begin), a.p(order.group_rows), a.p(order.slot_row), slots,
-         a.p(order.row_slot), a.p(status))
+    _run(a, "miep_expert_order", a.arg(recv_topk_idx, "recv_topk_idx", torch.int64),
+         a.arg(order.recv_rank_offset, "recv_rank_offset", _I32, (R + 1,)), cap, K, E, R, int(expert_alignment),
+         a.arg(workspace, "workspace", _I32, (parts, E)), parts, a.arg(order.group_begin, "group_begin", _I32, (E,)),
+         a.arg(order.group_rows, "group_rows", _I32, (E,)), a.arg(order.slot_row, "slot_row", _I32, (slots,)), slots,
+         a.arg(order.row_slot, "row_slot", _I32, (cap, K)), a.opt(status, "status", _I32, (1,)))
 
 
 def expert_order(recv_topk_idx: torch.Tensor, recv_rank_offset: torch.Tensor, num_experts: int,
@@ -141,32 +135,26 @@ def expert_order(recv_topk_idx: torch.Tensor, recv_rank_offset: torch.Tensor, nu
     return order
 
 
-def _check_reduce(order: ExpertOrder, topk_weights, name="topk_weights"):
+def _reduce_args(a: _Args, order: ExpertOrder, topk_weights):
+    """row_slot, cap, K, where the received rows' number is (recv_rank_offset's last entry), topk_weights."""
     cap, K = order.row_slot.shape
-    _want(order.row_slot, "row_slot", torch.int32, (cap, K))
-    _want(order.recv_rank_offset, "recv_rank_offset", torch.int32)
-    if order.recv_rank_offset.dim() != 1 or order.recv_rank_offset.numel() < 2:
-        raise ValueError("recv_rank_offset must be [R + 1]")
-    _want(topk_weights, name, torch.float32, (cap, K))
-    return cap, K
-
-
-def _total_rows(a: _Args, order: ExpertOrder) -> int:
-    """Where the received rows' number is: recv_rank_offset's last entry."""
     off = order.recv_rank_offset
-    return a.p(off) + 4 * (off.numel() - 1)
+    if off.dim() != 1 or off.numel() < 2:
+        raise ValueError("recv_rank_offset must be [R + 1]")
+    return (a.arg(order.row_slot, "row_slot", _I32), cap, K,
+            a.arg(off, "recv_rank_offset", _I32) + 4 * (off.numel() - 1),
+            a.opt(topk_weights, "topk_weights", _F32, (cap, K)))
 
 
 def expert_reduce_into(z, order: ExpertOrder, y, topk_weights=None) -> None:
     """expert_reduce into y [cap, H] (allocates nothing); rows behind the last received one are left as they were."""
-    cap, K = _check_reduce(order, topk_weights)
-    _want(z, "z", torch.bfloat16)
+    a = _Args()
     if z.dim() != 2 or z.shape[0] != order.num_slots:
         raise ValueError("z must be [%d, H]" % order.num_slots)
-    _want(y, "y", torch.bfloat16, (cap, z.shape[1]))
-    a = _Args()
-    _run(a, "miep_expert_reduce", a.p(z), z.shape[0], z.shape[1], a.p(order.row_slot), cap, K, _total_rows(a, order),
-         a.p(topk_weights), a.p(y))
+    slots, H = z.shape
+    row_slot, cap, K, total, weights = _reduce_args(a, order, topk_weights)
+    _run(a, "miep_expert_reduce", a.arg(z, "z", _BF16), slots, H, row_slot, cap, K, total, weights,
+         a.arg(y, "y", _BF16, (cap, H)))
 
 
 def expert_reduce(z: torch.Tensor, order: ExpertOrder, topk_weights: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -180,19 +168,16 @@ def expert_reduce(z: torch.Tensor, order: ExpertOrder, topk_weights: Optional[to
 def expert_reduce_backward_into(dy, z, order: ExpertOrder, dz, topk_weights=None, d_topk_weights=None) -> None:
     """Gradients of expert_reduce (allocates nothing): dz [slots, H], and d_topk_weights [cap, K] fp32 when given
     (then z is needed).  Slots that no entry names and rows behind the last received one are left as they were."""
-    cap, K = _check_reduce(order, topk_weights)
-    _want(dy, "dy", torch.bfloat16)
+    a = _Args()
+    row_slot, cap, K, total, weights = _reduce_args(a, order, topk_weights)
     if dy.dim() != 2 or dy.shape[0] != cap:
         raise ValueError("dy must be [%d, H]" % cap)
-    H = dy.shape[1]
-    _want(dz, "dz", torch.bfloat16, (order.num_slots, H))
-    _want(z, "z", torch.bfloat16, (order.num_slots, H))
-    _want(d_topk_weights, "d_topk_weights", torch.float32, (cap, K))
+    H, slots = dy.shape[1], order.num_slots
     if d_topk_weights is not None and z is None:
         raise ValueError("d_topk_weights needs z")
-    a = _Args()
-    _run(a, "miep_expert_reduce_backward", a.p(dy), a.p(z), order.num_slots, H, a.p(order.row_slot), cap, K,
-         _total_rows(a, order), a.p(topk_weights), a.p(dz), a.p(d_topk_weights))
+    _run(a, "miep_expert_reduce_backward", a.arg(dy, "dy", _BF16), a.opt(z, "z", _BF16, (slots, H)), slots, H, row_slot,
+         cap, K, total, weights, a.arg(dz, "dz", _BF16, (slots, H)),
+         a.opt(d_topk_weights, "d_topk_weights", _F32, (cap, K)))
 
 
 def expert_reduce_backward(dy: torch.Tensor, z: torch.Tensor, order: ExpertOrder,
@@ -214,9 +199,7 @@ def _check_product(x, w, groups: RowGroups, rows: int, row_index, wide: str):
     _, N, K = shape
     if channels != (K if wide == "K" else N):
         raise ValueError("rows of %d channels do not match w %s" % (channels, tuple(shape)))
-    if row_index is not None:
-        _want(row_index, "row_index", torch.int32, (rows,))
-    elif x_rows != rows:
+    if row_index is None and x_rows != rows:
         raise ValueError("x has %d rows, the output %d (and there is no row_index)" % (x_rows, rows))
     return x_rows, N, K
 
@@ -226,13 +209,10 @@ def grouped_gemm_into(x, w, groups: RowGroups, y, row_index=None, expected_rows:
     x, y = _flat(x, "x"), _flat(y, "y")
     rows = y.shape[0]
     x_rows, N, K = _check_product(x, w, groups, rows, row_index, "K")
-    _want(x, "x", torch.bfloat16)
-    _want(w, "w", torch.bfloat16)
-    _want(y, "y", torch.bfloat16, (rows, N))
     a = _Args()
     g = groups.c(a, rows)
-    _run(a, "miep_grouped_gemm", ctypes.byref(g), a.p(x), x_rows, a.p(w), N, K, a.p(row_index), int(expected_rows),
-         a.p(y))
+    _run(a, "miep_grouped_gemm", ctypes.byref(g), a.arg(x, "x", _BF16), x_rows, a.arg(w, "w", _BF16), N, K,
+         a.opt(row_index, "row_index", _I32, (rows,)), int(expected_rows), a.arg(y, "y", _BF16, (rows, N)))
 
 
 def grouped_gemm(x: torch.Tensor, w: torch.Tensor, groups: RowGroups, row_index: Optional[torch.Tensor] = None,
@@ -255,12 +235,10 @@ def grouped_gemm_dgrad_into(dy, w, groups: RowGroups, dx, expected_rows: int = 0
     dy, dx = _flat(dy, "dy"), _flat(dx, "dx")
     rows = dx.shape[0]
     _, N, K = _check_product(dy, w, groups, rows, None, "N")
-    _want(dy, "dy", torch.bfloat16)
-    _want(w, "w", torch.bfloat16)
-    _want(dx, "dx", torch.bfloat16, (rows, K))
     a = _Args()
     g = groups.c(a, rows)
-    _run(a, "miep_grouped_gemm_dgrad", ctypes.byref(g), a.p(dy), a.p(w), N, K, int(expected_rows), a.p(dx))
+    _run(a, "miep_grouped_gemm_dgrad", ctypes.byref(g), a.arg(dy, "dy", _BF16), a.arg(w, "w", _BF16), N, K,
+         int(expected_rows), a.arg(dx, "dx", _BF16, (rows, K)))
 
 
 def grouped_gemm_dgrad(dy: torch.Tensor, w: torch.Tensor, groups: RowGroups, expected_rows: int = 0) -> torch.Tensor:
@@ -278,15 +256,13 @@ def grouped_gemm_wgrad_into(dy, x, groups: RowGroups, dw, row_index=None, accumu
         raise TypeError("dw must be float32 or bfloat16, got %s" % dw.dtype)
     if accumulate and dw.dtype != torch.float32:
         raise TypeError("accumulate needs a float32 dw")
-    _want(dy, "dy", torch.bfloat16)
-    _want(x, "x", torch.bfloat16)
     rows = dy.shape[0]
     x_rows, N, K = _check_product(x, dw, groups, rows, row_index, "K")
-    _want(dy, "dy", torch.bfloat16, (rows, N))
     a = _Args()
     g = groups.c(a, rows)
-    _run(a, "miep_grouped_gemm_wgrad", ctypes.byref(g), a.p(dy), a.p(x), x_rows, a.p(row_index), N, K,
-         int(dw.dtype == torch.float32), int(bool(accumulate)), a.p(dw))
+    _run(a, "miep_grouped_gemm_wgrad", ctypes.byref(g), a.arg(dy, "dy", _BF16, (rows, N)), a.arg(x, "x", _BF16), x_rows,
+         a.opt(row_index, "row_index", _I32, (rows,)), N, K, int(dw.dtype == _F32), int(bool(accumulate)),
+         a.arg(dw, "dw", dw.dtype))
 
 
 def grouped_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, groups: RowGroups, row_index: Optional[torch.Tensor] = None,
@@ -302,22 +278,22 @@ def grouped_gemm_fp8_into(x, x_scales, w, w_scales, groups: RowGroups, y, row_in
                           expected_rows: int = 0) -> None:
     """grouped_gemm_fp8 into y (allocates nothing)."""
     x, x_scales, y = _flat(x, "x"), _flat(x_scales, "x_scales"), _flat(y, "y")
+    kind = x_scales.dtype
     for t, name in ((x, "x"), (w, "w")):
         if t.dtype not in _FP8:
             raise TypeError("%s must be float8_e4m3fn/uint8 codes, got %s" % (name, t.dtype))
-    if x_scales.dtype not in (torch.float32, torch.uint8):
-        raise TypeError("x_scales must be float32, or uint8 exponent bytes, got %s" % x_scales.dtype)
+    if kind != _F32 and kind != torch.uint8:
+        raise TypeError("x_scales must be float32, or uint8 exponent bytes, got %s" % kind)
     rows = y.shape[0]
     x_rows, N, K = _check_product(x, w, groups, rows, row_index, "K")
     if K % 128:
         raise ValueError("FP8 products need K % 128 == 0")
-    _want(x_scales, "x_scales", x_scales.dtype, (x_rows, K // 128))
-    _want(w_scales, "w_scales", x_scales.dtype, (w.shape[0], -(-N // 128), K // 128))
-    _want(y, "y", torch.bfloat16, (rows, N))
     a = _Args()
     g = groups.c(a, rows)
-    _run(a, "miep_grouped_gemm_fp8", ctypes.byref(g), a.p(x), a.p(x_scales), x_rows, a.p(w), a.p(w_scales),
-         int(x_scales.dtype == torch.uint8), N, K, a.p(row_index), int(expected_rows), a.p(y))
+    _run(a, "miep_grouped_gemm_fp8", ctypes.byref(g), a.arg(x, "x", x.dtype),
+         a.arg(x_scales, "x_scales", kind, (x_rows, K // 128)), x_rows, a.arg(w, "w", w.dtype),
+         a.arg(w_scales, "w_scales", kind, (w.shape[0], -(-N // 128), K // 128)), int(kind == torch.uint8), N, K,
+         a.opt(row_index, "row_index", _I32, (rows,)), int(expected_rows), a.arg(y, "y", _BF16, (rows, N)))
 
 
 def grouped_gemm_fp8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
@@ -336,22 +312,21 @@ def grouped_gemm_fp8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w
 
 
 # --------------------------------------------------------------------------- activation
-def _check_h(h, name="h"):
-    h = _flat(h, name)
-    _want(h, name, torch.bfloat16)
-    if h.shape[1] % 2:
-        raise ValueError("%s must be [rows, 2 * inner]" % name)
-    return h, h.shape[0], h.shape[1] // 2
+def _check_h(h):
+    h = _flat(h, "h")
+    rows, width = h.shape
+    if width % 2:
+        raise ValueError("h must be [rows, 2 * inner]")
+    return h, rows, width // 2
 
 
 def swiglu_into(h, groups: RowGroups, a_out) -> None:
     """swiglu into a_out [rows, inner] bf16 (allocates nothing)."""
     h, rows, inner = _check_h(h)
     out = _flat(a_out, "a")
-    _want(out, "a", torch.bfloat16, (rows, inner))
     a = _Args()
     g = groups.c(a, rows)
-    _run(a, "miep_swiglu", ctypes.byref(g), a.p(h), inner, a.p(out))
+    _run(a, "miep_swiglu", ctypes.byref(g), a.arg(h, "h", _BF16), inner, a.arg(out, "a", _BF16, (rows, inner)))
 
 
 def swiglu(h: torch.Tensor, groups: RowGroups) -> torch.Tensor:
@@ -368,16 +343,17 @@ def swiglu_fp8_into(h, groups: RowGroups, a_out, a_scales, round_scale: bool = F
     if inner % 128:
         raise ValueError("the FP8 cast needs inner % 128 == 0")
     out, scales = _flat(a_out, "a"), _flat(a_scales, "a_scales")
-    if out.dtype not in _FP8 or tuple(out.shape) != (rows, inner):
+    if out.dtype not in _FP8 or out.shape != (rows, inner):
         raise TypeError("a must be [%d, %d] E4M3 codes" % (rows, inner))
-    _want(scales, "a_scales", torch.float32, (rows, inner // 128))
     ue = _flat(a_scales_ue8m0, "a_scales_ue8m0") if a_scales_ue8m0 is not None else None
-    _want(ue, "a_scales_ue8m0", torch.uint8, (rows, inner // 128))
     if ue is not None and not round_scale:
         raise ValueError("a_scales_ue8m0 needs round_scale=True")
     a = _Args()
     g = groups.c(a, rows)
-    _run(a, "miep_swiglu_fp8", ctypes.byref(g), a.p(h), inner, int(bool(round_scale)), a.p(out), a.p(scales), a.p(ue))
+    blocks = (rows, inner // 128)
+    _run(a, "miep_swiglu_fp8", ctypes.byref(g), a.arg(h, "h", _BF16), inner, int(bool(round_scale)),
+         a.arg(out, "a", out.dtype), a.arg(scales, "a_scales", _F32, blocks),
+         a.opt(ue, "a_scales_ue8m0", torch.uint8, blocks))
 
 
 def swiglu_fp8(h: torch.Tensor, groups: RowGroups, round_scale: bool = False, use_ue8m0: bool = False):
@@ -398,11 +374,10 @@ def swiglu_backward_into(da, h, groups: RowGroups, dh) -> None:
     """swiglu_backward into dh [rows, 2 * inner], which may be h itself (allocates nothing)."""
     h, rows, inner = _check_h(h)
     da, out = _flat(da, "da"), _flat(dh, "dh")
-    _want(da, "da", torch.bfloat16, (rows, inner))
-    _want(out, "dh", torch.bfloat16, (rows, 2 * inner))
     a = _Args()
     g = groups.c(a, rows)
-    _run(a, "miep_swiglu_backward", ctypes.byref(g), a.p(da), a.p(h), inner, a.p(out))
+    _run(a, "miep_swiglu_backward", ctypes.byref(g), a.arg(da, "da", _BF16, (rows, inner)), a.arg(h, "h", _BF16), inner,
+         a.arg(out, "dh", _BF16, (rows, 2 * inner)))
 
 
 def swiglu_backward(da: torch.Tensor, h: torch.Tensor, groups: RowGroups) -> torch.Tensor:
