@@ -7,7 +7,9 @@
 // the second starts every counter at its expert's first slot plus the entries
 // of the parts (and, in the part, of the wavefronts) before it, and gives out
 // slots 64 entries at a time, equal experts in lane order.  No counter is
-// shared between wavefronts then, so the order never depends on timing.  16384
+// shared between wavefronts then, so the order never depends on timing.  A few
+// entries are counted by every workgroup of the placing kernel for itself: one
+// launch instead of two.  16384
 // tokens' top-8 over 64 ranks (12 MB to move) take 12.8 us, of which two launches
 // are about 7: bound by those and a memory latency each.
 #include "device.h"
@@ -64,6 +66,12 @@ __global__ __launch_bounds__(kOrderThreads) void order_count_kernel(OrderArgs a)
   for (int l = threadIdx.x; l < a.L; l += kOrderThreads) out[l] = count[l];
 }
 
+// One launch, a part a rank, up to this many entries and experts (a call for 64
+// tokens' top-8 over 8 ranks 7.3 us against 9.7, with 4096 entries 8.4 against
+// 10.5; with 8192 the same, and over 64 ranks 14 against 10.6).
+constexpr int kOneEntries = kOrderHold * kOrderThreads, kOneExperts = 2048;
+
+template <bool ONE>
 __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs a) {
   __shared__ int next[kOrderWaves][kMaxLocalExperts];   // each wavefront's next slot per expert
   __shared__ int sums[512], waves[kOrderWaves];
@@ -80,7 +88,32 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs a)
   hold(a, i0 + lane, i1, kWave, held);
 
   for (int l = tid; l < kOrderWaves * a.L; l += kOrderThreads) next[l / a.L][l % a.L] = 0;
+  __shared__ int total[ONE ? kOneExperts : 1], from[ONE ? kMaxRanks + 1 : 1];
+  if constexpr (ONE) {
+    for (int e = tid; e < a.E; e += kOrderThreads) total[e] = 0;
+    for (int q = tid; q <= a.R; q += kOrderThreads)
+      from[q] = static_cast<int>(min(max(static_cast<int64_t>(a.off[q]), static_cast<int64_t>(0)), a.rows));
+  }
   __syncthreads();
+  if constexpr (ONE) {
+    const int end = from[a.R] * a.K;
+    for (int i = tid; i < end; i += kBlock * kOrderWaves) {
+      int e[kOrderHold];
+      hold(a, i, end, kOrderThreads, e);
+#pragma unroll
+      for (int k = 0; k < kOrderHold; ++k) {
+        if (e[k] < 0) continue;
+        const int row = fdiv(i + k * kOrderThreads, a.Kdiv);
+        int lo = 0, hi = a.R;                                         // the row's rank: the last that begins at or before it
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) / 2;
+          if (from[mid] <= row) lo = mid;
+          else hi = mid;
+        }
+        atomicAdd(&total[lo * a.L + e[k]], 1);
+      }
+    }
+  }
   for (int64_t i = i0; i < i1; i += kBlock) {
     if (i != i0) hold(a, i + lane, i1, kWave, held);
 #pragma unroll
@@ -99,7 +132,9 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs a)
     int all = 0, before = 0;
     if (e < a.E)
       for (int q = tid / width; q < a.parts; q += kOrderThreads / width) {
-        const int c = a.counts[static_cast<int64_t>(q) * a.E + e];
+        int c;
+        if constexpr (ONE) c = total[e];
+        else c = a.counts[static_cast<int64_t>(q) * a.E + e];
         all += c;
         before += q < p ? c : 0;
       }
@@ -186,8 +221,12 @@ hipError_t launch_order(const OrderArgs& args, hipStream_t st) {
   if (want < a.parts) a.parts = want < 1 ? 1 : static_cast<int>(want);
   const int64_t grid = static_cast<int64_t>(a.parts) * a.R;
   if (grid > max_blocks(kOrderThreads)) return hipErrorInvalidConfiguration;
+  if (a.parts == 1 && a.rows * a.K <= kOneEntries && a.E <= kOneExperts) {
+    order_place_kernel<true><<<static_cast<unsigned>(grid), kOrderThreads, 0, st>>>(a);
+    return hipGetLastError();
+  }
   order_count_kernel<<<static_cast<unsigned>(grid), kOrderThreads, 0, st>>>(a);
-  order_place_kernel<<<static_cast<unsigned>(grid), kOrderThreads, 0, st>>>(a);
+  order_place_kernel<false><<<static_cast<unsigned>(grid), kOrderThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -718,6 +718,9 @@ def received(R, L, K, per_rank, cap, g, dead=0.3):
     (64, 4, 8, [17 * (i % 5) for i in range(64)], 40, 4, 4),
     (3, 64, 64, [0, 0, 333], 2, 1, 7),
     (2, 7, 4, [0, 0], 3, 1, 1),
+    (2, 8, 4, [500, 524], 0, 1, 128),
+    (2, 8, 4, [500, 525], 0, 1, 128),
+    (16, 128, 2, [0, 9, 0, 0, 100] + [7] * 9 + [0, 0], 4, 8, 16),
 ])
 def test_expert_order(R, L, K, per_rank, spare, align, parts):
     say("order", R, L, K, align, parts)
