@@ -520,9 +520,10 @@ __device__ __forceinline__ void rows_tiles(const GemmRowsArgs& a, int total, uin
       // bytes a lane) with all of Q's.  P's operands come a slot ahead through
       // a ring of two; Q's are held over the step and each replaced by the
       // next step's behind its last use, so the barrier lies before the last
-      // slot.  fp32 scales multiply each block's fp32 sum into the result (the
-      // MFMAs start from zero); power-of-two scales go into the MFMAs as their
-      // exponent bytes.
+      // slot.  fp32 scales multiply each block's sum into the result in fp32
+      // (the MFMAs start from zero); power-of-two scales go into the MFMAs as
+      // their exponent bytes, and the running sum through them.  What the MFMAs
+      // keep of their products is said in gemm.h.
       i32x8 pf[2], qf[TQ];
       float s[TQ];
       int e[TQ], ep = 0;
