@@ -30,9 +30,9 @@ __device__ __forceinline__ uint64_t ballot(bool p) { return __ballot(p); }
 // Uniform broadcast of lane `src` (src must be wave-uniform).
 __device__ __forceinline__ int readlane(int v, int src) { return __builtin_amdgcn_readlane(v, src); }
 
-// floor(n / f.d) for 0 <= n with n * f.d < 2^40 (see FastDiv).
+// floor(n / f.d) for every n >= 0 (see FastDiv).
 __host__ __device__ __forceinline__ int fdiv(int n, const FastDiv& f) {
-  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * f.m) >> 40);
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * f.m) >> f.shift);
 }
 
 // Inclusive scan across the 64 lanes of a wavefront.

@@ -19,20 +19,23 @@ constexpr int kMaxExperts = 8192;  // experts (LDS histogram bound)
 constexpr int kStatusCapacity = 4; // device status word value of MIEP_ECAPACITY
 
 // Division by a launch constant without the ~30-instruction integer divide:
-// floor(n / d) = (n * m) >> 40 with m = ceil(2^40 / d).  Writing m = (2^40 +
-// e) / d with 0 <= e < d, the product overshoots n/d by n*e / (d * 2^40) <
-// n / 2^40, which stays below the 1/d gap to the next integer whenever
-// n * d < 2^40.  Uses: expert / experts-per-rank (both <= 8192, always
-// exact) and token / tokens-per-channel (exact for T <= 2^20, which the
-// kernels check before taking it).
+// floor(n / d) = (n * m) >> shift with shift = 31 + ceil(log2 d) and m =
+// ceil(2^shift / d), which is at least 2^31 and below 2^32.  Writing m =
+// (2^shift + e) / d with 0 <= e < d, the product overshoots n / d by n * e /
+// (d * 2^shift), below the 1 / d gap to the next integer because n * e < 2^31
+// * d <= 2^shift; and n * m < 2^63.  So it is exact for every 0 <= n < 2^31
+// and 1 <= d < 2^31.
 struct FastDiv {
-  uint64_t m;
+  uint32_t m;
+  int shift;
   int d;
 };
 inline FastDiv make_fastdiv(int d) {
   FastDiv f;
   f.d = d > 0 ? d : 1;
-  f.m = ((1ull << 40) + static_cast<uint64_t>(f.d) - 1) / static_cast<uint64_t>(f.d);
+  f.shift = 31;
+  while ((1ll << (f.shift - 31)) < f.d) ++f.shift;
+  f.m = static_cast<uint32_t>(((1ull << f.shift) + static_cast<uint64_t>(f.d) - 1) / static_cast<uint64_t>(f.d));
   return f;
 }
 

@@ -265,7 +265,6 @@ __global__ __launch_bounds__(1024) void notify_kernel(NotifyArgs a) {
   __syncthreads();
 
   const int tc = a.tcdiv.d;
-  const bool fast_tc = T <= (1 << 20);                // FastDiv is exact there
   int fin[MW];                                        // tokens of s per rank (wavefront 0, after the loop)
 #pragma unroll
   for (int i = 0; i < MW; ++i) fin[i] = 0;
@@ -328,7 +327,7 @@ __global__ __launch_bounds__(1024) void notify_kernel(NotifyArgs a) {
     // pass 2: exclusive rank within source s -> send_head, channel prefixes.
     // Lane j holds rank r0 + j's bases in registers; per-rank values come by
     // readlane, so no lane walks a dependent LDS chain.
-    const int ch = fast_tc ? fdiv(t, a.tcdiv) : t / tc;   // channel of token t
+    const int ch = fdiv(t, a.tcdiv);   // channel of token t
     const bool last_in_channel = valid && (t - ch * tc == tc - 1 || t == T - 1);
     const uint64_t clast = ballot(last_in_channel);
     if constexpr (kWide) {
@@ -834,7 +833,7 @@ __global__ __launch_bounds__(256) void notify_chan_kernel(NotifyArgs a, int cpw)
   // every channel that ends on a token of this wavefront
   {
     const int t = t0 + tid;
-    const int ch = T <= (1 << 20) ? fdiv(t, a.tcdiv) : t / tc;   // FastDiv is exact below 2^20
+    const int ch = fdiv(t, a.tcdiv);
     const bool last_in_channel = mine && (t - ch * tc == tc - 1 || t == T - 1);
     const uint64_t clast = ballot(last_in_channel);
     for (uint64_t cl = clast; cl != 0; cl &= cl - 1) {

@@ -214,7 +214,7 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs a)
 
 hipError_t launch_order(const OrderArgs& args, hipStream_t st) {
   OrderArgs a = args;
-  a.Kdiv = make_fastdiv(a.K);                                        // entries stay below 2^31, K <= 64
+  a.Kdiv = make_fastdiv(a.K);                                        // entries stay below 2^31
   // a part is worth the entries that its lanes hold: fewer leave more to sum up than to sort
   constexpr int kPart = kOrderHold * kOrderThreads;
   const int64_t want = (a.rows * a.K / a.R + kPart - 1) / kPart;
