@@ -84,6 +84,10 @@ template <class T>
 __device__ __forceinline__ T lds_read(uint32_t at) {
   return *reinterpret_cast<const __attribute__((address_space(3))) T*>(at);
 }
+template <class T>
+__device__ __forceinline__ void lds_write(uint32_t at, const T& v) {
+  *reinterpret_cast<__attribute__((address_space(3))) T*>(at) = v;
+}
 __device__ __forceinline__ i16x4 lds_read_tr(uint32_t at) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) i16x4*>(at));
 }

@@ -100,18 +100,19 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
   auto q_at = [&](int buf) MIEP_INLINE { return lds + NSP * S::kPBytes + buf * (S::kQBytes + S::kIndexBytes); };
   // A gathered row's address; a row behind the group's last, or without a
   // source, reads zeros.
+  auto sourced = [&](int src) MIEP_INLINE { return src >= 0 && src < a.p_rows; };
   auto gathered = [&](int i, int step, int src) MIEP_INLINE {
-    const bool in = step * S::kRows + prow + i * PR < rows && src >= 0 && src < a.p_rows;
+    const bool in = step * S::kRows + prow + i * PR < rows && sourced(src);
     return in ? static_cast<const void*>(pbase + src * ldp + poff[i]) : static_cast<const void*>(g_zero16);
   };
   // Load i of a step of 64 whole rows (gathered: of any).  The indices of a
   // gathered step come with the Q loads two steps before its own loads, those
   // of step u + 1 in the place behind Q's step u.
+  auto index_at = [&](int step, int row) MIEP_INLINE { return lds_read<int>(q_at((step - 1) & 1) + S::kQBytes + row * 4); };
   auto load_p = [&](int i, int step, int buf) MIEP_INLINE {
     const uint32_t to = p_at(buf) + (i * S::kWaves + wave) * 1024;
     if constexpr (GATHER) {
-      const int src = lds_read<int>(q_at((step - 1) & 1) + S::kQBytes + (prow + i * PR) * 4);
-      dma16(gathered(i, step, src), to);
+      dma16(gathered(i, step, index_at(step, prow + i * PR)), to);
     } else {
       dma16s(pbase + static_cast<int64_t>(step) * S::kRows * ldp, poff[i], to);
     }
@@ -149,6 +150,19 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
     }
   };
 
+  // dY's row that goes with one without a source may hold NaN or infinities,
+  // which zeros on the other side do not take away: once it has come, and
+  // before the barrier that publishes it, its place is overwritten with zeros,
+  // by the lanes that loaded it.  (Rows without a source are rare: choosing
+  // every load's address instead took 4% of a long group's time.)
+  auto clear_lost = [&](uint64_t lost, int buf) MIEP_INLINE {
+    if (lost == 0) return;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < QL; ++i)
+      if (lost >> (qrow + i * QR) & 1) lds_write(q_at(buf) + (i * S::kWaves + wave) * 1024 + lane * 16, i32x4{0, 0, 0, 0});
+  };
+
   f32x4 acc[TP][TQ];
 #pragma unroll
   for (int i = 0; i < TP; ++i)
@@ -170,19 +184,25 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
     // The order of loads, waits and barriers is the rows kernel's: step t
     // issues P's step t - 1 + NSP over its MFMAs and, behind its barrier, Q's
     // step t + NSQ.
+    uint64_t lost = 0;
 #pragma unroll
     for (int t = -NSP; t < 0; ++t) {
       if (t - 1 + NSP >= 0) {
         if constexpr (GATHER) {                                       // step 0: its indices straight from memory
+          const int src = a.row_index[begin + min(lane, rows - 1)];
+          lost = ballot(!sourced(src));
+          int from[S::kPLoads];
 #pragma unroll
-          for (int i = 0; i < S::kPLoads; ++i)
-            dma16(gathered(i, 0, a.row_index[begin + min(prow + i * PR, rows - 1)]), p_at(0) + (i * S::kWaves + wave) * 1024);
+          for (int i = 0; i < S::kPLoads; ++i) from[i] = __shfl(src, prow + i * PR);
+#pragma unroll
+          for (int i = 0; i < S::kPLoads; ++i) dma16(gathered(i, 0, from[i]), p_at(0) + (i * S::kWaves + wave) * 1024);
         } else {
           issue_p(t - 1 + NSP, t - 1 + NSP);
         }
       }
       if (t + NSQ >= 0) issue_q(t + NSQ, t + NSQ);
     }
+    if constexpr (GATHER) clear_lost(lost, 0);
     if (nk >= NSP) wait_tiles<S::kBehind + S::kQLoads>();
     else wait_tiles<0>();
     auto publish = [&](int step) MIEP_INLINE {
@@ -213,11 +233,16 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_weight_kernel(GemmWei
       pbuf = pbuf == NSP - 1 ? 0 : pbuf + 1;
       qbuf = qbuf == NSQ - 1 ? 0 : qbuf + 1;
       if constexpr (!more) issue_p(step - 1 + NSP, before(pb));
+      int src = 0;
+      if constexpr (GATHER && !last) src = index_at(step + 1, lane);
 #pragma unroll
       for (int k = 0; k < SLOTS; ++k) {
         const int late = k - (SLOTS - D);
         if constexpr (!last)
-          if (late == 0) publish(step);
+          if (late == 0) {
+            if constexpr (GATHER) clear_lost(ballot(!sourced(src)), qbuf);
+            publish(step);
+          }
         if (k + D < SLOTS) read_p(k + D, p_at(pb));
         else if constexpr (!last) read_p(k + D - SLOTS, p_at(pbuf));
         if (k < TP) {
@@ -356,15 +381,15 @@ __global__ __launch_bounds__(512, 2) void gemm_weight_split_kernel(GemmWeightArg
       if (p0 + pc / 2 >= a.K) pc = 0;
       if (q0 + qc / 2 >= a.N) qc = 0;
       bool in = r < rows;
-      const uint8_t* q = qbase + r * ldq + qc;
-      dma16(in ? static_cast<const void*>(q) : static_cast<const void*>(g_zero16), mine + (2 * buf + 1) * S::kBytes + i * 1024);
       const uint8_t* p;
-      if constexpr (GATHER) {
+      if constexpr (GATHER) {                                         // a row without a source: zeros from both
         in = in && src[i] >= 0 && src[i] < a.p_rows;
         p = pbase + src[i] * ldp + pc;
       } else {
         p = pbase + r * ldp + pc;
       }
+      const uint8_t* q = qbase + r * ldq + qc;
+      dma16(in ? static_cast<const void*>(q) : static_cast<const void*>(g_zero16), mine + (2 * buf + 1) * S::kBytes + i * 1024);
       dma16(in ? static_cast<const void*>(p) : static_cast<const void*>(g_zero16), mine + 2 * buf * S::kBytes + i * 1024);
     }
   };

@@ -469,7 +469,7 @@ miep_status miep_grouped_gemm_dgrad(const miep_row_groups* g, const uint16_t* dy
  * rows i of group g of dy[i][n] * x[src(i)][k], summed in fp32.
  *   dw_f32      1: dw is fp32; 0: bf16, rounded once
  *   accumulate  1 (fp32 only): added to what dw holds.  0: dw is overwritten, with zeros for an empty group.
- * Rows whose row_index is outside [0, x_rows) contribute nothing. */
+ * Rows whose row_index is outside [0, x_rows) contribute nothing, whatever dy holds there. */
 miep_status miep_grouped_gemm_wgrad(const miep_row_groups* g, const uint16_t* dy, const uint16_t* x, int64_t x_rows,
                                     const int32_t* row_index, int32_t n, int32_t k, int32_t dw_f32,
                                     int32_t accumulate, void* dw, void* stream);
