@@ -147,3 +147,112 @@ def test_sums_norm_wise(kind, K):
             most = float(BF_HALF * want.norm() + K ** 0.5 * ULP * mag.norm()) + (float(cuts[i].norm()) if cuts else 0.0)
             assert off <= most, (kind, i, off, most)
             assert most < 0.9 * float(want.norm()) / K ** 0.5   # (of the oracle: one product is more than the tolerance)
+
+
+# ------------------------------------------------------------------ workgroups that walk several tiles
+def make(kind, rows, N, K, expected, src=None, seed=0):
+    """(call, checks): the call's product over groups of these rows, and for every group (its rows, 64-bit operands)."""
+    G, begin = len(rows), np.cumsum([0] + [n + i % 3 for i, n in enumerate(rows)][:-1]).tolist()
+    total = begin[-1] + rows[-1] + 2
+    gd = torch.Generator(device=DEV).manual_seed(seed + N + K)
+    rnd = lambda *s: torch.randn(s, generator=gd, device=DEV)  # noqa: E731
+    gather, grp = "gather" in kind, groups_of(rows, begin)
+    src = (src or 700) if gather else total
+    index = torch.randint(-1, src, (total,), generator=gd, device=DEV, dtype=torch.int32) if gather else None
+    kw = dict(row_index=index, expected_rows=expected) if gather else dict(expected_rows=expected)
+    y = torch.full((total, N), MARK, dtype=BF, device=DEV)
+    x, w = rnd(src, K), rnd(G, K, N) if kind == "dgrad" else rnd(G, N, K)
+    if "8" not in kind:
+        x, w = x.to(BF), w.to(BF)
+        if kind == "dgrad":
+            call = lambda: miep.grouped_gemm_dgrad_into(x, w, grp, y, **kw)  # noqa: E731
+        else:
+            call = lambda: miep.grouped_gemm_into(x, w, grp, y, **kw)  # noqa: E731
+        xd, wd = x.double(), [(t if kind == "dgrad" else t.T).double().contiguous() for t in w]
+    else:
+        pow2 = "ue8m0" in kind
+        xq, xs = quant_rows(x.cpu(), pow2)
+        wq, ws = quant_blocks(w.cpu(), pow2)
+        arg = ue8m0_bytes if pow2 else (lambda s: s)
+        args = [t.to(DEV) for t in (xq, arg(xs), wq, arg(ws))]
+        call = lambda: miep.grouped_gemm_fp8_into(*args, grp, y, **kw)  # noqa: E731
+        xd = xq.to(DEV).float().double() * xs.to(DEV).double().repeat_interleave(128, 1)
+        big = ws.to(DEV).double().repeat_interleave(128, 1)[:, :N].repeat_interleave(128, 2)
+        wd = [(wq[i].to(DEV).float().double() * big[i]).T.contiguous() for i in range(G)]
+    if gather:
+        xd = torch.where((index >= 0).unsqueeze(1), xd[index.long().clamp_min(0)], 0.0)
+    parts_ = [(b, n, xd[b:b + n], wd[i]) for i, (n, b) in enumerate(zip(rows, begin)) if n]
+    return call, y, parts_, members(rows, begin, total).to(DEV)
+
+
+def verify(kind, K, y, groups, live):
+    assert bool((y[~live] == MARK).all())
+    for b, n, a, c in groups:
+        want, mag = a @ c, a.abs() @ c.abs()
+        # E4M3: also the cuts, at most 7 * 2^-13 of every group's largest factors (normal-sized codes: within 2^3 of 2^e)
+        tol = BF_HALF * want.abs() + (K + (K // 128 + 3 if "8" in kind else 0)) * ULP * mag
+        if "8" in kind:
+            top = lambda t: t.abs().reshape(t.shape[0], K // 8, 8).amax(2)  # noqa: E731
+            tol = tol + 7 * 2.0 ** -13 * (top(a) @ top(c.T.contiguous()).T)
+        off = (y[b:b + n].double() - want).abs() > tol
+        assert not bool(off.any()), (kind, b, n, off.nonzero()[:4].tolist())
+
+
+# 24 groups whose rows are up to three tiles of 192 or 256, some whole and some a few rows short, under 12 tiles of 128
+# channels: 684 tiles for 256 workgroups.  144 tiles of 256 channels by the expected rows are too few for the wide
+# kernel, and 576 of 128 x 128 too many for that one.  A contraction of 2 to 8 steps (buffers are three or four deep),
+# the last one short where the type allows.
+def many_tiles(tile):
+    return [3 * tile, 3 * tile - 1, 2 * tile, 3 * tile - 5, tile, 3 * tile, tile - 1, 3 * tile - 63] * 3
+
+
+def steps(kind, n):
+    return n * 128 if "8" in kind else n * 64 - (8 if n % 4 == 3 else 0)
+
+
+@pytest.mark.parametrize("nk", [2, 3, 4, 7, 8])
+@pytest.mark.parametrize("tile,expected", [(192, 150), (256, 230)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_rounds_of_narrow_tiles(kind, tile, expected, nk):
+    say("narrow tiles", kind, tile, nk)
+    K = steps(kind, nk)
+    call, y, groups, live = make(kind, many_tiles(tile), 1416, K, expected)
+    call()
+    verify(kind, K, y, groups, live)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_tiles_give_the_same_every_time(kind):
+    """Repeated, in a graph beside eager work, and on two streams at once: workgroups of several tiles each."""
+    say("repeated", kind)
+    problems = [make(kind, many_tiles(tile), 1416, steps(kind, 7), expected, seed=tile) for tile, expected in ((192, 150), (256, 230))]
+    problems.append(make(kind, [256 - i % 7 for i in range(70)], 1040, steps(kind, 5), 256))   # the wide kernel's
+    first = []
+    for call, y, groups, live in problems:
+        call()
+        first.append(y.clone())
+    for _ in range(10):
+        for (call, y, _, _), want in zip(problems, first):
+            y.fill_(MARK)
+            call()
+            assert torch.equal(y, want)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(DEV) for _ in problems]
+    for _ in range(5):
+        for (call, y, _, _), st in zip(problems, streams):
+            with torch.cuda.stream(st):
+                y.fill_(MARK)
+                call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for (_, y, _, _), want in zip(problems, first))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for call, *_ in problems:
+            call()
+    for _ in range(4):
+        for _, y, _, _ in problems:
+            y.fill_(MARK)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want) for (_, y, _, _), want in zip(problems, first))
+        problems[0][0]()
