@@ -256,3 +256,96 @@ def test_many_tiles_give_the_same_every_time(kind):
         torch.cuda.synchronize()
         assert all(torch.equal(y, want) for (_, y, _, _), want in zip(problems, first))
         problems[0][0]()
+
+
+# ------------------------------------------------------------------ the tile kernels past 32 bits of byte offset
+# Contractions of 16 or 8 steps (the split kernel takes 24 and more).  Only the rows that some group or index names hold numbers.
+def far_rows(rows, K, at, g, fp8):
+    """[rows, K] whose rows ``at`` are random, and those rows in 64 bits; E4M3: with fp32 scales of random size."""
+    if not fp8:
+        x = torch.zeros((rows, K), dtype=BF, device=DEV)
+        x[at] = torch.randn((len(at), K), generator=g, device=DEV).to(BF)
+        return x, None, x[at].double()
+    x = torch.zeros((rows, K), dtype=torch.uint8, device=DEV)
+    x[at] = (torch.randn((len(at), K), generator=g, device=DEV) * 50).to(F8).view(torch.uint8)
+    s = torch.zeros((rows, K // 128), device=DEV)
+    s[at] = torch.exp2(torch.randint(-4, 5, (len(at), K // 128), generator=g, device=DEV).float())
+    return x, s, x[at].view(F8).float().double() * s[at].double().repeat_interleave(128, 1)
+
+
+@pytest.mark.parametrize("expected,N,G", [(4, 72, 3), (100, 136, 3), (256, 1040, 48)])   # tiles of 32 and 128 rows, and the wide ones
+@pytest.mark.parametrize("kind", KINDS)
+def test_tiles_past_four_gigabytes(kind, expected, N, G):
+    say("far rows", kind, expected)
+    fp8 = "8" in kind
+    K = 1024
+    rows = (2 ** 32 + 2 ** 28) // (K if fp8 else 2 * K)      # the source's bytes pass 2^32
+    g = torch.Generator(device=DEV).manual_seed(expected)
+    border = 2 ** 32 // (K if fp8 else 2 * K)
+    at = [0, border - 1, border, border + 1] + list(range(rows - 60, rows))
+    x, xs, xd = far_rows(rows, K, at, g, fp8)
+    w = torch.randn((G, K, N) if kind == "dgrad" else (G, N, K), generator=g, device=DEV).to(BF)
+    if fp8:
+        w = (w.float() * 50).to(F8)
+        ws = torch.exp2(torch.randint(-4, 5, (G, -(-N // 128), K // 128), generator=g, device=DEV).float())
+    wd = lambda i: (w[i].double() if kind == "dgrad" else w[i].double().T.contiguous() if not fp8 else  # noqa: E731
+                    (w[i].float().double() * ws[i].double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)).T.contiguous())
+    if "gather" in kind:
+        pick = torch.randint(0, len(at), (70,), generator=g, device=DEV)
+        pick[:6] = torch.tensor([0, 1, 2, 3, 4, 63], device=DEV)
+        index = torch.tensor(at, device=DEV)[pick].int()
+        count, begin = [0] * (G - 2) + [30, 40], [0] * (G - 1) + [30]
+        y = torch.full((70, N), MARK, dtype=BF, device=DEV)
+        spans = [(G - 2, slice(0, 30), xd[pick[:30]]), (G - 1, slice(30, 70), xd[pick[30:]])]
+    else:
+        index = None
+        count, begin = [1, 3] + [0] * (G - 3) + [60], [0, border - 1] + [7] * (G - 3) + [rows - 60]
+        y = torch.full((rows, N), MARK, dtype=BF, device=DEV)
+        spans = [(0, slice(0, 1), xd[:1]), (1, slice(border - 1, border + 2), xd[1:4]), (G - 1, slice(rows - 60, rows), xd[4:])]
+    grp = groups_of(count, begin)
+    kw = dict(expected_rows=expected) if kind == "dgrad" else dict(expected_rows=expected, row_index=index)
+    if fp8:
+        arg = ue8m0_far if "ue8m0" in kind else (lambda s: s)
+        miep.grouped_gemm_fp8_into(x, arg(xs), w, arg(ws), grp, y, **kw)
+    elif kind == "dgrad":
+        miep.grouped_gemm_dgrad_into(x, w, grp, y, **kw)
+    else:
+        miep.grouped_gemm_into(x, w, grp, y, **kw)
+    for i, span, a in spans:
+        verify(kind, K, y, [(span.start, span.stop - span.start, a, wd(i))], torch.ones(y.shape[0], dtype=torch.bool, device=DEV))
+    if index is None:
+        assert bool((y[1:border - 1] == MARK).all()) and bool((y[border + 2:rows - 60] == MARK).all())
+
+
+def ue8m0_far(s):
+    return torch.where(s > 0, torch.log2(s) + 127, 0.0).to(torch.uint8)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("N", [512, 1024])                   # tiles of 128 and, with all the groups' 256 of them, of 256
+def test_weight_tiles_past_four_gigabytes(N, gather):
+    say("far weights", N, gather)
+    K, G = 1024, 33
+    rows = (2 ** 32 + 2 ** 28) // (2 * K)
+    border = 2 ** 32 // (2 * K)
+    g = torch.Generator(device=DEV).manual_seed(N)
+    at = [0, border - 1, border, border + 1] + list(range(rows - 150, rows))
+    x, _, xd = far_rows(rows, K, at, g, False)
+    if gather:
+        pick = torch.randint(0, len(at), (154,), generator=g, device=DEV)
+        pick[:6] = torch.tensor([0, 1, 2, 3, 4, 153], device=DEV)
+        index = torch.tensor(at, device=DEV)[pick].int()
+        count, begin = [4] + [0] * (G - 2) + [150], [0] + [4] * (G - 1)
+        dy = torch.randn((154, N), generator=g, device=DEV).to(BF)
+        spans = [(0, dy[:4], xd[pick[:4]]), (G - 1, dy[4:], xd[pick[4:]])]
+        dw = miep.grouped_gemm_wgrad(dy, x, groups_of(count, begin), row_index=index)
+    else:
+        dy, _, dd = far_rows(rows, N, at, g, False)
+        count, begin = [1, 3] + [0] * (G - 3) + [150], [0, border - 1] + [7] * (G - 3) + [rows - 150]
+        spans = [(0, dd[:1], xd[:1]), (1, dd[1:4], xd[1:4]), (G - 1, dd[4:], xd[4:])]
+        dw = miep.grouped_gemm_wgrad(dy, x, groups_of(count, begin))
+    for i, d, v in spans:
+        d, v = d.double().T.contiguous(), v
+        want, mag = d @ v, d.abs() @ v.abs()
+        assert bool(((dw[i].double() - want).abs() <= (v.shape[0] + 1) * ULP * mag).all()), i
+    assert not bool(dw[2:G - 1].any())
