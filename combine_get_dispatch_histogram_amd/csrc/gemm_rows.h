@@ -7,10 +7,12 @@
 // A workgroup computes BQ rows x BP output channels.  Each 128-byte step of
 // the contraction comes to LDS by asynchronous 16-byte loads, several buffers deep,
 // with one barrier a step; wavefront (wp, wq) multiplies its BP/WP x BQ/WQ part
-// with 16x16 MFMAs.  16384 rows over 4 even groups of 4096 x 7168: bf16 741 us,
-// 1,300 TFLOP/s at 1.9 GHz (a library's large product reaches 1,450), E4M3 468
-// us, with power-of-two scales 408 us, 2,360 TFLOP/s (library 3,180).  A few
-// rows a group: bound by the weights' bytes, 6.0 to 6.3 TB/s.
+// with 16x16 MFMAs.  16384 rows over 4 even groups of 4096 x 7168: bf16 726 us,
+// 1,325 TFLOP/s at 1.9 GHz (a library's large product reaches 1,450), E4M3 463
+// us, 2,080 TFLOP/s, with power-of-two scales 405 us, 2,370 (library 3,180).  A
+// few rows a group: bound by the weights' bytes (8 x 4096 x 7168: bf16 79 us,
+// 6.0 TB/s; E4M3 42 us, 5.6 TB/s, and 34 us where the last-level cache still
+// holds part of the same weights from the call before).
 #pragma once
 
 #include <cmath>

@@ -10,7 +10,7 @@
 // shared between wavefronts then, so the order never depends on timing.  A few
 // entries are counted by every workgroup of the placing kernel for itself: one
 // launch instead of two.  16384
-// tokens' top-8 over 64 ranks (12 MB to move) take 12.8 us, of which two launches
+// tokens' top-8 over 64 ranks (12 MB to move) take 12.2 us, of which two launches
 // are about 7: bound by those and a memory latency each.
 #include "device.h"
 #include "kernels.h"
@@ -242,7 +242,7 @@ __device__ __forceinline__ v4u narrow(const float (&f)[8]) {
 // One workgroup a row; a thread owns 8 channels at a time.  The row's slots
 // and weights are read by the lanes k of every wavefront and broadcast.
 // Terms are added in ascending k in fp32, one rounding to bf16.  Bound by
-// memory: 4096 rows of 7168 with 97 MB of slots and results take 18 us, 5.4 TB/s;
+// memory: 4096 slots of 7168 to 2,700 rows (97 MB) take 18 us, 5.4 TB/s;
 // four slots' loads are in flight at a time.
 __global__ __launch_bounds__(256) void reduce_kernel(ReduceArgs a) {
   const int lane = lane_id();

@@ -7,8 +7,8 @@
 // in fp32 from bf16, rounded once: to bf16, or cast to E4M3 by the dispatch's
 // rule (a scale per 128 channels) straight from the fp32 value, so that the
 // low-latency path's second product reads codes that were rounded once.
-// Bound by memory: a row is 4*I bytes read and I to 2*I written (backward 6*I
-// and 4*I: 16384 rows of 2 x 2048 take 54 us, 6.2 TB/s).  A lane owns 8 channels (16-byte loads of gate and up); sixteen
+// Bound by memory at I = 2048 and more: a row is 4*I bytes read and I to 2*I
+// written (backward 6*I and 4*I: 16384 rows of 2 x 2048 take 54 us, 6.2 TB/s).  A lane owns 8 channels (16-byte loads of gate and up); sixteen
 // lanes hold one scale's 128.
 #include "gemm.h"
 
@@ -102,7 +102,11 @@ __global__ __launch_bounds__(256) void swiglu_kernel(SwigluArgs a) {
 hipError_t launch_swiglu(const SwigluArgs& args, int kind, hipStream_t st) {
   SwigluArgs a = args;
   if (a.g.G == 0 || a.g.limit == 0) return hipSuccess;
-  // One row a workgroup at a time (16384 rows of 2 x 2048, backward: 61 us; 4 rows 65, 8 rows 72).
+  // One row a workgroup at a time (16384 rows of 2 x 2048, backward: 61 us; 4
+  // rows 65, 8 rows 72).  Chosen at that width, where a row is 256 lanes' work;
+  // narrower rows leave lanes idle, and 16384 rows take (bf16 / E4M3 / backward)
+  // 35 / 37 / 52 us at 2048, 28 / 32 / 39 at 1408, 23 / 26 / 30 at 768 and 21 /
+  // 22 / 26 at 512, where their bytes would take 8 / 7 / 13.
   a.rows_per_tile = 1;
   const int64_t most = a.g.limit + a.g.G;
   const unsigned grid = static_cast<unsigned>(most < 2048 ? most : 2048);

@@ -222,7 +222,7 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, groups: RowGroups, row_index:
     x [rows, K] (or [G, block, K]), w [G, N, K].  ``row_index`` [slots] int32 gathers: src(i) = row_index[i] (a
     negative one gives a zero row) and y has one row per entry; without it src(i) = i.  ``expected_rows`` is the
     rows a group is expected to hold (default: the layout's rows / G); it only chooses the tile size, so give it
-    where the layout is mostly empty, as the low-latency one is.
+    where the layout is mostly empty, as the low-latency one is and an order's of worst-case slots.
     """
     lead = x.shape[:-1] if row_index is None else tuple(row_index.shape)
     y = torch.empty((*lead, w.shape[1]), dtype=torch.bfloat16, device=x.device)

@@ -451,7 +451,8 @@ miep_status miep_expert_reduce_backward(const uint16_t* dy, const uint16_t* z, i
  *             outside [0, x_rows) gives zeros.  A gathered x is at most 64 GiB.
  *   w         [num_groups][N][K] bf16;  y [num_rows][N] bf16 out
  *   expected_rows  rows a group is expected to hold, 0 = num_rows / num_groups: chooses the tile,
- *             never the result's meaning.  Give it where the layout is mostly empty (low latency).
+ *             never the result's meaning.  Give it where the layout is mostly empty (low latency, or slots
+ *             for the worst case): 29 rows in 8 blocks of 256 take 79 us with it and 108 without.
  * x, w, y 16-byte aligned; N % 8 == 0, K % 8 == 0, both at most 2^21, and
  * (num_rows / 32 + 1 + num_groups) * (max(N, K) / 128 + 1) at most 2^31-2^16.
  * Errors: EINVAL for null pointers or sizes, EUNSUPPORTED for the limits above. */
