@@ -10,8 +10,9 @@
 // With few rows a group the fp32 result is most of the traffic (4 N K bytes a
 // group), so it leaves in whole 128-byte lines (see the stores): 32 ragged groups
 // of 8192 rows, 7168 x 2048, take 496 us, of which the stores alone 308 and the
-// rest alone 271 (a bf16 result 403, added to an fp32 one 998, gathered 514).  With many rows the MFMAs and their LDS reads bound it: 16384
-// rows over 4 groups 404 us, 1,190 TFLOP/s.
+// rest alone 271 (a bf16 result 403, added to an fp32 one 998, gathered 514).
+// With many rows the MFMAs and their LDS reads bound it: 16384 rows over 4
+// groups 404 us, 1,190 TFLOP/s, of 4096 x 7168 785 us, 1,225.
 #include <type_traits>
 
 #include "gemm.h"

@@ -8,8 +8,9 @@
 // rule (a scale per 128 channels) straight from the fp32 value, so that the
 // low-latency path's second product reads codes that were rounded once.
 // Bound by memory at I = 2048 and more: a row is 4*I bytes read and I to 2*I
-// written (backward 6*I and 4*I: 16384 rows of 2 x 2048 take 54 us, 6.2 TB/s).  A lane owns 8 channels (16-byte loads of gate and up); sixteen
-// lanes hold one scale's 128.
+// written (backward 6*I and 4*I: 16384 rows of 2 x 2048 take 54 us, 6.2 TB/s).
+// A lane owns 8 channels (16-byte loads of gate and up); sixteen lanes hold one
+// scale's 128.
 #include "gemm.h"
 
 namespace miep {
