@@ -19,6 +19,8 @@ sections 4.1-4.3, for ranks that are partitions of one GPU):
   update_mask_buffer / clean_mask_buffer / query_mask_buffer        rank masking
   expert_order, grouped_gemm (+ _dgrad, _wgrad, _fp8), swiglu (+ _fp8, _backward), expert_reduce (+ _backward):
   what the experts compute between dispatch and combine (experts.py)
+  gate_topk (+ _backward), linear (+ _backward), expert_layer (+ _fp8): the block around them, and the whole layer
+  for a few tokens (layer.py)
 The ``*_into`` variants take preallocated outputs and allocate nothing.
 """
 from __future__ import annotations
@@ -37,6 +39,9 @@ from .experts import (ExpertOrder, RowGroups, expert_order, expert_order_into, e
                       grouped_gemm_dgrad_into, grouped_gemm_fp8, grouped_gemm_fp8_into, grouped_gemm_into,
                       grouped_gemm_wgrad, grouped_gemm_wgrad_into, swiglu, swiglu_backward, swiglu_backward_into,
                       swiglu_fp8, swiglu_fp8_into, swiglu_into)
+from .layer import (expert_layer, expert_layer_fp8, expert_layer_fp8_into, expert_layer_into, gate_topk,
+                    gate_topk_backward, gate_topk_backward_into, gate_topk_into, linear, linear_backward,
+                    linear_backward_into, linear_into)
 
 __all__ = ["Handle", "MiepError", "get_dispatch_layout", "get_dispatch_layout_into", "dispatch", "dispatch_into", "cached_dispatch",
            "cached_dispatch_into", "combine", "combine_into", "low_latency_dispatch", "low_latency_dispatch_into",
@@ -49,7 +54,10 @@ __all__ = ["Handle", "MiepError", "get_dispatch_layout", "get_dispatch_layout_in
            "expert_reduce_backward", "expert_reduce_backward_into", "grouped_gemm", "grouped_gemm_into",
            "grouped_gemm_dgrad", "grouped_gemm_dgrad_into", "grouped_gemm_wgrad", "grouped_gemm_wgrad_into",
            "grouped_gemm_fp8", "grouped_gemm_fp8_into", "swiglu", "swiglu_into", "swiglu_fp8", "swiglu_fp8_into",
-           "swiglu_backward", "swiglu_backward_into"]
+           "swiglu_backward", "swiglu_backward_into",
+           "gate_topk", "gate_topk_into", "gate_topk_backward", "gate_topk_backward_into", "linear", "linear_into",
+           "linear_backward", "linear_backward_into", "expert_layer", "expert_layer_into", "expert_layer_fp8",
+           "expert_layer_fp8_into"]
 
 
 def version() -> str:

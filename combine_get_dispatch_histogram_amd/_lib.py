@@ -21,6 +21,8 @@ EXPORTS = ("miep_get_dispatch_layout", "miep_dispatch", "miep_cached_dispatch", 
            "miep_expert_order", "miep_expert_reduce", "miep_expert_reduce_backward", "miep_grouped_gemm",
            "miep_grouped_gemm_dgrad", "miep_grouped_gemm_wgrad", "miep_grouped_gemm_fp8", "miep_swiglu",
            "miep_swiglu_fp8", "miep_swiglu_backward",
+           "miep_gate_topk", "miep_gate_topk_backward", "miep_linear", "miep_linear_act_backward", "miep_linear_dgrad",
+           "miep_linear_wgrad", "miep_expert_layer", "miep_expert_layer_fp8",
            "miep_last_error", "miep_version")
 
 
@@ -53,6 +55,19 @@ class LLProblem(ctypes.Structure):
 class RowGroupsC(ctypes.Structure):
     _fields_ = [("begin", ctypes.c_void_p), ("rows", ctypes.c_void_p), ("num_rows", ctypes.c_int64),
                 ("num_groups", ctypes.c_int32), ("stride", ctypes.c_int32)]
+
+
+class GateC(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int64), ("num_experts", ctypes.c_int32), ("num_topk", ctypes.c_int32),
+                ("sigmoid", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("num_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_best", ctypes.c_int32), ("logits_f32", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class LayerC(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_topk", ctypes.c_int32), ("num_experts", ctypes.c_int32),
+                ("hidden", ctypes.c_int32), ("inner", ctypes.c_int32), ("scales_ue8m0", ctypes.c_int32),
+                ("first_expert", ctypes.c_int64)]
 
 
 class MiepError(RuntimeError):
@@ -105,6 +120,18 @@ def load() -> ctypes.CDLL:
         lib.miep_swiglu.argtypes = [groups, _P, _I32, _P, _P]
         lib.miep_swiglu_fp8.argtypes = [groups, _P, _I32, _I32, _P, _P, _P, _P]
         lib.miep_swiglu_backward.argtypes = [groups, _P, _P, _I32, _P, _P]
+        gate, layer = ctypes.POINTER(GateC), ctypes.POINTER(LayerC)
+        lib.miep_gate_topk.argtypes = [gate, _P, _P, _P, _P, _P]
+        lib.miep_gate_topk_backward.argtypes = [gate, _P, _P, _P, _P, _P]
+        lib.miep_linear.argtypes = [_P, _I64, _P, _I32, _I32, _P, _I32, _P, _P, _P, _I32, _P]
+        lib.miep_linear_act_backward.argtypes = [_P, _I32, _P, _I64, _I32, _I32, _P, _P, _I32, _P, _I32, _P]
+        lib.miep_linear_dgrad.argtypes = [_P, _I64, _P, _I32, _I32, _P, _P]
+        lib.miep_linear_wgrad.argtypes = [_P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P]
+        lib.miep_expert_layer.argtypes = [layer] + [_P] * 9
+        lib.miep_expert_layer_fp8.argtypes = [layer] + [_P] * 11
+        for f in ("miep_gate_topk", "miep_gate_topk_backward", "miep_linear", "miep_linear_act_backward",
+                  "miep_linear_dgrad", "miep_linear_wgrad", "miep_expert_layer", "miep_expert_layer_fp8"):
+            getattr(lib, f).restype = ctypes.c_int
         for f in ("miep_expert_order", "miep_expert_reduce", "miep_expert_reduce_backward", "miep_grouped_gemm",
                   "miep_grouped_gemm_dgrad", "miep_grouped_gemm_wgrad", "miep_grouped_gemm_fp8", "miep_swiglu",
                   "miep_swiglu_fp8", "miep_swiglu_backward"):

@@ -23,7 +23,7 @@ OBJ = os.path.join(ROOT, "_build", "miep")
 LIB = os.path.join(HERE, "libmiep.so")
 
 SOURCES = ["api.cpp", "layout.hip", "notify.hip", "pack.hip", "combine.hip", "ll.hip", "relay.hip", "order.hip", "gemm.hip",
-           "gemm_fp8.hip", "gemm_weight.hip", "swiglu.hip"]
+           "gemm_fp8.hip", "gemm_weight.hip", "swiglu.hip", "gate.hip", "linear.hip", "gemm_linear.hip", "layer.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

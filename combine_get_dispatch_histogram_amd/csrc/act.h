@@ -1,0 +1,71 @@
+// act.h -- activations and their derivatives in fp32, shared by the epilogues.
+#pragma once
+
+#include "device.h"
+
+namespace miep {
+
+// exp(-g) to fp32 accuracy from the hardware's exp2: the product g * log2(e)
+// is carried in two parts, the low one applied to first order.  |g| is capped
+// where the sigmoid is 1 (or exp(-g) overflows and it is 0) to fp32.
+__device__ __forceinline__ float sigmoid(float g) {
+  const float c = -fminf(fmaxf(g, -100.f), 100.f);
+  const float hi = c * 1.44269502f;                                   // log2(e), rounded to fp32
+  const float lo = fmaf(c, 1.44269502f, -hi) + c * 1.92596299e-8f;    // and its rest
+  const float e = __builtin_amdgcn_exp2f(hi) * fmaf(lo, 0.693147182f, 1.f);   // infinity stays infinity
+  return __builtin_amdgcn_rcpf(1.f + e);
+}
+
+// The normal distribution function by formula 7.1.26 of Abramowitz and Stegun
+// (erfc to 1.5e-7, its tail a multiple of exp(-x*x)): 14 instructions a value
+// where the library's erff takes several times that, and an epilogue is not
+// hidden behind its product.  *density: exp(-z*z/2) / sqrt(2 pi).
+__device__ __forceinline__ float normal_cdf(float z, float* density) {
+  const float x = fabsf(z) * 0.707106781f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+  const float e = __builtin_amdgcn_exp2f(-x * x * 1.44269502f);
+  const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+  const float tail = 0.5f * poly * e;
+  *density = e * 0.398942280f;
+  return z < 0.f ? tail : 1.f - tail;
+}
+
+// gelu's tanh form is z * sigmoid(2u), u = sqrt(2/pi) * (z + 0.044715 z^3).
+__device__ __forceinline__ float gelu_tanh_sigmoid(float z) {
+  return sigmoid(1.59576912f * fmaf(0.044715f * z * z, z, z));
+}
+
+// f(z); kActNone and kActSwiglu (whose two halves a caller joins) give z.
+__device__ __forceinline__ float activate(float z, int act) {
+  float unused;
+  switch (act) {
+    case kActRelu: return z > 0.f || z != z ? z : 0.f;
+    case kActSilu: return z * sigmoid(z);
+    case kActGelu: return z * normal_cdf(z, &unused);
+    case kActGeluTanh: return z * gelu_tanh_sigmoid(z);
+    default: return z;
+  }
+}
+
+// f'(z)
+__device__ __forceinline__ float activate_slope(float z, int act) {
+  switch (act) {
+    case kActRelu: return z > 0.f ? 1.f : 0.f;
+    case kActSilu: {
+      const float s = sigmoid(z);
+      return s * (1.f + z * (1.f - s));
+    }
+    case kActGelu: {
+      float density;
+      const float cdf = normal_cdf(z, &density);
+      return fmaf(z, density, cdf);
+    }
+    case kActGeluTanh: {
+      const float s = gelu_tanh_sigmoid(z);
+      return s + z * s * (1.f - s) * (1.59576912f * fmaf(0.134145f * z, z, 1.f));
+    }
+    default: return 1.f;
+  }
+}
+
+}  // namespace miep

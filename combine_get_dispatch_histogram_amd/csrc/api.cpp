@@ -284,6 +284,103 @@ miep_status check_reduce(int64_t num_slots, int32_t hidden, const int32_t* row_s
   return MIEP_OK;
 }
 
+// A dense product of rows x k by n x k.
+miep_status check_linear(int64_t rows, int32_t n, int32_t k) {
+  if (rows < 0) return fail(MIEP_EINVAL, "rows must be >= 0");
+  if (rows > miep::kMostRows) return fail(MIEP_EUNSUPPORTED, "rows > 2^31 - 2^16");
+  if (n <= 0 || k <= 0) return fail(MIEP_EINVAL, "n and k must be > 0");
+  if (n % 8 != 0 || k % 8 != 0) return fail(MIEP_EUNSUPPORTED, "n and k must be multiples of 8 (16-byte rows)");
+  if (n > (1 << 21) || k > (1 << 21)) return fail(MIEP_EUNSUPPORTED, "n or k > 2^21");
+  if ((rows / 32 + 2) * ((n > k ? n : k) / 128 + 1) > miep::kMostTiles)
+    return fail(MIEP_EUNSUPPORTED, "more than 2^31 - 2^16 tiles of 32 rows x 128 columns");
+  return MIEP_OK;
+}
+
+miep_status check_activation(int32_t activation, int32_t n) {
+  if (activation < MIEP_ACT_NONE || activation > MIEP_ACT_SWIGLU) return fail(MIEP_EINVAL, "no activation %d", activation);
+  if (activation == MIEP_ACT_SWIGLU && n % 16 != 0)
+    return fail(MIEP_EUNSUPPORTED, "SwiGLU needs n %% 16 == 0 (16-byte rows of gate and up)");
+  return MIEP_OK;
+}
+
+miep::GroupArgs all_rows(int64_t rows) {
+  miep::GroupArgs g{};
+  g.G = 1;
+  g.limit = rows;
+  return g;
+}
+
+miep_status gate_args(const miep_gate* g, const void* logits, miep::GateArgs* a) {
+  if (!g) return fail(MIEP_EINVAL, "gate is NULL");
+  if (g->num_tokens < 0 || g->num_experts <= 0 || g->num_topk <= 0 || g->num_topk > g->num_experts)
+    return fail(MIEP_EINVAL, "num_tokens >= 0, num_experts > 0 and num_topk in [1, num_experts] are needed");
+  if (g->num_groups <= 0 || g->num_experts % g->num_groups != 0)
+    return fail(MIEP_EINVAL, "num_groups must divide num_experts");
+  if (g->topk_groups <= 0 || g->topk_groups > g->num_groups)
+    return fail(MIEP_EINVAL, "topk_groups must be in [1, num_groups]");
+  if (g->group_best != 1 && g->group_best != 2) return fail(MIEP_EINVAL, "group_best must be 1 or 2");
+  if (g->num_experts > miep::kGateExperts) return fail(MIEP_EUNSUPPORTED, "num_experts > %d", miep::kGateExperts);
+  if (g->num_topk > miep::kGateTopk) return fail(MIEP_EUNSUPPORTED, "num_topk > %d", miep::kGateTopk);
+  if (g->num_groups > miep::kGateGroups) return fail(MIEP_EUNSUPPORTED, "num_groups > %d", miep::kGateGroups);
+  if (g->num_tokens > kMaxRowsI32) return fail(MIEP_EUNSUPPORTED, "num_tokens > 2^31-1");
+  miep_status st = check_array(logits, g->num_tokens > 0, "logits");
+  if (st != MIEP_OK) return st;
+  a->N = g->num_tokens;
+  a->E = g->num_experts;
+  a->K = g->num_topk;
+  a->score = g->sigmoid ? miep::kGateSigmoid : miep::kGateSoftmax;
+  a->renorm = g->renormalize != 0;
+  a->groups = g->num_groups;
+  a->top_groups = g->topk_groups;
+  a->group_best = g->group_best;
+  a->scale = g->scale;
+  a->f32 = g->logits_f32 != 0;
+  a->logits = logits;
+  return MIEP_OK;
+}
+
+miep_status layer_args(const miep_layer* q, int type, const uint16_t* x, const int64_t* topk_idx,
+                       const float* topk_weights, const void* w1, const void* w2, const uint16_t* residual,
+                       uint16_t* workspace, uint16_t* y, miep::LayerArgs* a) {
+  if (!q) return fail(MIEP_EINVAL, "layer is NULL");
+  const int32_t N = q->num_tokens, K = q->num_topk, E = q->num_experts, H = q->hidden, I = q->inner;
+  if (N < 0 || K <= 0 || E <= 0 || H <= 0 || I <= 0) return fail(MIEP_EINVAL, "sizes must be positive");
+  if (N > miep::kLayerTokens) return fail(MIEP_EUNSUPPORTED, "num_tokens > %d", miep::kLayerTokens);
+  if (K > 64) return fail(MIEP_EUNSUPPORTED, "num_topk > 64");
+  const int unit = type == miep::kGemmBf16 ? 8 : miep::kFp8Group, bytes = type == miep::kGemmBf16 ? 2 : 1;
+  if (H % unit != 0 || I % unit != 0) return fail(MIEP_EUNSUPPORTED, "hidden and inner must be multiples of %d", unit);
+  if (H > (1 << 21) || I > (1 << 21)) return fail(MIEP_EUNSUPPORTED, "hidden or inner > 2^21");
+  if (2ll * I * H * bytes >= (1ll << 32)) return fail(MIEP_EUNSUPPORTED, "an expert's w1 of 4 GiB or more");
+  if (2ll * N * K * I >= (1ll << 32)) return fail(MIEP_EUNSUPPORTED, "a workspace of 4 GiB or more");
+  if (E > miep::kMaxExperts || miep::lists_layout(N, K, E).end > miep::kLayerListBytes)
+    return fail(MIEP_EUNSUPPORTED, "num_experts %d with %d x %d entries: the lists of experts need more than %d bytes", E,
+                N, K, miep::kLayerListBytes);
+  if (N > 0 && (!topk_idx || !topk_weights)) return fail(MIEP_EINVAL, "topk_idx / topk_weights NULL");
+  miep_status st;
+  if ((st = check_array(x, N > 0, "x")) != MIEP_OK) return st;
+  if ((st = check_array(w1, N > 0, "w1")) != MIEP_OK) return st;
+  if ((st = check_array(w2, N > 0, "w2")) != MIEP_OK) return st;
+  if ((st = check_array(residual, false, "residual")) != MIEP_OK) return st;
+  if ((st = check_array(workspace, N > 0, "workspace")) != MIEP_OK) return st;
+  if ((st = check_array(y, N > 0, "y")) != MIEP_OK) return st;
+  a->N = N;
+  a->K = K;
+  a->E = E;
+  a->H = H;
+  a->I = I;
+  a->first = q->first_expert;
+  a->type = type;
+  a->x = x;
+  a->idx = topk_idx;
+  a->wts = topk_weights;
+  a->w1 = w1;
+  a->w2 = w2;
+  a->residual = residual;
+  a->a = workspace;
+  a->y = y;
+  return MIEP_OK;
+}
+
 }  // namespace
 
 namespace miep {
@@ -1020,6 +1117,154 @@ miep_status miep_swiglu_backward(const miep_row_groups* g, const uint16_t* da, c
   a.out = dh;
   return hip_status(miep::launch_swiglu(a, miep::kSwigluBackward, static_cast<hipStream_t>(stream)),
                     "swiglu backward launch");
+}
+
+miep_status miep_gate_topk(const miep_gate* g, const void* logits, const float* bias, int64_t* topk_idx,
+                           float* topk_weights, void* stream) {
+  miep::GateArgs a{};
+  miep_status st = gate_args(g, logits, &a);
+  if (st != MIEP_OK) return st;
+  if (a.N > 0 && (!topk_idx || !topk_weights)) return fail(MIEP_EINVAL, "topk_idx / topk_weights NULL");
+  a.bias = bias;
+  a.idx = topk_idx;
+  a.w = topk_weights;
+  return hip_status(miep::launch_gate(a, false, static_cast<hipStream_t>(stream)), "gate launch");
+}
+
+miep_status miep_gate_topk_backward(const miep_gate* g, const float* d_topk_weights, const void* logits,
+                                    const int64_t* topk_idx, void* d_logits, void* stream) {
+  miep::GateArgs a{};
+  miep_status st = gate_args(g, logits, &a);
+  if (st == MIEP_OK) st = check_array(d_logits, a.N > 0, "d_logits");
+  if (st != MIEP_OK) return st;
+  if (a.N > 0 && (!topk_idx || !d_topk_weights)) return fail(MIEP_EINVAL, "topk_idx / d_topk_weights NULL");
+  a.idx = const_cast<int64_t*>(topk_idx);
+  a.d_w = d_topk_weights;
+  a.d_logits = d_logits;
+  return hip_status(miep::launch_gate(a, true, static_cast<hipStream_t>(stream)), "gate backward launch");
+}
+
+miep_status miep_linear(const uint16_t* x, int64_t rows, const uint16_t* w, int32_t n, int32_t k, const float* bias,
+                        int32_t activation, const uint16_t* residual, uint16_t* z, void* y, int32_t y_f32,
+                        void* stream) {
+  miep_status st = check_linear(rows, n, k);
+  if (st == MIEP_OK) st = check_activation(activation, n);
+  if (st != MIEP_OK) return st;
+  if (activation == MIEP_ACT_SWIGLU && (n + 1024ll) * k * 2 >= (1ll << 32))
+    return fail(MIEP_EUNSUPPORTED, "SwiGLU over a weight of 4 GiB (less 1024 rows) or more");
+  if ((st = check_array(x, rows > 0, "x")) != MIEP_OK) return st;
+  if ((st = check_array(w, rows > 0, "w")) != MIEP_OK) return st;
+  if ((st = check_array(bias, false, "bias")) != MIEP_OK) return st;
+  if ((st = check_array(residual, false, "residual")) != MIEP_OK) return st;
+  if ((st = check_array(z, false, "z")) != MIEP_OK) return st;
+  if ((st = check_array(y, rows > 0, "y")) != MIEP_OK) return st;
+  miep::LinearArgs a{};
+  a.rows = rows;
+  a.N = n;
+  a.K = k;
+  a.x = x;
+  a.w = w;
+  a.out = y;
+  a.epi.bias = bias;
+  a.epi.residual = residual;
+  a.epi.z = z;
+  a.epi.act = activation;
+  a.epi.out_f32 = y_f32 != 0;
+  return hip_status(miep::launch_linear(a, static_cast<hipStream_t>(stream)), "linear launch");
+}
+
+miep_status miep_linear_act_backward(const void* dy, int32_t dy_f32, const uint16_t* z, int64_t rows, int32_t n,
+                                     int32_t activation, uint16_t* dz, float* dbias, int32_t accumulate,
+                                     float* workspace, int32_t parts, void* stream) {
+  miep_status st = check_linear(rows, n, 8);
+  if (st == MIEP_OK) st = check_activation(activation, n);
+  if (st != MIEP_OK) return st;
+  if (dbias && parts <= 0) return fail(MIEP_EINVAL, "dbias needs a workspace of parts > 0");
+  if ((st = check_array(dy, rows > 0, "dy")) != MIEP_OK) return st;
+  if ((st = check_array(z, rows > 0 && activation != MIEP_ACT_NONE, "z")) != MIEP_OK) return st;
+  if ((st = check_array(dz, false, "dz")) != MIEP_OK) return st;
+  if ((st = check_array(dbias, false, "dbias")) != MIEP_OK) return st;
+  if ((st = check_array(workspace, dbias != nullptr, "workspace")) != MIEP_OK) return st;
+  if (!dz && !dbias) return MIEP_OK;
+  miep::ActBackwardArgs a{};
+  a.rows = rows;
+  a.N = n;
+  a.act = activation;
+  a.dy_f32 = dy_f32 != 0;
+  a.parts = parts;
+  a.dy = dy;
+  a.z = z;
+  a.dz = dz;
+  a.partial = workspace;
+  a.dbias = dbias;
+  a.accumulate = accumulate != 0;
+  return hip_status(miep::launch_act_backward(a, static_cast<hipStream_t>(stream)), "linear activation backward launch");
+}
+
+miep_status miep_linear_dgrad(const uint16_t* dy, int64_t rows, const uint16_t* w, int32_t n, int32_t k, uint16_t* dx,
+                              void* stream) {
+  miep_status st = check_linear(rows, n, k);
+  if (st == MIEP_OK) st = check_array(dy, rows > 0, "dy");
+  if (st == MIEP_OK) st = check_array(w, rows > 0, "w");
+  if (st == MIEP_OK) st = check_array(dx, rows > 0, "dx");
+  if (st != MIEP_OK) return st;
+  miep::GemmRowsArgs a{};
+  a.g = all_rows(rows);
+  a.q = dy;
+  a.p = w;
+  a.q_rows = rows;
+  a.C = n;
+  a.NO = k;
+  a.out = dx;
+  a.type = miep::kGemmBf16;
+  a.transposed = 1;
+  return hip_status(miep::launch_gemm_rows(a, static_cast<hipStream_t>(stream)), "linear dgrad launch");
+}
+
+miep_status miep_linear_wgrad(const uint16_t* dy, const uint16_t* x, int64_t rows, int32_t n, int32_t k,
+                              int32_t dw_f32, int32_t accumulate, void* dw, void* stream) {
+  miep_status st = check_linear(rows, n, k);
+  if (st == MIEP_OK) st = check_array(dy, rows > 0, "dy");
+  if (st == MIEP_OK) st = check_array(x, rows > 0, "x");
+  if (st == MIEP_OK) st = check_array(dw, true, "dw");
+  if (st != MIEP_OK) return st;
+  if (accumulate && !dw_f32) return fail(MIEP_EINVAL, "accumulate needs an fp32 dw");
+  if (static_cast<int64_t>((n + 127) / 128) * ((k + 127) / 128) > (1 << 24))
+    return fail(MIEP_EUNSUPPORTED, "dw has more than 2^24 tiles of 128 x 128");
+  miep::GemmWeightArgs a{};
+  a.g = all_rows(rows);
+  a.q = dy;
+  a.p = x;
+  a.p_rows = rows;
+  a.N = n;
+  a.K = k;
+  a.out = dw;
+  a.out_f32 = dw_f32 != 0;
+  a.accumulate = accumulate != 0;
+  return hip_status(miep::launch_gemm_weight(a, static_cast<hipStream_t>(stream)), "linear wgrad launch");
+}
+
+miep_status miep_expert_layer(const miep_layer* q, const uint16_t* x, const int64_t* topk_idx,
+                              const float* topk_weights, const uint16_t* w1, const uint16_t* w2,
+                              const uint16_t* residual, uint16_t* workspace, uint16_t* y, void* stream) {
+  miep::LayerArgs a{};
+  miep_status st = layer_args(q, miep::kGemmBf16, x, topk_idx, topk_weights, w1, w2, residual, workspace, y, &a);
+  if (st != MIEP_OK) return st;
+  return hip_status(miep::launch_layer(a, static_cast<hipStream_t>(stream)), "expert layer launch");
+}
+
+miep_status miep_expert_layer_fp8(const miep_layer* q, const uint16_t* x, const int64_t* topk_idx,
+                                  const float* topk_weights, const uint8_t* w1, const void* w1_scales,
+                                  const uint8_t* w2, const void* w2_scales, const uint16_t* residual,
+                                  uint16_t* workspace, uint16_t* y, void* stream) {
+  miep::LayerArgs a{};
+  const int type = q && q->scales_ue8m0 ? miep::kGemmFp8Ue8m0 : miep::kGemmFp8;
+  miep_status st = layer_args(q, type, x, topk_idx, topk_weights, w1, w2, residual, workspace, y, &a);
+  if (st != MIEP_OK) return st;
+  if (a.N > 0 && (!w1_scales || !w2_scales)) return fail(MIEP_EINVAL, "w1_scales / w2_scales NULL");
+  a.s1 = w1_scales;
+  a.s2 = w2_scales;
+  return hip_status(miep::launch_layer(a, static_cast<hipStream_t>(stream)), "expert layer fp8 launch");
 }
 
 }  // extern "C"

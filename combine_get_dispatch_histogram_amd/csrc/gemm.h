@@ -125,6 +125,11 @@ __device__ __forceinline__ void pin(f32x4& v) { asm volatile("" : "+v"(v)); }
 // ---- the groups' rows, never trusted: a group reads as the part of
 // [begin, begin + rows) inside [0, limit).
 __device__ __forceinline__ void group_range(const GroupArgs& g, int i, int64_t* begin, int* rows) {
+  if (!g.rows) {                                                      // one group: the whole layout
+    *begin = 0;
+    *rows = static_cast<int>(g.limit);
+    return;
+  }
   const int64_t b = g.begin ? g.begin[i] : static_cast<int64_t>(i) * g.stride;
   int64_t n = g.rows[i];
   if (!g.begin && n > g.stride) n = g.stride;

@@ -19,6 +19,7 @@
 #include <type_traits>
 
 #include "gemm.h"
+#include "gemm_epilogue.h"
 #include "gemm_rows_split.h"
 
 namespace miep {
@@ -58,8 +59,9 @@ struct RowsTile {
 // of the place, s the other three).
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 
-// One workgroup's tiles, of `total`; its LDS from `lds` on (kLds bytes).
-template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
+// One workgroup's tiles, of `total`; its LDS from `lds` on (kLds bytes).  EPI:
+// what happens to the results (gemm_epilogue.h).
+template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ, int EPI>
 __device__ __forceinline__ void rows_tiles(const GemmRowsArgs& a, int total, uint32_t lds) {
   using S = RowsTile<EL, PT, GATHER, BP, BQ, WP, WQ, NSP, NSQ>;
   constexpr int TP = S::kTP, TQ = S::kTQ, EB = S::kEB;
@@ -127,7 +129,7 @@ __device__ __forceinline__ void rows_tiles(const GemmRowsArgs& a, int total, uin
     pg = static_cast<const uint8_t*>(a.p) + static_cast<int64_t>(at.group) * NO * C * EB;
 
     // Sources of this lane's 16 bytes of every load of a stage.
-    pbase = pg + (PT ? static_cast<int64_t>(p0) * EB : static_cast<int64_t>(p0) * ldp);
+    pbase = pg + (PT ? static_cast<int64_t>(p0) * EB : static_cast<int64_t>(EPI == kEpiSwiglu ? p0 / 2 : p0) * ldp);
 #pragma unroll
     for (int i = 0; i < S::kPLoads; ++i) {
       const int l = i * S::kWaves + wave;
@@ -140,7 +142,8 @@ __device__ __forceinline__ void rows_tiles(const GemmRowsArgs& a, int total, uin
       } else {
         int row = l * 8 + lane / 8;
         const int c = (lane & 7) ^ swz(row);
-        if (p0 + row >= NO) row = NO - 1 - p0;
+        if constexpr (EPI == kEpiSwiglu) row = swiglu_row(p0, row, NO);
+        else if (p0 + row >= NO) row = NO - 1 - p0;
         poff[i] = static_cast<uint32_t>(row * ldp + c * 16);
       }
     }
@@ -628,8 +631,23 @@ __device__ __forceinline__ void rows_tiles(const GemmRowsArgs& a, int total, uin
       const v4u v = pack_pair(acc[i][j], acc[i + 1][j]);
       return GATHER && (out_none >> j & 1) ? v4u{0u, 0u, 0u, 0u} : v;
     };
-    stored = out_live == BQ && out_p0 + BP <= NO;
-    if (stored) {
+    stored = EPI == kEpiNone && out_live == BQ && out_p0 + BP <= NO;
+    if constexpr (EPI != kEpiNone) {
+      if (busy) {
+#pragma unroll
+        for (int j = 0; j < TQ; ++j) {
+          const int row = (wq * TQ + j) * 16 + m;
+          if (row >= out_live) continue;
+          const EpilogueRow to(a.epi, a.out, out_row0 + row, NO);
+#pragma unroll
+          for (int i = 0; i < TP; i += EPI == kEpiSwiglu ? 4 : 2) {
+            const int p = out_p0 + (wp * TP + i) * 16;
+            if constexpr (EPI == kEpiSwiglu) to.swiglu(p / 2, quarter, acc[i][j], acc[i + 1][j], acc[i + 2][j], acc[i + 3][j]);
+            else to.plain(p, quarter, acc[i][j], acc[i + 1][j]);
+          }
+        }
+      }
+    } else if (stored) {
 #pragma unroll
       for (int j = 0; j < TQ; ++j) {
         uint16_t* o = a.out + (out_row0 + (wq * TQ + j) * 16 + m) * NO + out_p0 + (wp * TP + (quarter & 1)) * 16 + (quarter >> 1) * 8;
@@ -654,10 +672,10 @@ __device__ __forceinline__ void rows_tiles(const GemmRowsArgs& a, int total, uin
   }
 }
 
-template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
+template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ, int EPI>
 __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsArgs a) {
   __shared__ __align__(1024) uint8_t lds_mem[RowsTile<EL, PT, GATHER, BP, BQ, WP, WQ, NSP, NSQ>::kLds];
-  rows_tiles<EL, PT, GATHER, BP, BQ, WP, WQ, NSP, NSQ>(a, count_tiles(a.g, BQ, (a.NO + BP - 1) / BP),
+  rows_tiles<EL, PT, GATHER, BP, BQ, WP, WQ, NSP, NSQ, EPI>(a, count_tiles(a.g, BQ, (a.NO + BP - 1) / BP),
                                                        (uint32_t)(uintptr_t)(lds_byte*)lds_mem);
 }
 
@@ -667,7 +685,7 @@ __global__ __launch_bounds__(WP * WQ * kWave, 2) void gemm_rows_kernel(GemmRowsA
 // 4096 x 2048, 151 and 190 of 7168 x 2048's gradient).  32 groups, bf16: of 256
 // rows each 218 us in 256s and 321 in 192s (gradient of 7168 x 2048); of 300
 // rows 224 and 183 (4096 x 2048).
-template <int EL, bool PT, bool GATHER>
+template <int EL, bool PT, bool GATHER, int EPI>
 __global__ __launch_bounds__(8 * kWave, 2) void gemm_rows_wide_kernel(GemmRowsArgs a) {
   constexpr int NSP = EL == kGemmBf16 ? 3 : 2;
   constexpr int kLds192 = RowsTile<EL, PT, GATHER, 256, 192, 2, 4, 3, 2>::kLds;
@@ -678,12 +696,12 @@ __global__ __launch_bounds__(8 * kWave, 2) void gemm_rows_wide_kernel(GemmRowsAr
   const int t192 = count_tiles(a.g, 192, ntiles), t256 = count_tiles(a.g, 256, ntiles);
   const int64_t grid = gridDim.x;
   if ((t192 + grid - 1) / grid * 5 < (t256 + grid - 1) / grid * 6)
-    rows_tiles<EL, PT, GATHER, 256, 192, 2, 4, 3, 2>(a, t192, lds);
+    rows_tiles<EL, PT, GATHER, 256, 192, 2, 4, 3, 2, EPI>(a, t192, lds);
   else
-    rows_tiles<EL, PT, GATHER, 256, 256, 2, 4, NSP, 2>(a, t256, lds);
+    rows_tiles<EL, PT, GATHER, 256, 256, 2, 4, NSP, 2, EPI>(a, t256, lds);
 }
 
-template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ>
+template <int EL, bool PT, bool GATHER, int BP, int BQ, int WP, int WQ, int NSP, int NSQ, int EPI = kEpiNone>
 hipError_t launch_rows_tile(const GemmRowsArgs& a, hipStream_t st) {
   const int64_t per = (a.NO + BP - 1) / BP;
   const int64_t most = ((a.g.limit + BQ - 1) / BQ + a.g.G) * per;     // disjoint groups have no more tiles
@@ -694,11 +712,11 @@ hipError_t launch_rows_tile(const GemmRowsArgs& a, hipStream_t st) {
   per_cu = per_cu < by_waves ? per_cu : by_waves;
   int64_t grid = 256ll * (per_cu > 0 ? per_cu : 1);
   if (grid > (most + 7) / 8 * 8) grid = (most + 7) / 8 * 8;
-  gemm_rows_kernel<EL, PT, GATHER, BP, BQ, WP, WQ, NSP, NSQ><<<static_cast<unsigned>(grid), WP * WQ * kWave, 0, st>>>(a);
+  gemm_rows_kernel<EL, PT, GATHER, BP, BQ, WP, WQ, NSP, NSQ, EPI><<<static_cast<unsigned>(grid), WP * WQ * kWave, 0, st>>>(a);
   return hipGetLastError();
 }
 
-template <int EL, bool PT, bool GATHER>
+template <int EL, bool PT, bool GATHER, int EPI = kEpiNone>
 hipError_t launch_rows(const GemmRowsArgs& a, hipStream_t st) {
   constexpr bool F8 = EL != kGemmBf16;
   // Few tiles over a long contraction: split it (bf16, us against the tiles
@@ -707,7 +725,7 @@ hipError_t launch_rows(const GemmRowsArgs& a, hipStream_t st) {
   // 16 steps only, 100 rows of 1 x 256 x 1024, 13 -> 14.5).
   const int64_t tiles32 = a.g.G * ((static_cast<int64_t>(a.expected) + 31) / 32) * ((a.NO + 31) / 32);
   if (tiles32 <= 256 && a.C / (F8 ? 128 : 64) >= 24 && split_tiles(a) <= kMostTiles)
-    return launch_rows_split<EL, PT, GATHER>(a, st);
+    return launch_rows_split<EL, PT, GATHER, EPI>(a, st);
   // Rows that most groups stay under when e are expected and chance spreads
   // them (a binomial count's deviation is at most sqrt(e)).
   const int64_t e = a.expected + static_cast<int64_t>(std::sqrt(static_cast<double>(a.expected)));
@@ -716,20 +734,21 @@ hipError_t launch_rows(const GemmRowsArgs& a, hipStream_t st) {
   //   A few rows: the weights stream past them.  128 x 32, two workgroups a
   //   CU, against 128 x 128: 16 rows 84 / 85.5, 4 rows 82 / 81, 16 rows of
   //   7168 x 2048 36 / 38, E4M3 21.2 / 25.7.
-  if (e <= 24) return launch_rows_tile<EL, PT, GATHER, 128, 32, 4, 1, F8 ? 3 : 4, F8 ? 3 : 4>(a, st);
+  if constexpr (EPI == kEpiNone)                                      // (a linear product of so few rows has its own kernel)
+    if (e <= 24) return launch_rows_tile<EL, PT, GATHER, 128, 32, 4, 1, F8 ? 3 : 4, F8 ? 3 : 4>(a, st);
   const int64_t wide = (a.NO + 255) / 256, narrow = (a.NO + 127) / 128;
   if (a.g.G * wide * ((e + 255) / 256) >= 192) {
     // enough tiles of 256 channels for the GPU's 256 CUs
-    gemm_rows_wide_kernel<EL, PT, GATHER><<<256, 8 * kWave, 0, st>>>(a);
+    gemm_rows_wide_kernel<EL, PT, GATHER, EPI><<<256, 8 * kWave, 0, st>>>(a);
     return hipGetLastError();
   }
   //   Fewer: 128 channels, as many rows as a group needs: 128 x 128 / 192 /
   //   256 at 64 rows 92 / 92 / 100, at 128 rows 160 / 106 / 110, at 180 rows
   //   (some groups more than 192) 145 / 186 / 123.
   if (e <= 108 || a.g.G * narrow * ((e + 127) / 128) <= 256)
-    return launch_rows_tile<EL, PT, GATHER, 128, 128, 2, 4, F8 ? 4 : 5, F8 ? 4 : 5>(a, st);
-  if (e <= 192) return launch_rows_tile<EL, PT, GATHER, 128, 192, 2, 4, F8 ? 3 : 4, F8 ? 3 : 4>(a, st);
-  return launch_rows_tile<EL, PT, GATHER, 128, 256, 2, 4, 3, 3>(a, st);
+    return launch_rows_tile<EL, PT, GATHER, 128, 128, 2, 4, F8 ? 4 : 5, F8 ? 4 : 5, EPI>(a, st);
+  if (e <= 192) return launch_rows_tile<EL, PT, GATHER, 128, 192, 2, 4, F8 ? 3 : 4, F8 ? 3 : 4, EPI>(a, st);
+  return launch_rows_tile<EL, PT, GATHER, 128, 256, 2, 4, 3, 3, EPI>(a, st);
 }
 
 }  // namespace miep

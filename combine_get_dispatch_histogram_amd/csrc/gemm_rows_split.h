@@ -8,6 +8,7 @@
 #pragma once
 
 #include "gemm.h"
+#include "gemm_epilogue.h"
 
 namespace miep {
 
@@ -26,7 +27,7 @@ struct RowsSplit {
 // Transposed P: 64 contraction rows of 32 channels, 64 bytes each.
 __device__ __forceinline__ int swz_t32(int row) { return (row >> 2) & 2; }
 
-template <int EL, bool PT, bool GATHER>
+template <int EL, bool PT, bool GATHER, int EPI>
 __global__ __launch_bounds__(512, 2) void gemm_rows_split_kernel(GemmRowsArgs a) {
   using S = RowsSplit<EL>;
   constexpr int EB = S::kFp8 ? 1 : 2, KE = kStepBytes / EB;
@@ -68,7 +69,8 @@ __global__ __launch_bounds__(512, 2) void gemm_rows_split_kernel(GemmRowsArgs a)
         pptr[i] = pg + row * ldp + static_cast<int64_t>(p0) * EB + col;
       } else {
         const int row = i * 8 + lane / 8;
-        pptr[i] = pg + static_cast<int64_t>(min(p0 + row, NO - 1)) * ldp + ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+        const int at_row = EPI == kEpiSwiglu ? p0 / 2 + swiglu_row(p0, row, NO) : min(p0 + row, NO - 1);
+        pptr[i] = pg + static_cast<int64_t>(at_row) * ldp + ((lane & 7) ^ ((row >> 1) & 7)) * 16;
       }
       const int row = i * 8 + lane / 8;
       int64_t src = row0 + min(row, live - 1);
@@ -201,7 +203,19 @@ __global__ __launch_bounds__(512, 2) void gemm_rows_split_kernel(GemmRowsArgs a)
         x += s[0];
         y += s[1];
       }
-      if (row < live && p0 + p < NO) {
+      if constexpr (EPI == kEpiSwiglu) {
+        // a tile's 16 gate columns lie before its 16 up columns
+        const float* s = reinterpret_cast<const float*>(lds_mem) + row * S::kPitch + p + 16;
+        float ux = 0.f, uy = 0.f;
+#pragma unroll
+        for (int w = 0; w < S::kWaves; ++w) {
+          ux += s[w * (2 * S::kStage / 4)];
+          uy += s[w * (2 * S::kStage / 4) + 1];
+        }
+        if (row < live && p < 16 && p0 / 2 + p < NO / 2) EpilogueRow(a.epi, a.out, row0 + row, NO).swiglu2(p0 / 2 + p, x, y, ux, uy);
+      } else if constexpr (EPI == kEpiPlain) {
+        if (row < live && p0 + p < NO) EpilogueRow(a.epi, a.out, row0 + row, NO).plain2(p0 + p, x, y);
+      } else if (row < live && p0 + p < NO) {
         bool none = false;
         if constexpr (GATHER) {
           const int src = a.row_index[row0 + row];
@@ -219,10 +233,10 @@ inline int64_t split_tiles(const GemmRowsArgs& a) {
   return ((a.g.limit + 31) / 32 + a.g.G) * ((static_cast<int64_t>(a.NO) + 31) / 32);
 }
 
-template <int EL, bool PT, bool GATHER>
+template <int EL, bool PT, bool GATHER, int EPI>
 hipError_t launch_rows_split(const GemmRowsArgs& a, hipStream_t st) {
   const int64_t most = split_tiles(a);
-  gemm_rows_split_kernel<EL, PT, GATHER><<<static_cast<unsigned>(most < 256 ? most : 256), 512, 0, st>>>(a);
+  gemm_rows_split_kernel<EL, PT, GATHER, EPI><<<static_cast<unsigned>(most < 256 ? most : 256), 512, 0, st>>>(a);
   return hipGetLastError();
 }
 

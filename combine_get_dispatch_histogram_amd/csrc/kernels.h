@@ -212,13 +212,26 @@ struct GroupArgs {
   int G;
   int stride;
   const int32_t* begin;
-  const int32_t* rows;
+  const int32_t* rows;       // null (dense products): one group, the whole layout
   int64_t limit;             // rows of the layout
 };
 
 // ---- grouped products, rows side: out[i][p] = sum_c Q[src(i)][c] * P_g[p][c]
 // for the rows i of every group g (P_g transposed for the rows' gradient)
 enum GemmType { kGemmBf16 = 0, kGemmFp8 = 1, kGemmFp8Ue8m0 = 2 };
+
+// What happens to a product z before it is stored:
+//   out = f(z + bias) + residual, z + bias kept aside where asked
+// kActSwiglu: the product's columns are [gate | up], out = silu(gate) * up has half of them.
+enum Activation { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4, kActSwiglu = 5 };
+struct Epilogue {
+  const float* bias;           // [NO] or null
+  const uint16_t* residual;    // [rows][NO or NO/2] bf16 or null
+  uint16_t* z;                 // [rows][NO] bf16 or null
+  int act;
+  int out_f32;
+};
+
 struct GemmRowsArgs {
   GroupArgs g;
   const void* q;               // [q_rows][C]
@@ -231,6 +244,7 @@ struct GemmRowsArgs {
   uint16_t* out;               // [limit][NO]
   int type, transposed;
   int expected;                // rows a group is expected to hold (0: limit / G)
+  Epilogue epi;                // of the linear product
 };
 hipError_t launch_gemm_rows(const GemmRowsArgs& a, hipStream_t st);
 
@@ -296,6 +310,94 @@ struct ReduceArgs {
 };
 hipError_t launch_reduce(const ReduceArgs& a, hipStream_t st);
 hipError_t launch_reduce_backward(const ReduceArgs& a, hipStream_t st);
+
+// ---- dense product with an epilogue: out = epilogue(x w^T), one weight for all rows
+struct LinearArgs {
+  int64_t rows;
+  int N, K;                    // the product's columns and contraction
+  const uint16_t* x;           // [rows][K]
+  const uint16_t* w;           // [N][K]
+  void* out;                   // [rows][N], or [rows][N/2] (kActSwiglu); bf16 or fp32
+  Epilogue epi;
+};
+hipError_t launch_linear(const LinearArgs& a, hipStream_t st);
+hipError_t launch_gemm_linear(const GemmRowsArgs& a, hipStream_t st);   // more than a few rows
+constexpr int kLinearFewRows = 64;
+
+// ---- gradient through bias and activation: dz = dy * f'(z), dbias = its sum over the rows
+struct ActBackwardArgs {
+  int64_t rows;
+  int N, act;
+  int dy_f32;
+  int parts, rows_per_part;    // the rows each workgroup of a column sums
+  const void* dy;              // [rows][N or N/2] bf16 or fp32
+  const uint16_t* z;           // [rows][N] or null (kActNone)
+  uint16_t* dz;                // [rows][N] or null
+  float* partial;              // [parts][N]
+  float* dbias;                // [N] or null
+  int accumulate;              // dbias is added to
+};
+hipError_t launch_act_backward(const ActBackwardArgs& a, hipStream_t st);
+
+// ---- a few tokens through their experts
+constexpr int kLayerTokens = 128, kLayerListBytes = 65536;
+// Where a workgroup keeps its lists of experts and their tokens in LDS (bytes).
+struct ListsLayout {
+  int words, most, entries;    // 64-bit words of an expert's token mask; listed experts and positions at most
+  int off, active, token, expert, weight;
+  int64_t end;
+};
+__host__ __device__ inline ListsLayout lists_layout(int N, int K, int E) {
+  ListsLayout l;
+  l.words = (N + 63) / 64;
+  l.entries = N * K;
+  l.most = E < l.entries ? E : l.entries;
+  l.end = static_cast<int64_t>(E) * l.words * 8 + (l.most + 1) * 6ll + l.entries * 8ll + 32;
+  l.off = E * l.words * 8;
+  l.active = l.off + (l.most + 1) * 4;
+  l.token = l.active + l.most * 2;
+  l.expert = l.token + l.entries * 2;
+  l.weight = (l.expert + l.entries * 2 + 3) / 4 * 4;
+  l.end = (l.end + 15) / 16 * 16;
+  return l;
+}
+struct LayerArgs {
+  int N, K, E, H, I;
+  int64_t first;               // the first expert that is here
+  int type;                    // GemmType of the weights
+  const uint16_t* x;           // [N][H]
+  const int64_t* idx;          // [N][K]
+  const float* wts;            // [N][K]
+  const void* w1;              // [E][2I][H]
+  const void* w2;              // [E][H][I]
+  const void* s1;              // E4M3: [E][2I/128][H/128]
+  const void* s2;              // E4M3: [E][H/128][I/128]
+  const uint16_t* residual;    // [N][H] or null
+  uint16_t* a;                 // [N*K][I] between the two products
+  uint16_t* y;                 // [N][H]
+};
+hipError_t launch_layer(const LayerArgs& a, hipStream_t st);
+
+// ---- the router's choice and its gradient
+enum GateScore { kGateSoftmax = 0, kGateSigmoid = 1 };
+constexpr int kGateExperts = 2048, kGateTopk = 64, kGateGroups = 64;
+struct GateArgs {
+  int64_t N;
+  int E, K;
+  int score, renorm;
+  int groups, top_groups, group_best;
+  float scale;
+  int f32;                     // logits (and their gradient): fp32, or bf16
+  int per_group, wide_loads;   // set by the launcher
+  FastDiv per_div;             // set by the launcher
+  const void* logits;          // [N][E]
+  const float* bias;           // [E] or null
+  int64_t* idx;                // [N][K]
+  float* w;                    // [N][K]
+  const float* d_w;            // backward: [N][K]
+  void* d_logits;              // backward: [N][E]
+};
+hipError_t launch_gate(const GateArgs& a, bool backward, hipStream_t st);
 
 // Optional launch-geometry overrides read once from the environment
 // (MIEP_PACK_VPL, MIEP_PACK_SLICES, MIEP_COMBINE_VPL, MIEP_COMBINE_SLICES,

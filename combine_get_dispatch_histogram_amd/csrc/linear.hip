@@ -1,0 +1,220 @@
+// linear.hip -- dense products with an epilogue for a few rows (more of them:
+// gemm_linear.hip), and the gradient through activation and bias.
+#include "gemm_epilogue.h"
+#include "stream.h"
+
+namespace miep {
+
+namespace {
+
+// A workgroup computes 16 of the weight's rows (SwiGLU: 8 of gate and the same 8
+// of up, so that narrow products still spread over the GPU) for all rows of x;
+// its wavefronts take every WAVES-th step of the contraction.
+template <int WAVES, int TQ, bool SWIGLU>
+__global__ __launch_bounds__(WAVES * kWave) void linear_few_kernel(LinearArgs a) {
+  __shared__ __align__(16) float sums[WAVES][TQ][16][16];
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+  const int m = lane & 15, quarter = lane >> 4;
+  const int rows = static_cast<int>(a.rows), half = a.N / 2;
+  const int p0 = blockIdx.x * (SWIGLU ? 8 : 16);
+  StreamSource<kGemmBf16, 1, TQ> src;
+  src.w = reinterpret_cast<const uint8_t*>(a.w) + static_cast<int64_t>(p0) * a.K * 2;
+  src.x = reinterpret_cast<const uint8_t*>(a.x);
+  src.C = a.K;
+  const uint32_t row = SWIGLU ? (m & 7) + (m >> 3) * half : min(m, a.N - 1 - p0);
+  src.woff[0] = row * static_cast<uint32_t>(a.K) * 2 + quarter * 16;
+#pragma unroll
+  for (int j = 0; j < TQ; ++j) src.xoff[j] = static_cast<uint32_t>(min(j * 16 + m, rows - 1)) * static_cast<uint32_t>(a.K) * 2 + quarter * 16;
+  f32x4 acc[1][TQ];
+#pragma unroll
+  for (int j = 0; j < TQ; ++j) acc[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  stream_steps<TQ == 1 ? 4 : TQ == 2 || WAVES == 8 ? 2 : 1>(src, wave, WAVES, (a.K + 63) / 64, acc);
+#pragma unroll
+  for (int j = 0; j < TQ; ++j) *reinterpret_cast<f32x4*>(&sums[wave][j][m][quarter * 4]) = acc[0][j];
+  __syncthreads();
+  constexpr int PAIRS = SWIGLU ? 4 : 8;
+  for (int i = threadIdx.x; i < rows * PAIRS; i += WAVES * kWave) {
+    const int r = i / PAIRS, p = i % PAIRS * 2;
+    const EpilogueRow to(a.epi, a.out, r, a.N);
+    float x = 0.f, y = 0.f, ux = 0.f, uy = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const float* s = sums[w][r / 16][r % 16] + p;
+      x += s[0];
+      y += s[1];
+      if constexpr (SWIGLU) {
+        ux += s[8];
+        uy += s[9];
+      }
+    }
+    if constexpr (SWIGLU) to.swiglu2(p0 + p, x, y, ux, uy);
+    else if (p0 + p < a.N) to.plain2(p0 + p, x, y);
+  }
+}
+
+template <int WAVES, bool SWIGLU>
+void launch_few(const LinearArgs& a, unsigned grid, hipStream_t st) {
+  if (a.rows <= 16) linear_few_kernel<WAVES, 1, SWIGLU><<<grid, WAVES * kWave, 0, st>>>(a);
+  else if (a.rows <= 32) linear_few_kernel<WAVES, 2, SWIGLU><<<grid, WAVES * kWave, 0, st>>>(a);
+  else linear_few_kernel<WAVES, 4, SWIGLU><<<grid, WAVES * kWave, 0, st>>>(a);
+}
+
+// Gradient through the activation: a lane 8 columns, a wavefront 512, the four
+// wavefronts of a workgroup every fourth row of its part.  The bias gradient is
+// summed from the unrounded values: by lane, by wavefront, then over the parts.
+template <bool DYF32>
+__device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
+  if constexpr (DYF32) {
+    const float* f = static_cast<const float*>(p) + at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = f[i];
+  } else {
+    const v4u t = ld16(static_cast<const uint16_t*>(p) + at);
+    v[0] = bf16_lo(t.x); v[1] = bf16_hi(t.x); v[2] = bf16_lo(t.y); v[3] = bf16_hi(t.y);
+    v[4] = bf16_lo(t.z); v[5] = bf16_hi(t.z); v[6] = bf16_lo(t.w); v[7] = bf16_hi(t.w);
+  }
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
+  *reinterpret_cast<v4u*>(p) = v4u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+
+template <bool DYF32, bool SWIGLU>
+__global__ __launch_bounds__(256) void act_backward_kernel(ActBackwardArgs a) {
+  __shared__ float sums[4][512][SWIGLU ? 2 : 1];
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  const int width = SWIGLU ? a.N / 2 : a.N;
+  const int c = blockIdx.x * 512 + lane * 8;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * a.rows_per_part;
+  const int64_t r1 = r0 + a.rows_per_part < a.rows ? r0 + a.rows_per_part : a.rows;
+  float sg[8] = {}, su[8] = {};
+  if (c < width) {
+    for (int64_t r = r0 + wave; r < r1; r += 4) {
+      float dy[8], z[8], d[8];
+      load8<DYF32>(a.dy, r * width + c, dy);
+      if constexpr (SWIGLU) {
+        float u[8], du[8];
+        load8<false>(a.z, r * a.N + c, z);
+        load8<false>(a.z, r * a.N + width + c, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float s = sigmoid(z[i]);
+          d[i] = dy[i] * u[i] * s * (1.f + z[i] * (1.f - s));
+          du[i] = dy[i] * (z[i] * s);
+          sg[i] += d[i];
+          su[i] += du[i];
+        }
+        if (a.dz) store8(a.dz + r * a.N + width + c, du);
+      } else {
+        if (a.act == kActNone) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] = dy[i];
+        } else {
+          load8<false>(a.z, r * a.N + c, z);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] = dy[i] * activate_slope(z[i], a.act);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sg[i] += d[i];
+      }
+      if (a.dz) store8(a.dz + r * a.N + c, d);
+    }
+  }
+  if (!a.dbias) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    sums[wave][lane * 8 + i][0] = sg[i];
+    if constexpr (SWIGLU) sums[wave][lane * 8 + i][1] = su[i];
+  }
+  __syncthreads();
+  float* out = a.partial + static_cast<int64_t>(blockIdx.y) * a.N;
+  for (int i = threadIdx.x; i < 512; i += 256) {
+    const int col = blockIdx.x * 512 + i;
+    if (col >= width) continue;
+    out[col] = sums[0][i][0] + sums[1][i][0] + sums[2][i][0] + sums[3][i][0];
+    if constexpr (SWIGLU) out[width + col] = sums[0][i][1] + sums[1][i][1] + sums[2][i][1] + sums[3][i][1];
+  }
+}
+
+// The parts' sums, a wavefront 64 columns, the four of a workgroup every fourth part.
+__global__ __launch_bounds__(256) void bias_sum_kernel(ActBackwardArgs a) {
+  __shared__ float sums[4][64];
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  const int c = blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (c < a.N)
+    for (int p = wave; p < a.parts; p += 4) s += a.partial[static_cast<int64_t>(p) * a.N + c];
+  sums[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < a.N) {
+    s = sums[0][lane] + sums[1][lane] + sums[2][lane] + sums[3][lane];
+    a.dbias[c] = a.accumulate ? a.dbias[c] + s : s;
+  }
+}
+
+__global__ __launch_bounds__(256) void bias_zero_kernel(float* p, int n) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < n) p[i] = 0.f;
+}
+
+}  // namespace
+
+hipError_t launch_linear(const LinearArgs& a, hipStream_t st) {
+  if (a.rows == 0) return hipSuccess;
+  if (a.rows <= kLinearFewRows) {
+    const bool swiglu = a.epi.act == kActSwiglu;
+    const unsigned tiles = static_cast<unsigned>(swiglu ? a.N / 16 : (a.N + 15) / 16);
+    // one workgroup a CU: twice the wavefronts keep as many loads in flight
+    if (tiles <= 256) {
+      if (swiglu) launch_few<16, true>(a, tiles, st);
+      else launch_few<16, false>(a, tiles, st);
+    } else {
+      if (swiglu) launch_few<8, true>(a, tiles, st);
+      else launch_few<8, false>(a, tiles, st);
+    }
+    return hipGetLastError();
+  }
+  GemmRowsArgs g{};
+  g.g.G = 1;
+  g.g.limit = a.rows;
+  g.q = a.x;
+  g.p = a.w;
+  g.q_rows = a.rows;
+  g.C = a.K;
+  g.NO = a.N;
+  g.out = static_cast<uint16_t*>(a.out);
+  g.type = kGemmBf16;
+  g.expected = static_cast<int>(a.rows);
+  g.epi = a.epi;
+  return launch_gemm_linear(g, st);
+}
+
+hipError_t launch_act_backward(const ActBackwardArgs& args, hipStream_t st) {
+  ActBackwardArgs a = args;
+  if (a.rows == 0) {
+    if (a.dbias && !a.accumulate) bias_zero_kernel<<<(a.N + 255) / 256, 256, 0, st>>>(a.dbias, a.N);
+    return hipGetLastError();
+  }
+  const int width = a.act == kActSwiglu ? a.N / 2 : a.N;
+  const unsigned cols = (width + 511) / 512;
+  // as many parts as fill the GPU a few times over, of at least 16 rows; with a
+  // bias no more than the caller's workspace has rows
+  int64_t parts = (a.rows + 15) / 16, most = 4096 / cols + 1;
+  if (a.dbias && most > a.parts) most = a.parts;
+  if (parts > most) parts = most;
+  if (parts > 65535) parts = 65535;
+  const int64_t per = (a.rows + parts - 1) / parts;
+  a.rows_per_part = static_cast<int>(per);
+  a.parts = static_cast<int>((a.rows + per - 1) / per);
+  const dim3 grid(cols, a.parts);
+  if (a.act == kActSwiglu) {
+    if (a.dy_f32) act_backward_kernel<true, true><<<grid, 256, 0, st>>>(a);
+    else act_backward_kernel<false, true><<<grid, 256, 0, st>>>(a);
+  } else {
+    if (a.dy_f32) act_backward_kernel<true, false><<<grid, 256, 0, st>>>(a);
+    else act_backward_kernel<false, false><<<grid, 256, 0, st>>>(a);
+  }
+  if (a.dbias) bias_sum_kernel<<<(a.N + 63) / 64, 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace miep

@@ -11,20 +11,10 @@
 // written (backward 6*I and 4*I: 16384 rows of 2 x 2048 take 54 us, 6.2 TB/s).
 // A lane owns 8 channels (16-byte loads of gate and up); sixteen lanes hold one
 // scale's 128.
+#include "act.h"
 #include "gemm.h"
 
 namespace miep {
-
-// exp(-g) to fp32 accuracy from the hardware's exp2: the product g * log2(e)
-// is carried in two parts, the low one applied to first order.  |g| is capped
-// where the sigmoid is 1 (or exp(-g) overflows and it is 0) to fp32.
-__device__ __forceinline__ float sigmoid(float g) {
-  const float c = -fminf(fmaxf(g, -100.f), 100.f);
-  const float hi = c * 1.44269502f;                                   // log2(e), rounded to fp32
-  const float lo = fmaf(c, 1.44269502f, -hi) + c * 1.92596299e-8f;    // and its rest
-  const float e = __builtin_amdgcn_exp2f(hi) * fmaf(lo, 0.693147182f, 1.f);   // infinity stays infinity
-  return __builtin_amdgcn_rcpf(1.f + e);
-}
 
 __device__ __forceinline__ void widen(const v4u& v, float (&f)[8]) {
   f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);

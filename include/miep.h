@@ -6,7 +6,9 @@
  * (expert-major, optionally FP8) dispatch and combine, the low-latency
  * rank mask, and what the experts compute between dispatch and combine:
  * expert order, grouped matrix products (bf16 with their gradients, E4M3),
- * the activation between them, and the weighted sum back to received rows.
+ * the activation between them, and the weighted sum back to received rows;
+ * and the block around them: the router's choice, dense products with their
+ * epilogue, and the whole expert layer for a few tokens.
  *
  * One GPU plays every rank: the R logical ranks are partitions of one
  * device's HBM, and the S source partitions are the token blocks that the
@@ -502,6 +504,104 @@ miep_status miep_swiglu_fp8(const miep_row_groups* g, const uint16_t* h, int32_t
                             uint8_t* a, float* a_scales, uint8_t* a_scales_ue8m0, void* stream);
 miep_status miep_swiglu_backward(const miep_row_groups* g, const uint16_t* da, const uint16_t* h, int32_t inner,
                                  uint16_t* dh, void* stream);
+
+/* ------------------------------------------------------------------ the block around them
+ * gate_topk -- the router's choice: the K experts of each token and their
+ * weights, as dispatch and the expert layer take them.
+ *   s = softmax(logits) over the experts, or sigmoid(logits) of each;
+ *   chosen: the K largest s + bias, equal ones by the lower index, among the experts of the topk_groups best
+ *   groups (num_groups equal ranges of experts; a group's score is the sum of its largest group_best s + bias);
+ *   topk_weights = scale * s, or with renormalize scale * s / (sum of the chosen s).
+ * bias enters the choice alone.  Without bias and groups the logits themselves are compared, otherwise s + bias in
+ * 64 bits, so that the choice is the formula's.  A logit of -inf or NaN is a masked expert: never chosen, score 0;
+ * +inf counts as the largest number.  Where fewer than K experts are left, the last topk_idx are -1, weight 0.
+ *   logits [num_tokens][E] fp32 (logits_f32) or bf16, 16-byte aligned;  bias [E] fp32, nullable
+ *   topk_idx [num_tokens][K] int64 out, descending;  topk_weights [num_tokens][K] fp32 out
+ * Errors: EINVAL for sizes, flags or null pointers; EUNSUPPORTED for E > 2048, K > 64, num_groups > 64. */
+typedef struct miep_gate {
+  int64_t num_tokens;    /* N >= 0                                     */
+  int32_t num_experts;   /* E                                          */
+  int32_t num_topk;      /* K <= E                                     */
+  int32_t sigmoid;       /* 0: softmax, 1: sigmoid                     */
+  int32_t renormalize;   /* weights of a token add up to scale         */
+  int32_t num_groups;    /* >= 1, divides E                            */
+  int32_t topk_groups;   /* 1..num_groups                              */
+  int32_t group_best;    /* 1 or 2                                     */
+  int32_t logits_f32;    /* logits and d_logits: 1 fp32, 0 bf16        */
+  float scale;
+} miep_gate;
+miep_status miep_gate_topk(const miep_gate* g, const void* logits, const float* bias, int64_t* topk_idx,
+                           float* topk_weights, void* stream);
+
+/* gate_topk_backward -- gradient of the logits, [N][E] in the logits' type,
+ * from the weights' (the choice itself has none; entries outside [0, E) add
+ * nothing, an expert named twice adds both). */
+miep_status miep_gate_topk_backward(const miep_gate* g, const float* d_topk_weights, const void* logits,
+                                    const int64_t* topk_idx, void* d_logits, void* stream);
+
+/* linear -- one weight for all rows (router, shared expert):
+ *   z = x w^T + bias,  y = f(z) + residual
+ * in fp32, rounded once.  f: the identity, relu, silu, gelu (by the error
+ * function, to 1e-7) or its tanh form; or SwiGLU, with z = [gate | up] and y =
+ * silu(gate) * up + residual of half the columns.
+ *   x [rows][K], w [N][K] bf16;  bias [N] fp32, nullable
+ *   residual [rows][N or N/2] bf16, nullable; may be y itself
+ *   z [rows][N] bf16 out, nullable: kept for the backward pass
+ *   y [rows][N or N/2] out, bf16 or fp32 (y_f32)
+ * Everything 16-byte aligned, rows at most 2^31-2^16; N, K % 8 == 0 (SwiGLU: N % 16 == 0), at most 2^21; SwiGLU's w
+ * under 4 GiB less 1024 rows.
+ * Errors: EINVAL for null pointers, sizes, flags; EUNSUPPORTED for the limits above. */
+enum { MIEP_ACT_NONE = 0, MIEP_ACT_RELU = 1, MIEP_ACT_SILU = 2, MIEP_ACT_GELU = 3, MIEP_ACT_GELU_TANH = 4, MIEP_ACT_SWIGLU = 5 };
+miep_status miep_linear(const uint16_t* x, int64_t rows, const uint16_t* w, int32_t n, int32_t k, const float* bias,
+                        int32_t activation, const uint16_t* residual, uint16_t* z, void* y, int32_t y_f32,
+                        void* stream);
+
+/* linear_act_backward -- dz = dy * f'(z) (bf16, rounded once; nullable) and
+ * dbias[n] = sum of dz's unrounded column over the rows, in fp32 (nullable;
+ * accumulate: added to what dbias holds).
+ *   dy [rows][N or N/2] bf16 or fp32 (dy_f32);  z [rows][N] bf16 from miep_linear (MIEP_ACT_NONE: ignored)
+ *   workspace [parts][N] fp32, parts >= 1, where dbias is given: the parts the rows may be summed in (one for
+ *   every 16 rows, up to 256, is enough to fill the GPU); of one call at a time
+ * linear_dgrad -- dx = dy w.  linear_wgrad -- dw = dy^T x, fp32 (dw_f32; accumulate: added) or bf16. */
+miep_status miep_linear_act_backward(const void* dy, int32_t dy_f32, const uint16_t* z, int64_t rows, int32_t n,
+                                     int32_t activation, uint16_t* dz, float* dbias, int32_t accumulate,
+                                     float* workspace, int32_t parts, void* stream);
+miep_status miep_linear_dgrad(const uint16_t* dy, int64_t rows, const uint16_t* w, int32_t n, int32_t k, uint16_t* dx,
+                              void* stream);
+miep_status miep_linear_wgrad(const uint16_t* dy, const uint16_t* x, int64_t rows, int32_t n, int32_t k,
+                              int32_t dw_f32, int32_t accumulate, void* dw, void* stream);
+
+/* expert_layer -- a few tokens through their experts and back, in place of
+ * dispatch, the experts' products and combine (decoding):
+ *   y[t] = residual[t] + sum over k of topk_weights[t][k] * W2_e (silu(g) * u),  [g | u] = W1_e x[t]
+ * for the entries e = topk_idx[t][k] in [first_expert, first_expert + num_experts); others (masked, or another
+ * rank's) add nothing.  Every chosen expert's weights are read once.  Sums are fp32, silu(g) * u is rounded to bf16
+ * between the products, y once; a token's experts are added in ascending order, an expert named twice with the sum
+ * of its weights.
+ *   x [N][H] bf16;  w1 [E][2I][H] = [gate | up], w2 [E][H][I], all bf16, or all E4M3 codes with a scale for each 128 x
+ *   128 block: w1_scales [E][2I/128][H/128], w2_scales [E][H/128][I/128], fp32 or (scales_ue8m0) exponent bytes.
+ *   Codes are multiplied as bf16 numbers, which they are exactly: x is not cast.
+ *   residual [N][H] bf16, nullable; may be y itself
+ *   workspace [N*K][I] bf16, of one call at a time
+ * N at most 128; H, I % 8 == 0 (E4M3: % 128 == 0); weights of one expert under 4 GiB, workspace too; E * ceil(N/64) *
+ * 8 + 6 * min(E, N*K) + 8 * N*K bytes at most 65,400.  Larger batches: dispatch.
+ * Errors: EINVAL for null pointers, sizes, flags; EUNSUPPORTED for the limits above. */
+typedef struct miep_layer {
+  int32_t num_tokens;    /* N >= 0                        */
+  int32_t num_topk;      /* K <= 64                       */
+  int32_t num_experts;   /* E, those that are here        */
+  int32_t hidden;        /* H                             */
+  int32_t inner;         /* I                             */
+  int32_t scales_ue8m0;  /* E4M3: scales are exponent bytes */
+  int64_t first_expert;
+} miep_layer;
+miep_status miep_expert_layer(const miep_layer* q, const uint16_t* x, const int64_t* topk_idx,
+                              const float* topk_weights, const uint16_t* w1, const uint16_t* w2,
+                              const uint16_t* residual, uint16_t* workspace, uint16_t* y, void* stream);
+miep_status miep_expert_layer_fp8(const miep_layer* q, const uint16_t* x, const int64_t* topk_idx,
+                                  const float* topk_weights, const uint8_t* w1, const void* w1_scales,
+                                  const uint8_t* w2, const void* w2_scales, const uint16_t* residual,
+                                  uint16_t* workspace, uint16_t* y, void* stream);
 
 /* Description of the last failure on this thread ("" if none). Host-only. */
 const char* miep_last_error(void);
