@@ -1218,7 +1218,9 @@ miep_status miep_linear_dgrad(const uint16_t* dy, int64_t rows, const uint16_t* 
   a.out = dx;
   a.type = miep::kGemmBf16;
   a.transposed = 1;
-  return hip_status(miep::launch_gemm_rows(a, static_cast<hipStream_t>(stream)), "linear dgrad launch");
+  a.expected = static_cast<int>(rows);
+  if (rows == 0) return ok();
+  return hip_status(miep::launch_gemm_linear(a, static_cast<hipStream_t>(stream)), "linear dgrad launch");
 }
 
 miep_status miep_linear_wgrad(const uint16_t* dy, const uint16_t* x, int64_t rows, int32_t n, int32_t k,

@@ -633,20 +633,7 @@ __device__ __forceinline__ void rows_tiles(const GemmRowsArgs& a, int total, uin
     };
     stored = EPI == kEpiNone && out_live == BQ && out_p0 + BP <= NO;
     if constexpr (EPI != kEpiNone) {
-      if (busy) {
-#pragma unroll
-        for (int j = 0; j < TQ; ++j) {
-          const int row = (wq * TQ + j) * 16 + m;
-          if (row >= out_live) continue;
-          const EpilogueRow to(a.epi, a.out, out_row0 + row, NO);
-#pragma unroll
-          for (int i = 0; i < TP; i += EPI == kEpiSwiglu ? 4 : 2) {
-            const int p = out_p0 + (wp * TP + i) * 16;
-            if constexpr (EPI == kEpiSwiglu) to.swiglu(p / 2, quarter, acc[i][j], acc[i + 1][j], acc[i + 2][j], acc[i + 3][j]);
-            else to.plain(p, quarter, acc[i][j], acc[i + 1][j]);
-          }
-        }
-      }
+      if (busy) epilogue_tile<EPI>(a.epi, a.out, NO, out_row0 + wq * 16 * TQ, out_live - wq * 16 * TQ, out_p0 + wp * 16 * TP, acc);
     } else if (stored) {
 #pragma unroll
       for (int j = 0; j < TQ; ++j) {
@@ -716,7 +703,7 @@ hipError_t launch_rows_tile(const GemmRowsArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int EL, bool PT, bool GATHER, int EPI = kEpiNone>
+template <int EL, bool PT, bool GATHER>
 hipError_t launch_rows(const GemmRowsArgs& a, hipStream_t st) {
   constexpr bool F8 = EL != kGemmBf16;
   // Few tiles over a long contraction: split it (bf16, us against the tiles
@@ -725,7 +712,7 @@ hipError_t launch_rows(const GemmRowsArgs& a, hipStream_t st) {
   // 16 steps only, 100 rows of 1 x 256 x 1024, 13 -> 14.5).
   const int64_t tiles32 = a.g.G * ((static_cast<int64_t>(a.expected) + 31) / 32) * ((a.NO + 31) / 32);
   if (tiles32 <= 256 && a.C / (F8 ? 128 : 64) >= 24 && split_tiles(a) <= kMostTiles)
-    return launch_rows_split<EL, PT, GATHER, EPI>(a, st);
+    return launch_rows_split<EL, PT, GATHER, kEpiNone>(a, st);
   // Rows that most groups stay under when e are expected and chance spreads
   // them (a binomial count's deviation is at most sqrt(e)).
   const int64_t e = a.expected + static_cast<int64_t>(std::sqrt(static_cast<double>(a.expected)));
@@ -734,21 +721,20 @@ hipError_t launch_rows(const GemmRowsArgs& a, hipStream_t st) {
   //   A few rows: the weights stream past them.  128 x 32, two workgroups a
   //   CU, against 128 x 128: 16 rows 84 / 85.5, 4 rows 82 / 81, 16 rows of
   //   7168 x 2048 36 / 38, E4M3 21.2 / 25.7.
-  if constexpr (EPI == kEpiNone)                                      // (a linear product of so few rows has its own kernel)
-    if (e <= 24) return launch_rows_tile<EL, PT, GATHER, 128, 32, 4, 1, F8 ? 3 : 4, F8 ? 3 : 4>(a, st);
+  if (e <= 24) return launch_rows_tile<EL, PT, GATHER, 128, 32, 4, 1, F8 ? 3 : 4, F8 ? 3 : 4>(a, st);
   const int64_t wide = (a.NO + 255) / 256, narrow = (a.NO + 127) / 128;
   if (a.g.G * wide * ((e + 255) / 256) >= 192) {
     // enough tiles of 256 channels for the GPU's 256 CUs
-    gemm_rows_wide_kernel<EL, PT, GATHER, EPI><<<256, 8 * kWave, 0, st>>>(a);
+    gemm_rows_wide_kernel<EL, PT, GATHER, kEpiNone><<<256, 8 * kWave, 0, st>>>(a);
     return hipGetLastError();
   }
   //   Fewer: 128 channels, as many rows as a group needs: 128 x 128 / 192 /
   //   256 at 64 rows 92 / 92 / 100, at 128 rows 160 / 106 / 110, at 180 rows
   //   (some groups more than 192) 145 / 186 / 123.
   if (e <= 108 || a.g.G * narrow * ((e + 127) / 128) <= 256)
-    return launch_rows_tile<EL, PT, GATHER, 128, 128, 2, 4, F8 ? 4 : 5, F8 ? 4 : 5, EPI>(a, st);
-  if (e <= 192) return launch_rows_tile<EL, PT, GATHER, 128, 192, 2, 4, F8 ? 3 : 4, F8 ? 3 : 4, EPI>(a, st);
-  return launch_rows_tile<EL, PT, GATHER, 128, 256, 2, 4, 3, 3, EPI>(a, st);
+    return launch_rows_tile<EL, PT, GATHER, 128, 128, 2, 4, F8 ? 4 : 5, F8 ? 4 : 5>(a, st);
+  if (e <= 192) return launch_rows_tile<EL, PT, GATHER, 128, 192, 2, 4, F8 ? 3 : 4, F8 ? 3 : 4>(a, st);
+  return launch_rows_tile<EL, PT, GATHER, 128, 256, 2, 4, 3, 3>(a, st);
 }
 
 }  // namespace miep

@@ -212,9 +212,13 @@ __global__ __launch_bounds__(512, 2) void gemm_rows_split_kernel(GemmRowsArgs a)
           ux += s[w * (2 * S::kStage / 4)];
           uy += s[w * (2 * S::kStage / 4) + 1];
         }
-        if (row < live && p < 16 && p0 / 2 + p < NO / 2) EpilogueRow(a.epi, a.out, row0 + row, NO).swiglu2(p0 / 2 + p, x, y, ux, uy);
+        if (row < live && p < 16 && p0 / 2 + p < NO / 2) {
+          float g[2] = {x, y}, u[2] = {ux, uy};
+          EpilogueRow(a.epi, a.out, row0 + row, NO).swiglu(p0 / 2 + p, g, u);
+        }
       } else if constexpr (EPI == kEpiPlain) {
-        if (row < live && p0 + p < NO) EpilogueRow(a.epi, a.out, row0 + row, NO).plain2(p0 + p, x, y);
+        float v[2] = {x, y};
+        if (row < live && p0 + p < NO) EpilogueRow(a.epi, a.out, row0 + row, NO).plain(p0 + p, v);
       } else if (row < live && p0 + p < NO) {
         bool none = false;
         if constexpr (GATHER) {

@@ -322,7 +322,7 @@ struct LinearArgs {
 };
 hipError_t launch_linear(const LinearArgs& a, hipStream_t st);
 hipError_t launch_gemm_linear(const GemmRowsArgs& a, hipStream_t st);   // more than a few rows
-constexpr int kLinearFewRows = 64;
+constexpr int kLinearFewRows = 16;
 
 // ---- gradient through bias and activation: dz = dy * f'(z), dbias = its sum over the rows
 struct ActBackwardArgs {
@@ -340,7 +340,7 @@ struct ActBackwardArgs {
 hipError_t launch_act_backward(const ActBackwardArgs& a, hipStream_t st);
 
 // ---- a few tokens through their experts
-constexpr int kLayerTokens = 128, kLayerListBytes = 65536;
+constexpr int kLayerTokens = 128, kLayerListBytes = 49152;
 // Where a workgroup keeps its lists of experts and their tokens in LDS (bytes).
 struct ListsLayout {
   int words, most, entries;    // 64-bit words of an expert's token mask; listed experts and positions at most
@@ -363,6 +363,7 @@ __host__ __device__ inline ListsLayout lists_layout(int N, int K, int E) {
 }
 struct LayerArgs {
   int N, K, E, H, I;
+  int tile;                    // output channels a workgroup; set by the launcher
   int64_t first;               // the first expert that is here
   int type;                    // GemmType of the weights
   const uint16_t* x;           // [N][H]

@@ -15,7 +15,11 @@ namespace miep {
 
 namespace {
 
-constexpr int kLayerWaves = 8, kLayerThreads = kLayerWaves * kWave;
+// LDS of a workgroup: RING bytes of rings, its wavefronts' sums, the lists; the
+// shorter rings where long lists leave no room for the others.
+constexpr int kUpWaves = 8, kDownWaves = 4, kMostLds = 163840;
+constexpr int kUpRing = 137216, kUpRingShort = 69632, kDownRing = 104448, kDownRingShort = 49152;
+constexpr int kUpSums = kUpWaves * 2048;
 
 // The experts that some token chose, ascending, with their tokens, in dynamic LDS.
 struct Lists {
@@ -25,11 +29,12 @@ struct Lists {
   uint16_t* token;             // [N*K] a position's token
   uint16_t* expert;            // [N*K] and expert
   float* weight;               // [N*K] its weight (an expert named twice: their sum)
-  int count;                   // listed experts
+  int count, positions;        // listed experts, their tokens
 };
 
-template <bool WEIGHTS>
+template <int WAVES, bool WEIGHTS>
 __device__ __forceinline__ Lists make_lists(const LayerArgs& a, uint8_t* lds, int* wave_sums) {
+  constexpr int THREADS = WAVES * kWave;
   const ListsLayout at = lists_layout(a.N, a.K, a.E);
   Lists l;
   l.mask = reinterpret_cast<uint64_t*>(lds);
@@ -39,9 +44,9 @@ __device__ __forceinline__ Lists make_lists(const LayerArgs& a, uint8_t* lds, in
   l.expert = reinterpret_cast<uint16_t*>(lds + at.expert);
   l.weight = reinterpret_cast<float*>(lds + at.weight);
   const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
-  for (int i = tid; i < a.E * at.words; i += kLayerThreads) l.mask[i] = 0;
+  for (int i = tid; i < a.E * at.words; i += THREADS) l.mask[i] = 0;
   __syncthreads();
-  for (int i = tid; i < at.entries; i += kLayerThreads) {
+  for (int i = tid; i < at.entries; i += THREADS) {
     const int64_t e = a.idx[i] - a.first;
     const int t = i / a.K;
     if (e >= 0 && e < a.E)
@@ -49,7 +54,7 @@ __device__ __forceinline__ Lists make_lists(const LayerArgs& a, uint8_t* lds, in
   }
   __syncthreads();
   int before = 0;                                                     // listed << 16 | positions
-  for (int e0 = 0; e0 < a.E; e0 += kLayerThreads) {
+  for (int e0 = 0; e0 < a.E; e0 += THREADS) {
     const int e = e0 + tid;
     int n = 0;
     if (e < a.E)
@@ -59,7 +64,7 @@ __device__ __forceinline__ Lists make_lists(const LayerArgs& a, uint8_t* lds, in
     if (lane == 63) wave_sums[wave] = inc;
     __syncthreads();
     int mine = before + inc - both;
-    for (int w = 0; w < kLayerWaves; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
       if (w < wave) mine += wave_sums[w];
       before += wave_sums[w];
     }
@@ -77,9 +82,10 @@ __device__ __forceinline__ Lists make_lists(const LayerArgs& a, uint8_t* lds, in
     __syncthreads();
   }
   l.count = before >> 16;
-  if (tid == 0) l.off[l.count] = before & 0xffff;
+  l.positions = before & 0xffff;
+  if (tid == 0) l.off[l.count] = l.positions;
   if constexpr (WEIGHTS) {
-    for (int p = tid; p < (before & 0xffff); p += kLayerThreads) {
+    for (int p = tid; p < l.positions; p += THREADS) {
       const int64_t t = l.token[p], e = a.first + l.expert[p];
       float w = 0.f;
       for (int k = 0; k < a.K; ++k) w += a.idx[t * a.K + k] == e ? a.wts[t * a.K + k] : 0.f;
@@ -90,162 +96,275 @@ __device__ __forceinline__ Lists make_lists(const LayerArgs& a, uint8_t* lds, in
   return l;
 }
 
-// ---- first products: units of 16 gate and 16 up channels of an expert
-template <int EL, int TQ>
-__device__ __forceinline__ void up_unit(const LayerArgs& a, const Lists& l, int place, int i0, int c0, int n, float* sums) {
+// The most tokens of an expert.
+template <int WAVES>
+__device__ __forceinline__ int most_tokens(const Lists& l, int* wave_sums) {
+  int n = 0;
+  for (int i = threadIdx.x; i < l.count; i += WAVES * kWave) n = max(n, l.off[i + 1] - l.off[i]);
+  for (int d = 32; d > 0; d >>= 1) n = max(n, __shfl_xor(n, d));
+  if (lane_id() == 0) wave_sums[threadIdx.x / kWave] = n;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) n = max(n, wave_sums[w]);
+  return __builtin_amdgcn_readfirstlane(n);
+}
+
+// ---- first products: units of 16 gate and 16 up channels of an expert, for 16 of
+// its tokens.  A workgroup's units come one after the other through its rings: the
+// next unit's first loads are under way while this one's sums are added up.
+template <int EL, int XL, int RING>
+__device__ __forceinline__ void up_units(const LayerArgs& a, const Lists& l, uint8_t* ring_mem, float* sums) {
   constexpr bool F8 = EL != kGemmBf16;
+  using Ring = StreamRing<EL, 4, XL, RING / kUpWaves>;
   constexpr int EB = F8 ? 1 : 2;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int m = lane & 15, quarter = lane >> 4;
-  const int e = l.active[place], first = l.off[place] + c0;
   const uint32_t ldw = static_cast<uint32_t>(a.H) * EB;
-  StreamSource<EL, 2, TQ> src;
-  src.w = static_cast<const uint8_t*>(a.w1) + static_cast<int64_t>(__builtin_amdgcn_readfirstlane(e)) * 2 * a.I * ldw;
-  src.x = reinterpret_cast<const uint8_t*>(a.x);
-  src.C = a.H;
-  const int row = min(i0 + m, a.I - 1);
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    src.woff[p] = static_cast<uint32_t>(p * a.I + row) * ldw + quarter * 16;
-    if constexpr (F8) {
-      const int kb = a.H / kFp8Group;
-      src.scales = a.s1;
-      src.srow[p] = (static_cast<int64_t>(__builtin_amdgcn_readfirstlane(e)) * (2 * a.I / kFp8Group) + (p * a.I + i0) / kFp8Group) * kb;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < TQ; ++j)
-    src.xoff[j] = static_cast<uint32_t>(l.token[first + min(j * 16 + m, n - 1)]) * (a.H * 2u) + quarter * (F8 ? 32 : 16);
-  f32x4 acc[2][TQ];
-#pragma unroll
-  for (int p = 0; p < 2; ++p)
-#pragma unroll
-    for (int j = 0; j < TQ; ++j) acc[p][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  constexpr int S = StreamType<EL>::kStep;
-  stream_steps<F8 ? 1 : 2>(src, wave, kLayerWaves, (a.H + S - 1) / S, acc);
-#pragma unroll
-  for (int p = 0; p < 2; ++p)
-#pragma unroll
-    for (int j = 0; j < TQ; ++j)
-      *reinterpret_cast<f32x4*>(sums + (((wave * TQ + j) * 16 + m) * 2 + p) * 16 + quarter * 4) = acc[p][j];
-  __syncthreads();
-  for (int i = threadIdx.x; i < TQ * 128; i += kLayerThreads) {
-    const int col = i / 8, p = i % 8 * 2;
-    if (col >= n || i0 + p >= a.I) continue;
-    float gx = 0.f, gy = 0.f, ux = 0.f, uy = 0.f;
-#pragma unroll
-    for (int w = 0; w < kLayerWaves; ++w) {
-      const float* s = sums + (w * TQ * 16 + col) * 32 + p;
-      gx += s[0];
-      gy += s[1];
-      ux += s[16];
-      uy += s[17];
-    }
-    *reinterpret_cast<uint32_t*>(a.a + static_cast<int64_t>(first + col) * a.I + i0 + p) =
-        pack_bf16x2(gx * sigmoid(gx) * ux, gy * sigmoid(gy) * uy);
-  }
-  __syncthreads();
-}
+  const int tiles = (a.I + 15) / 16, kb = a.H / kFp8Group;
+  const int steps = (a.H + Ring::kChannels - 1) / Ring::kChannels;
+  const int mine = wave < steps ? (steps - wave + kUpWaves - 1) / kUpWaves : 0;         // this wavefront's steps of a unit
 
-template <int EL, int MOST>
-__global__ __launch_bounds__(kLayerThreads, MOST == 1 ? 4 : 2) void layer_up_kernel(LayerArgs a) {
-  extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ __align__(16) float sums[kLayerWaves * MOST * 16 * 32];
-  __shared__ int wave_sums[kLayerWaves];
-  const Lists l = make_lists<false>(a, lds, wave_sums);
-  const int tiles = (a.I + 15) / 16;
-  for (int u = blockIdx.x; u < l.count * tiles; u += gridDim.x) {
-    const int place = u / tiles, i0 = (u - place * tiles) * 16;
-    const int n = l.off[place + 1] - l.off[place];
-    for (int c0 = 0; c0 < n; c0 += MOST * 16) {
-      const int left = n - c0;
-      if (MOST == 1 || left <= 16) up_unit<EL, 1>(a, l, place, i0, c0, min(left, 16), sums);
-      else if constexpr (MOST > 1) {
-        if (left <= 32) up_unit<EL, 2>(a, l, place, i0, c0, left, sums);
-        else up_unit<EL, 4>(a, l, place, i0, c0, min(left, 64), sums);
+  // units: every expert's tiles, a tile once for each 16 of its tokens
+  struct Unit { int place, i0, c0, n; };
+  struct Walk { int place, tile, c0; };                               // from here `skip` units on
+  auto move = [&](Walk& at, int skip) MIEP_INLINE {
+    while (at.place < l.count) {
+      const int n = __builtin_amdgcn_readfirstlane(l.off[at.place + 1] - l.off[at.place]);
+      const int blocks = (n + 15) / 16, left = (tiles - at.tile) * blocks - at.c0;
+      if (skip < left) {
+        const int u = at.tile * blocks + at.c0 + skip;
+        at.tile = u / blocks;
+        at.c0 = u - at.tile * blocks;
+        return;
       }
+      skip -= left;
+      ++at.place;
+      at.tile = at.c0 = 0;
     }
+  };
+  auto unit_of = [&](const Walk& at) MIEP_INLINE {
+    const int n = __builtin_amdgcn_readfirstlane(l.off[at.place + 1] - l.off[at.place]);
+    return Unit{at.place, at.tile * 16, at.c0 * 16, min(n - at.c0 * 16, 16)};
+  };
+
+  // the issuing side
+  Ring ring((uint32_t)(uintptr_t)(lds_byte*)ring_mem + wave * (RING / kUpWaves));
+  Walk ahead{0, 0, 0};
+  move(ahead, blockIdx.x);
+  int ahead_step = 0;
+  const uint8_t *w = nullptr, *scale = nullptr;
+  constexpr int SB = EL == kGemmFp8 ? 4 : 1;                          // bytes of a scale
+  uint32_t woff[4], xoff[XL];
+  auto set_unit = [&]() MIEP_INLINE {
+    const Unit u = unit_of(ahead);
+    const int e = __builtin_amdgcn_readfirstlane(static_cast<int>(l.active[u.place])), first = l.off[u.place] + u.c0;
+    w = static_cast<const uint8_t*>(a.w1) + (static_cast<int64_t>(e) * 2 * a.I + u.i0) * ldw;
+    if constexpr (F8)                                                 // of the gate rows' block, and of the up rows'
+      scale = static_cast<const uint8_t*>(a.s1) +
+              (static_cast<int64_t>(e) * (2 * a.I / kFp8Group) + ((lane & 1) * a.I + u.i0) / kFp8Group) * kb * SB;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = Ring::w_row(i);
+      woff[i] = static_cast<uint32_t>(min(row & 15, a.I - 1 - u.i0) + (row >> 4) * a.I) * ldw + Ring::w_chunk(i) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      xoff[i] = static_cast<uint32_t>(l.token[first + min(Ring::x_row(i), u.n - 1)]) * (a.H * 2u) + Ring::x_chunk(i) * 16;
+  };
+  auto issue = [&]() MIEP_INLINE {
+    if (ahead.place >= l.count) return;
+    if (ahead_step == 0) set_unit();
+    const int step = wave + ahead_step * kUpWaves;
+    ring.issue(w + step * 128ll, woff, reinterpret_cast<const uint8_t*>(a.x) + step * static_cast<int64_t>(Ring::kXRow), xoff, scale + step * SB,
+               a.H - step * Ring::kChannels);
+    if (++ahead_step == mine) {
+      ahead_step = 0;
+      move(ahead, gridDim.x);
+    }
+  };
+  if (mine > 0)
+    for (int i = 0; i < Ring::kDepth; ++i) issue();
+
+  Walk at{0, 0, 0};
+  move(at, blockIdx.x);
+  while (at.place < l.count) {
+    const Unit u = unit_of(at);
+    f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+    for (int i = 0; i < mine; ++i) {
+      typename Ring::Frag f;
+      ring.take(f, ahead.place < l.count);
+      issue();
+      Ring::multiply(f, [](int p, int) { return p == 1; }, acc);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) *reinterpret_cast<f32x4*>(sums + ((wave * 16 + m) * 2 + p) * 16 + quarter * 4) = acc[p];
+    all_read();
+    for (int i = threadIdx.x; i < 128; i += kUpWaves * kWave) {
+      const int col = i / 8, p = i % 8 * 2;
+      if (col >= u.n || u.i0 + p >= a.I) continue;
+      float gx = 0.f, gy = 0.f, ux = 0.f, uy = 0.f;
+#pragma unroll
+      for (int k = 0; k < kUpWaves; ++k) {
+        const float* v = sums + (k * 16 + col) * 32 + p;
+        gx += v[0];
+        gy += v[1];
+        ux += v[16];
+        uy += v[17];
+      }
+      *reinterpret_cast<uint32_t*>(a.a + static_cast<int64_t>(l.off[u.place] + u.c0 + col) * a.I + u.i0 + p) =
+          pack_bf16x2(gx * sigmoid(gx) * ux, gy * sigmoid(gy) * uy);
+    }
+    all_read();
+    move(at, gridDim.x);
   }
 }
 
-// ---- second products: 16 output channels a workgroup; the experts' steps one
-// after the other are cut evenly over its wavefronts
-template <int EL, int TQ>
-__device__ __forceinline__ void down_part(const LayerArgs& a, const Lists& l, int place, int h0, int s0, int s1, int c0, int n, float* out) {
+template <int EL, int RING>
+__global__ __launch_bounds__(kUpWaves * kWave) void layer_up_kernel(LayerArgs a) {
+  extern __shared__ __align__(1024) uint8_t lds[];                    // rings, sums, lists
+  float* sums = reinterpret_cast<float*>(lds + RING);
+  int* wave_sums = reinterpret_cast<int*>(lds + RING + kUpSums);
+  const Lists l = make_lists<kUpWaves, false>(a, lds + RING + kUpSums + 64, wave_sums);
+  const int most = most_tokens<kUpWaves>(l, wave_sums);
+  // as few of X's rows as the fullest expert has tokens
+  if constexpr (EL == kGemmBf16) {
+    if (most <= 8) up_units<EL, 1, RING>(a, l, lds, sums);
+    else up_units<EL, 2, RING>(a, l, lds, sums);
+  } else {
+    if (most <= 4) up_units<EL, 1, RING>(a, l, lds, sums);
+    else if (most <= 8) up_units<EL, 2, RING>(a, l, lds, sums);
+    else up_units<EL, 4, RING>(a, l, lds, sums);
+  }
+}
+
+// ---- second products: a.tile output channels a workgroup; the experts' steps one
+// after the other (an expert's once for each 16 of its tokens) go to its wavefronts
+// in turn, so that together they read whole rows.  At an expert's end a wavefront
+// adds its results, times the gate weights, to its own sums of every token.
+template <int EL, int WL, int XL, int RING>
+__device__ __forceinline__ void down_part(const LayerArgs& a, const Lists& l, uint8_t* ring_mem, float* out) {
   constexpr bool F8 = EL != kGemmBf16;
-  constexpr int EB = F8 ? 1 : 2;
-  const int lane = lane_id(), m = lane & 15, quarter = lane >> 4;
-  const int e = __builtin_amdgcn_readfirstlane(static_cast<int>(l.active[place]));
-  const int first = l.off[place] + c0;
-  const uint32_t ldw = static_cast<uint32_t>(a.I) * EB;
-  StreamSource<EL, 1, TQ> src;
-  src.w = static_cast<const uint8_t*>(a.w2) + (static_cast<int64_t>(e) * a.H + h0) * ldw;
-  src.x = reinterpret_cast<const uint8_t*>(a.a);
-  src.C = a.I;
-  src.woff[0] = static_cast<uint32_t>(min(m, a.H - 1 - h0)) * ldw + quarter * 16;
-  if constexpr (F8) {
-    src.scales = a.s2;
-    src.srow[0] = (static_cast<int64_t>(e) * (a.H / kFp8Group) + h0 / kFp8Group) * (a.I / kFp8Group);
-  }
+  using Ring = StreamRing<EL, WL, XL, RING / kDownWaves>;
+  constexpr int EB = F8 ? 1 : 2, TP = Ring::TP, P = 16 * TP;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+  const int m = lane & 15, quarter = lane >> 4;
+  const int h0 = blockIdx.x * a.tile, kb = a.I / kFp8Group;
+  const uint32_t ldw = static_cast<uint32_t>(a.I) * EB, ldx = static_cast<uint32_t>(a.I) * 2;
+  const int steps = (a.I + Ring::kChannels - 1) / Ring::kChannels;
+
+  int64_t total = 0;
+  for (int p = lane; p < l.count; p += kWave) total += (l.off[p + 1] - l.off[p] + 15) / 16;
+  for (int d = 32; d > 0; d >>= 1) total += __shfl_xor(static_cast<int>(total), d);
+  total = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(total))) * steps;
+  struct Walk { int place, c0, step; };                               // an expert, its 16 tokens from c0 on, a step
+  auto tokens = [&](const Walk& at) MIEP_INLINE { return __builtin_amdgcn_readfirstlane(l.off[at.place + 1] - l.off[at.place]); };
+  auto move = [&](Walk& at, int by) MIEP_INLINE {                     // true: to other tokens or another expert
+    at.step += by;
+    if (at.step < steps) return false;
+    while (at.step >= steps && at.place < l.count) {
+      at.step -= steps;
+      at.c0 += 16;
+      if (at.c0 >= tokens(at)) {
+        at.c0 = 0;
+        ++at.place;
+      }
+    }
+    return true;
+  };
+  const int64_t mine = total > wave ? (total - wave + kDownWaves - 1) / kDownWaves : 0;
+  Walk at{0, 0, 0};
+  move(at, wave);
+
+  Ring ring((uint32_t)(uintptr_t)(lds_byte*)ring_mem + wave * (RING / kDownWaves));
+  uint32_t woff[WL], xoff[XL];
 #pragma unroll
-  for (int j = 0; j < TQ; ++j)
-    src.xoff[j] = static_cast<uint32_t>(first + min(j * 16 + m, n - 1)) * (a.I * 2u) + quarter * (F8 ? 32 : 16);
-  f32x4 acc[1][TQ];
+  for (int i = 0; i < WL; ++i) woff[i] = static_cast<uint32_t>(min(Ring::w_row(i), min(a.tile, a.H - h0) - 1)) * ldw + Ring::w_chunk(i) * 16;
+  // E4M3: the tile's rows lie in one block of 128 or, from row `border` on, in the next
+  constexpr int SB = EL == kGemmFp8 ? 4 : 1;                          // bytes of a scale
+  const int border = kFp8Group - h0 % kFp8Group;
+  const int second = border < min(a.tile, a.H - h0) ? kb : 0;
+  Walk ahead = at;
+  int64_t issued = 0;
+  const uint8_t *w = nullptr, *scale = nullptr;
+  bool fresh = true;
+  auto issue = [&]() MIEP_INLINE {
+    if (issued >= mine) return;
+    if (fresh) {
+      const int e = __builtin_amdgcn_readfirstlane(static_cast<int>(l.active[ahead.place]));
+      const int first = l.off[ahead.place] + ahead.c0, n = tokens(ahead) - ahead.c0;
+      w = static_cast<const uint8_t*>(a.w2) + (static_cast<int64_t>(e) * a.H + h0) * ldw;
+      if constexpr (F8)
+        scale = static_cast<const uint8_t*>(a.s2) +
+                ((static_cast<int64_t>(e) * (a.H / kFp8Group) + h0 / kFp8Group) * kb + (lane & 1) * second) * SB;
 #pragma unroll
-  for (int j = 0; j < TQ; ++j) acc[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  stream_steps<F8 ? (TQ == 4 ? 1 : 2) : (TQ == 1 ? 4 : 2)>(src, s0, 1, s1, acc);
+      for (int i = 0; i < XL; ++i) xoff[i] = static_cast<uint32_t>(first + min(Ring::x_row(i), n - 1)) * ldx + Ring::x_chunk(i) * 16;
+    }
+    ring.issue(w + ahead.step * 128ll, woff, reinterpret_cast<const uint8_t*>(a.a) + ahead.step * static_cast<int64_t>(Ring::kXRow), xoff,
+               scale + ahead.step * SB, a.I - ahead.step * Ring::kChannels);
+    fresh = move(ahead, kDownWaves);
+    ++issued;
+  };
+  for (int i = 0; i < Ring::kDepth; ++i) issue();
+
+  f32x4 acc[TP];
 #pragma unroll
-  for (int j = 0; j < TQ; ++j) {
-    const int col = j * 16 + m;
-    if (col < n) {
-      const float w = l.weight[first + col];
-      f32x4* o = reinterpret_cast<f32x4*>(out + l.token[first + col] * 16 + quarter * 4);
-      f32x4 v = *o;
+  for (int i = 0; i < TP; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int64_t done = 0; done < mine; ++done) {
+    const Walk now = at;
+    const bool last = move(at, kDownWaves) || done + 1 == mine;
+    typename Ring::Frag f;
+    ring.take(f, issued < mine);
+    issue();
+    Ring::multiply(f, [&](int i, int r) { return i * 16 + quarter * 4 + r >= border; }, acc);
+    if (last) {
+      const int col = now.c0 + m;
+      if (col < tokens(now)) {
+        const int p = l.off[now.place] + col;
+        const float gate = l.weight[p];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(w, acc[0][j][r], v[r]);
-      *o = v;
+        for (int i = 0; i < TP; ++i) {
+          f32x4* o = reinterpret_cast<f32x4*>(out + l.token[p] * P + i * 16 + quarter * 4);
+          f32x4 v = *o;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(gate, acc[i][r], v[r]);
+          *o = v;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < TP; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
   }
 }
 
-template <int EL, int MOST>
-__global__ __launch_bounds__(kLayerThreads, MOST == 1 ? 4 : 2) void layer_down_kernel(LayerArgs a) {
-  extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ int wave_sums[kLayerWaves];
-  const Lists l = make_lists<true>(a, lds, wave_sums);
-  float* sums = reinterpret_cast<float*>(lds + lists_layout(a.N, a.K, a.E).end);      // [wavefront][token][16]
+template <int EL, int WL, int RING>
+__global__ __launch_bounds__(kDownWaves* kWave) void layer_down_kernel(LayerArgs a) {
+  constexpr int P = (WL + 1) / 2 * 16, THREADS = kDownWaves * kWave;
+  extern __shared__ __align__(1024) uint8_t lds[];                    // rings, sums, lists
+  float* sums = reinterpret_cast<float*>(lds + RING);                 // [wavefront][token][P]
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-  float* out = sums + wave * a.N * 16;
-  for (int i = lane_id(); i < a.N * 4; i += kWave) reinterpret_cast<f32x4*>(out)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  __builtin_amdgcn_wave_barrier();
-  constexpr int S = StreamType<EL>::kStep;
-  const int h0 = blockIdx.x * 16, steps = (a.I + S - 1) / S;
-  const int64_t total = static_cast<int64_t>(l.count) * steps;
-  int64_t at = total * wave / kLayerWaves;
-  const int64_t end = total * (wave + 1) / kLayerWaves;
-  while (at < end) {
-    const int place = static_cast<int>(at / steps), s0 = static_cast<int>(at - static_cast<int64_t>(place) * steps);
-    const int s1 = static_cast<int>(end - at < steps - s0 ? s0 + (end - at) : steps);
-    const int n = __builtin_amdgcn_readfirstlane(l.off[place + 1] - l.off[place]);
-    for (int c0 = 0; c0 < n; c0 += MOST * 16) {
-      const int left = n - c0;
-      if (MOST == 1 || left <= 16) down_part<EL, 1>(a, l, place, h0, s0, s1, c0, min(left, 16), out);
-      else if constexpr (MOST > 1) {
-        if (left <= 32) down_part<EL, 2>(a, l, place, h0, s0, s1, c0, left, out);
-        else down_part<EL, 4>(a, l, place, h0, s0, s1, c0, min(left, 64), out);
-      }
-    }
-    at += s1 - s0;
+  float* out = sums + wave * a.N * P;
+  for (int i = lane_id(); i < a.N * (P / 4); i += kWave) reinterpret_cast<f32x4*>(out)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  uint8_t* rest = lds + RING + kDownWaves * a.N * P * 4;
+  int* wave_sums = reinterpret_cast<int*>(rest);
+  const Lists l = make_lists<kDownWaves, true>(a, rest + 64, wave_sums);
+  const int most = most_tokens<kDownWaves>(l, wave_sums);
+  if constexpr (EL == kGemmBf16) {
+    if (most <= 8) down_part<EL, WL, 1, RING>(a, l, lds, out);
+    else down_part<EL, WL, 2, RING>(a, l, lds, out);
+  } else {
+    if (most <= 4) down_part<EL, WL, 1, RING>(a, l, lds, out);
+    else if (most <= 8) down_part<EL, WL, 2, RING>(a, l, lds, out);
+    else down_part<EL, WL, 4, RING>(a, l, lds, out);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.N * 8; i += kLayerThreads) {
-    const int t = i / 8, p = i % 8 * 2;
-    if (h0 + p >= a.H) continue;
+  const int h0 = blockIdx.x * a.tile, pairs = min(a.tile, a.H - h0) / 2;
+  for (int i = threadIdx.x; i < a.N * pairs; i += THREADS) {
+    const int t = i / pairs, p = (i - t * pairs) * 2;
     float x = 0.f, y = 0.f;
 #pragma unroll
-    for (int w = 0; w < kLayerWaves; ++w) {
-      x += sums[(w * a.N + t) * 16 + p];
-      y += sums[(w * a.N + t) * 16 + p + 1];
+    for (int k = 0; k < kDownWaves; ++k) {
+      x += sums[(k * a.N + t) * P + p];
+      y += sums[(k * a.N + t) * P + p + 1];
     }
     const int64_t o = static_cast<int64_t>(t) * a.H + h0 + p;
     if (a.residual) {
@@ -257,21 +376,32 @@ __global__ __launch_bounds__(kLayerThreads, MOST == 1 ? 4 : 2) void layer_down_k
   }
 }
 
-template <int EL, int MOST>
-hipError_t launch_sized(const LayerArgs& a, hipStream_t st) {
-  const ListsLayout at = lists_layout(a.N, a.K, a.E);
-  const int64_t units = static_cast<int64_t>(at.most) * ((a.I + 15) / 16);
-  const unsigned most = MOST == 1 ? 512 : 256;
-  layer_up_kernel<EL, MOST><<<static_cast<unsigned>(units < most ? units : most), kLayerThreads, static_cast<unsigned>(at.end), st>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  layer_down_kernel<EL, MOST><<<(a.H + 15) / 16, kLayerThreads, static_cast<unsigned>(at.end + kLayerWaves * a.N * 64), st>>>(a);
+template <int EL, int WL>
+hipError_t launch_down(const LayerArgs& a, unsigned rest, hipStream_t st) {
+  const unsigned tiles = (a.H + a.tile - 1) / a.tile, threads = kDownWaves * kWave;
+  const unsigned sums = kDownWaves * a.N * ((WL + 1) / 2) * 64;
+  if (kDownRing + sums + rest <= kMostLds) layer_down_kernel<EL, WL, kDownRing><<<tiles, threads, kDownRing + sums + rest, st>>>(a);
+  else layer_down_kernel<EL, WL, kDownRingShort><<<tiles, threads, kDownRingShort + sums + rest, st>>>(a);
   return hipGetLastError();
 }
 
 template <int EL>
 hipError_t launch_typed(const LayerArgs& a, hipStream_t st) {
-  return a.N <= 16 ? launch_sized<EL, 1>(a, st) : launch_sized<EL, 4>(a, st);
+  const ListsLayout lists = lists_layout(a.N, a.K, a.E);
+  const int64_t units = static_cast<int64_t>(lists.most) * ((a.I + 15) / 16) * ((a.N + 15) / 16);
+  const unsigned grid = static_cast<unsigned>(units < 256 ? units : 256), rest = static_cast<unsigned>(lists.end) + 64;
+  if (kUpRing + kUpSums + rest <= kMostLds) layer_up_kernel<EL, kUpRing><<<grid, kUpWaves * kWave, kUpRing + kUpSums + rest, st>>>(a);
+  else layer_up_kernel<EL, kUpRingShort><<<grid, kUpWaves * kWave, kUpRingShort + kUpSums + rest, st>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  // as many channels a workgroup as make whole rounds of the 256 CUs, 8 to 32
+  LayerArgs d = a;
+  const int rounds = (a.H + 256 * 32 - 1) / (256 * 32);
+  d.tile = ((a.H + 256 * rounds - 1) / (256 * rounds) + 1) / 2 * 2;
+  if (d.tile < 8) d.tile = 8;
+  if (d.tile <= 8) return launch_down<EL, 1>(d, rest, st);
+  if (d.tile <= 16) return launch_down<EL, 2>(d, rest, st);
+  return launch_down<EL, 4>(d, rest, st);
 }
 
 }  // namespace

@@ -7,56 +7,80 @@ namespace miep {
 
 namespace {
 
-// A workgroup computes 16 of the weight's rows (SwiGLU: 8 of gate and the same 8
-// of up, so that narrow products still spread over the GPU) for all rows of x;
-// its wavefronts take every WAVES-th step of the contraction.
-template <int WAVES, int TQ, bool SWIGLU>
-__global__ __launch_bounds__(WAVES * kWave) void linear_few_kernel(LinearArgs a) {
-  __shared__ __align__(16) float sums[WAVES][TQ][16][16];
+// At most 16 rows of x: a workgroup computes 16 * TP of the weight's rows (SwiGLU:
+// half of them gate and the same ones of up, so that it has both); its wavefronts
+// take every 8th step of the contraction.
+template <int TP, int XL, bool SWIGLU>
+__global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs a) {
+  constexpr int WAVES = 8, P = 16 * TP, RING = 16384;
+  using Ring = StreamRing<kGemmBf16, 2 * TP, XL, RING>;
+  __shared__ __align__(1024) uint8_t lds_mem[WAVES * RING];
+  __shared__ __align__(16) float sums[WAVES][16][P];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int m = lane & 15, quarter = lane >> 4;
   const int rows = static_cast<int>(a.rows), half = a.N / 2;
-  const int p0 = blockIdx.x * (SWIGLU ? 8 : 16);
-  StreamSource<kGemmBf16, 1, TQ> src;
-  src.w = reinterpret_cast<const uint8_t*>(a.w) + static_cast<int64_t>(p0) * a.K * 2;
-  src.x = reinterpret_cast<const uint8_t*>(a.x);
-  src.C = a.K;
-  const uint32_t row = SWIGLU ? (m & 7) + (m >> 3) * half : min(m, a.N - 1 - p0);
-  src.woff[0] = row * static_cast<uint32_t>(a.K) * 2 + quarter * 16;
+  const int p0 = blockIdx.x * (SWIGLU ? P / 2 : P);
+  const uint32_t pitch = static_cast<uint32_t>(a.K) * 2;
+  const uint8_t* w = reinterpret_cast<const uint8_t*>(a.w) + static_cast<int64_t>(p0) * pitch;
+  const uint8_t* x = reinterpret_cast<const uint8_t*>(a.x);
+  uint32_t woff[2 * TP], xoff[XL];
 #pragma unroll
-  for (int j = 0; j < TQ; ++j) src.xoff[j] = static_cast<uint32_t>(min(j * 16 + m, rows - 1)) * static_cast<uint32_t>(a.K) * 2 + quarter * 16;
-  f32x4 acc[1][TQ];
+  for (int i = 0; i < 2 * TP; ++i) {
+    const int at = Ring::w_row(i);
+    const uint32_t row = SWIGLU ? min(at % (P / 2), half - 1 - p0) + at / (P / 2) * half : min(at, a.N - 1 - p0);
+    woff[i] = row * pitch + Ring::w_chunk(i) * 16;
+  }
 #pragma unroll
-  for (int j = 0; j < TQ; ++j) acc[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  stream_steps<TQ == 1 ? 4 : TQ == 2 || WAVES == 8 ? 2 : 1>(src, wave, WAVES, (a.K + 63) / 64, acc);
+  for (int i = 0; i < XL; ++i) xoff[i] = min(Ring::x_row(i), rows - 1) * pitch + Ring::x_chunk(i) * 16;
+  f32x4 acc[TP];
 #pragma unroll
-  for (int j = 0; j < TQ; ++j) *reinterpret_cast<f32x4*>(&sums[wave][j][m][quarter * 4]) = acc[0][j];
+  for (int i = 0; i < TP; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  Ring ring((uint32_t)(uintptr_t)(lds_byte*)lds_mem + wave * RING);
+  const int steps = (a.K + 63) / 64, n = wave < steps ? (steps - wave + WAVES - 1) / WAVES : 0;
+  auto issue = [&](int i) MIEP_INLINE {
+    const int step = wave + i * WAVES;
+    ring.issue(w + step * 128ll, woff, x + step * 128ll, xoff, nullptr, a.K - step * 64);
+  };
+#pragma unroll
+  for (int i = 0; i < Ring::kDepth; ++i)
+    if (i < n) issue(i);
+  for (int i = 0; i < n; ++i) {
+    typename Ring::Frag f;
+    ring.take(f, i + Ring::kDepth <= n);
+    if (i + Ring::kDepth < n) issue(i + Ring::kDepth);
+    Ring::multiply(f, [](int, int) { return false; }, acc);
+  }
+#pragma unroll
+  for (int i = 0; i < TP; ++i) *reinterpret_cast<f32x4*>(&sums[wave][m][i * 16 + quarter * 4]) = acc[i];
   __syncthreads();
-  constexpr int PAIRS = SWIGLU ? 4 : 8;
+  constexpr int PAIRS = SWIGLU ? P / 4 : P / 2;
   for (int i = threadIdx.x; i < rows * PAIRS; i += WAVES * kWave) {
     const int r = i / PAIRS, p = i % PAIRS * 2;
     const EpilogueRow to(a.epi, a.out, r, a.N);
-    float x = 0.f, y = 0.f, ux = 0.f, uy = 0.f;
+    float v[2] = {}, u[2] = {};
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-      const float* s = sums[w][r / 16][r % 16] + p;
-      x += s[0];
-      y += s[1];
+    for (int k = 0; k < WAVES; ++k) {
+      const float* s = sums[k][r] + p;
+      v[0] += s[0];
+      v[1] += s[1];
       if constexpr (SWIGLU) {
-        ux += s[8];
-        uy += s[9];
+        u[0] += s[P / 2];
+        u[1] += s[P / 2 + 1];
       }
     }
-    if constexpr (SWIGLU) to.swiglu2(p0 + p, x, y, ux, uy);
-    else if (p0 + p < a.N) to.plain2(p0 + p, x, y);
+    if constexpr (SWIGLU) {
+      if (p0 + p < half) to.swiglu(p0 + p, v, u);
+    } else if (p0 + p < a.N) {
+      to.plain(p0 + p, v);
+    }
   }
 }
 
-template <int WAVES, bool SWIGLU>
-void launch_few(const LinearArgs& a, unsigned grid, hipStream_t st) {
-  if (a.rows <= 16) linear_few_kernel<WAVES, 1, SWIGLU><<<grid, WAVES * kWave, 0, st>>>(a);
-  else if (a.rows <= 32) linear_few_kernel<WAVES, 2, SWIGLU><<<grid, WAVES * kWave, 0, st>>>(a);
-  else linear_few_kernel<WAVES, 4, SWIGLU><<<grid, WAVES * kWave, 0, st>>>(a);
+template <int TP, bool SWIGLU>
+void launch_few(const LinearArgs& a, hipStream_t st) {
+  const unsigned grid = SWIGLU ? (a.N / 2 + 8 * TP - 1) / (8 * TP) : (a.N + 16 * TP - 1) / (16 * TP);
+  if (a.rows <= 8) linear_few_kernel<TP, 1, SWIGLU><<<grid, 512, 0, st>>>(a);
+  else linear_few_kernel<TP, 2, SWIGLU><<<grid, 512, 0, st>>>(a);
 }
 
 // Gradient through the activation: a lane 8 columns, a wavefront 512, the four
@@ -161,16 +185,13 @@ __global__ __launch_bounds__(256) void bias_zero_kernel(float* p, int n) {
 hipError_t launch_linear(const LinearArgs& a, hipStream_t st) {
   if (a.rows == 0) return hipSuccess;
   if (a.rows <= kLinearFewRows) {
-    const bool swiglu = a.epi.act == kActSwiglu;
-    const unsigned tiles = static_cast<unsigned>(swiglu ? a.N / 16 : (a.N + 15) / 16);
-    // one workgroup a CU: twice the wavefronts keep as many loads in flight
-    if (tiles <= 256) {
-      if (swiglu) launch_few<16, true>(a, tiles, st);
-      else launch_few<16, false>(a, tiles, st);
-    } else {
-      if (swiglu) launch_few<8, true>(a, tiles, st);
-      else launch_few<8, false>(a, tiles, st);
-    }
+    // one workgroup a CU: tiles of 32 rows of the weight where 16 make more than
+    // the GPU holds at a time
+    const bool swiglu = a.epi.act == kActSwiglu, wide = (a.N + 15) / 16 > 256;
+    if (swiglu && wide) launch_few<2, true>(a, st);
+    else if (swiglu) launch_few<1, true>(a, st);
+    else if (wide) launch_few<2, false>(a, st);
+    else launch_few<1, false>(a, st);
     return hipGetLastError();
   }
   GemmRowsArgs g{};

@@ -1,37 +1,26 @@
 // stream.h -- products of a few rows, where reading the weights is the cost.
 //
-//   acc[tp][tq] = sum_c W[row(tp, i)][c] * X[col(tq, j)][c]      16 x 16 each
+//   acc[i] = sum_c W[row(i, m)][c] * X[col(n)][c]      16 rows of W x 16 of X each
 //
-// The weights go from memory straight to registers (each is used by one
-// wavefront once, so LDS would only add a trip), 16 bytes a lane: a load takes 64
-// consecutive bytes of each of 16 rows.  The contraction's order is free, so E4M3
-// codes need no reordering for the bf16 MFMAs that they are converted to: a
-// lane's 16 codes meet the 16 channels of X at the same places.  A wavefront
-// keeps kAhead steps of 128 bytes a row in flight; the wavefronts of a workgroup
-// share a tile's contraction and add their sums up in LDS, in order.
+// Every step of 128 bytes a row of W comes to LDS by asynchronous loads, into a
+// ring that a wavefront has for itself, so without barriers; the wavefronts of a
+// workgroup share a contraction's steps and add their sums up in LDS, in order.
+// The loads are what a CU has too little of: a load whose four neighbouring lanes
+// lie in different 128-byte lines (an MFMA operand straight into registers) took
+// 57 cycles a KiB, 18 bytes a cycle and CU; eight lanes a line take under half of
+// that.  The contraction's order is free, so E4M3 codes need no reordering for
+// the bf16 MFMAs that they are converted to: a lane's 16 codes meet the 16
+// channels of X at the same places.
 #pragma once
 
 #include "gemm.h"
 
 namespace miep {
 
-// E4M3 codes (products of a converted code and a bf16 number are exact in fp32,
-// so unlike the E4M3 MFMA's nothing is cut) with a scale a 128 x 128 block.
-template <int EL>
-struct StreamType {
-  static constexpr bool kFp8 = EL != kGemmBf16;
-  static constexpr int kStep = kFp8 ? 128 : 64;                       // channels
-  static constexpr int kXLoads = kFp8 ? 4 : 2;                        // 16-byte loads of X a step and lane
-};
+__device__ __forceinline__ int swz8(int row) { return (row >> 1) & 7; }
 
-template <int EL, int TP, int TQ>
-struct StreamFrag {
-  u32x4 w[TP][2];
-  u32x4 x[TQ][StreamType<EL>::kXLoads];
-  float s[TP];
-};
-
-// Two E4M3 codes of v (the low or the high half) as bf16, exactly.
+// Two E4M3 codes of v (the low or the high half) as bf16, exactly: their products
+// with bf16 numbers are exact in fp32, so nothing is cut as the E4M3 MFMA cuts.
 template <bool HIGH>
 __device__ __forceinline__ uint32_t bf16x2_of_e4m3(uint32_t v) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -43,135 +32,123 @@ __device__ __forceinline__ bf16x8 bf16x8_of_e4m3(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(bf16x8, t);
 }
 
-__device__ __forceinline__ u32x4 load16(const uint8_t* base, uint32_t off) {
-  return *reinterpret_cast<const u32x4*>(base + off);
+// A pointer that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v)), hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-// A scale of block (row, step): fp32, or the exponent byte of a power of two.
-template <int EL>
-__device__ __forceinline__ float block_scale(const void* s, int64_t at) {
-  if constexpr (EL == kGemmFp8) return static_cast<const float*>(s)[at];
-  else return __uint_as_float(static_cast<uint32_t>(static_cast<const uint8_t*>(s)[at]) << 23);
-}
+// A wavefront's ring of steps in BYTES bytes of LDS: the rows of W that WL loads of
+// 1 KiB bring (8 each), those of X that XL loads bring (8 each, E4M3 4: its step is
+// 128 channels), and E4M3's two scales, of the blocks that the rows of W lie in
+// (read when they are needed, they would stop a wavefront for a memory's latency at
+// every tile and expert: 64 tokens over 55 experts, second product, 260 -> 150 us).
+template <int EL, int WL, int XL, int BYTES>
+struct StreamRing {
+  static constexpr int TP = (WL + 1) / 2;                             // 16 x 16 results
+  static constexpr bool kFp8 = EL != kGemmBf16;
+  static constexpr int kChannels = kFp8 ? 128 : 64;                   // of a step
+  static constexpr int kXRow = kChannels * 2, kXRows = XL * 1024 / kXRow;
+  static constexpr int kWBytes = WL * 1024, kScales = kWBytes + XL * 1024, kStep = kScales + (kFp8 ? 256 : 0);
+  static constexpr int kDepth = BYTES / kStep < 8 ? BYTES / kStep : 8;
+  static constexpr int kLoads = WL + XL + (kFp8 ? 1 : 0);
+  static_assert(kDepth >= 1 && kDepth * kLoads < 64, "ring");
 
-// What a wavefront multiplies: bases are uniform, offsets a lane's own (row *
-// pitch + 16 * quarter for W; X's of a step's first 16 bytes).
-template <int EL, int TP, int TQ>
-struct StreamSource {
-  const uint8_t* w;
-  const uint8_t* x;
-  uint32_t woff[TP], xoff[TQ];
-  const void* scales;          // E4M3: of the weight's matrix
-  int64_t srow[TP];            // E4M3: first scale of the tile's block of rows
-  int C;                       // channels; bf16: behind them both operands read as zeros
+  uint32_t lds;
+  int head, tail;                                                     // buffers: next to fill, next to read
 
-  // A step of whole 128 bytes a row.
-  __device__ __forceinline__ void load(StreamFrag<EL, TP, TQ>& f, int step) const {
-    constexpr bool F8 = StreamType<EL>::kFp8;
-    const uint8_t* wb = w + static_cast<int64_t>(step) * 128;
-    const uint8_t* xb = x + static_cast<int64_t>(step) * (F8 ? 256 : 128);
+  struct Frag {
+    u32x4 w[TP][2];
+    u32x4 x[kFp8 ? 4 : 2];
+    float s[2];
+  };
+
+  __device__ __forceinline__ explicit StreamRing(uint32_t at) : lds(at), head(0), tail(0) {}
+
+  // Where the lane's 16 bytes of W load i lie in a step of 128 bytes a row (row
+  // i * 8 + lane / 8), and of X load i.
+  static __device__ __forceinline__ int w_row(int i) { return i * 8 + lane_id() / 8; }
+  static __device__ __forceinline__ int w_chunk(int i) { return (lane_id() & 7) ^ swz8(w_row(i) & 15); }
+  static __device__ __forceinline__ int x_row(int i) { return kFp8 ? i * 4 + lane_id() / 16 : i * 8 + lane_id() / 8; }
+  static __device__ __forceinline__ int x_chunk(int i) {
+    if constexpr (kFp8) return (lane_id() & 15) ^ (x_row(i) & 15);
+    else return (lane_id() & 7) ^ swz8(x_row(i));
+  }
+
+  // The next step's loads.  `scale`: the lane's, of the first block in even lanes
+  // and of the second in odd ones (any in bf16).  `left`: channels of the contraction from this step
+  // on; bf16 behind its end reads zeros in both operands (0 * NaN would not be 0).
+  __device__ __forceinline__ void issue(const uint8_t* w, const uint32_t (&woff)[WL], const uint8_t* x, const uint32_t (&xoff)[XL], const uint8_t* scale, int left) {
+    w = uniform(w);
+    x = uniform(x);
+    const uint32_t to = lds + head * kStep;
+    head = head == kDepth - 1 ? 0 : head + 1;
+    if (kFp8 || left >= kChannels) {
 #pragma unroll
-    for (int i = 0; i < TP; ++i)
+      for (int i = 0; i < WL; ++i) dma16s(w, woff[i], to + i * 1024);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) f.w[i][h] = load16(wb + h * 64, woff[i]);
+      for (int i = 0; i < XL; ++i) dma16s(x, xoff[i], to + kWBytes + i * 1024);
+      if constexpr (EL == kGemmFp8) dma4(scale, to + kScales);
+      else if constexpr (kFp8) dma1(scale, to + kScales);
+    } else {
 #pragma unroll
-    for (int j = 0; j < TQ; ++j)
+      for (int i = 0; i < WL; ++i)
+        dma16(w_chunk(i) * 8 < left ? static_cast<const void*>(w + woff[i]) : static_cast<const void*>(g_zero16), to + i * 1024);
 #pragma unroll
-      for (int h = 0; h < StreamType<EL>::kXLoads; ++h)
-        f.x[j][h] = load16(xb + (F8 ? (h >> 1) * 128 + (h & 1) * 16 : h * 64), xoff[j]);
-    if constexpr (F8) {
-#pragma unroll
-      for (int i = 0; i < TP; ++i) f.s[i] = block_scale<EL>(scales, srow[i] + step);
+      for (int i = 0; i < XL; ++i)
+        dma16(x_chunk(i) * 8 < left ? static_cast<const void*>(x + xoff[i]) : static_cast<const void*>(g_zero16), to + kWBytes + i * 1024);
     }
   }
-  // bf16, the last step of a contraction that is not whole: behind its end both
-  // operands are zeros (0 * NaN would not be 0).
-  __device__ __forceinline__ void load_end(StreamFrag<EL, TP, TQ>& f, int step) const {
-    const u32x4 zero = {0u, 0u, 0u, 0u};
-    const int c = step * 64 + (lane_id() >> 4) * 8;
+
+  // Waits for the oldest step, of which `more` say that kDepth - 1 others have been
+  // issued behind it, and takes it to registers; its buffer is free then.
+  __device__ __forceinline__ void take(Frag& f, bool more) {
+    if (more) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kDepth - 1) * kLoads) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const uint32_t at = lds + tail * kStep;
+    tail = tail == kDepth - 1 ? 0 : tail + 1;
+    const int m = lane_id() & 15, quarter = lane_id() >> 4;
+    // (rows that were not loaded: any)
+    const int wm = WL == 1 ? m & 7 : m, xm = m & (kXRows - 1);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool in = c + h * 32 < C;
-      const int64_t at = static_cast<int64_t>(step) * 128 + h * 64;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < TP; ++i) f.w[i][h] = in ? load16(w + at, woff[i]) : zero;
+      for (int i = 0; i < TP; ++i) f.w[i][h] = lds_read<u32x4>(at + i * 2048 + wm * 128 + ((h * 4 + quarter) ^ swz8(wm)) * 16);
 #pragma unroll
-      for (int j = 0; j < TQ; ++j) f.x[j][h] = in ? load16(x + at, xoff[j]) : zero;
+    for (int h = 0; h < (kFp8 ? 4 : 2); ++h) {
+      const int chunk = kFp8 ? (((h >> 1) * 4 + quarter) * 2 + (h & 1)) ^ xm : (h * 4 + quarter) ^ swz8(xm);
+      f.x[h] = lds_read<u32x4>(at + kWBytes + xm * kXRow + chunk * 16);
+    }
+    if constexpr (kFp8) {
+      const u32x2 t = lds_read<u32x2>(at + kScales);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) f.s[i] = __uint_as_float(EL == kGemmFp8 ? t[i] : t[i] << 23);   // a power of two's exponent byte
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+
+  // acc += W * X of a step; E4M3: second(i, r) says whether row r of result i's four
+  // lies in the second block.
+  template <class SECOND>
+  static __device__ __forceinline__ void multiply(const Frag& f, SECOND second, f32x4 (&acc)[TP]) {
+#pragma unroll
+    for (int i = 0; i < TP; ++i) {
+      if constexpr (kFp8) {
+        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16x8_of_e4m3(f.w[i][h >> 1][(h & 1) * 2], f.w[i][h >> 1][(h & 1) * 2 + 1]),
+                                                      __builtin_bit_cast(bf16x8, f.x[h]), d, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(d[r], second(i, r) ? f.s[1] : f.s[0], acc[i][r]);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.w[i][h]), __builtin_bit_cast(bf16x8, f.x[h]), acc[i], 0, 0, 0);
+      }
     }
   }
 };
-
-template <int EL, int TP, int TQ>
-__device__ __forceinline__ void stream_multiply(const StreamFrag<EL, TP, TQ>& f, f32x4 (&acc)[TP][TQ]) {
-#pragma unroll
-  for (int i = 0; i < TP; ++i) {
-    if constexpr (StreamType<EL>::kFp8) {
-      f32x4 d[TQ];
-#pragma unroll
-      for (int j = 0; j < TQ; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const bf16x8 p = bf16x8_of_e4m3(f.w[i][h >> 1][(h & 1) * 2], f.w[i][h >> 1][(h & 1) * 2 + 1]);
-#pragma unroll
-        for (int j = 0; j < TQ; ++j)
-          d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, __builtin_bit_cast(bf16x8, f.x[j][h]), d[j], 0, 0, 0);
-      }
-#pragma unroll
-      for (int j = 0; j < TQ; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[j][r], f.s[i], acc[i][j][r]);
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < TQ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.w[i][h]),
-                                                              __builtin_bit_cast(bf16x8, f.x[j][h]), acc[i][j], 0, 0, 0);
-    }
-  }
-}
-
-// acc += the steps first, first + stride, ... below `end`, AHEAD of them in
-// flight.
-template <int AHEAD, int EL, int TP, int TQ>
-__device__ __forceinline__ void stream_steps(const StreamSource<EL, TP, TQ>& src, int first, int stride, int end, f32x4 (&acc)[TP][TQ]) {
-  const int whole = min(end, src.C / StreamType<EL>::kStep);
-  const int n = first < whole ? (whole - first + stride - 1) / stride : 0;
-  StreamFrag<EL, TP, TQ> f[AHEAD + 1];
-  // (The first loads stand apart in either branch: where the compiler sees that
-  // they may be missing, it has the loop wait for all loads, not for its own.)
-  int i = 0;
-  if (n > 2 * AHEAD) {
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k) src.load(f[k], first + k * stride);
-    do {
-#pragma unroll
-      for (int d = 0; d <= AHEAD; ++d) {
-        src.load(f[(d + AHEAD) % (AHEAD + 1)], first + (i + d + AHEAD) * stride);
-        __builtin_amdgcn_sched_barrier(0);
-        stream_multiply(f[d], acc);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      i += AHEAD + 1;
-    } while (i + 2 * AHEAD < n);
-  } else {
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k)
-      if (k < n) src.load(f[k], first + k * stride);
-  }
-  // AHEAD .. 2 * AHEAD steps are left (or as many as there are), the first of
-  // them under way
-#pragma unroll
-  for (int d = 0; d < 2 * AHEAD; ++d) {
-    if (d < AHEAD && i + d + AHEAD < n) src.load(f[(d + AHEAD) % (AHEAD + 1)], first + (i + d + AHEAD) * stride);
-    if (i + d < n) stream_multiply(f[d % (AHEAD + 1)], acc);
-  }
-  if constexpr (!StreamType<EL>::kFp8) {
-    if (whole < end && first <= whole && (whole - first) % stride == 0) {
-      src.load_end(f[0], whole);
-      stream_multiply(f[0], acc);
-    }
-  }
-}
 
 }  // namespace miep

@@ -584,7 +584,7 @@ miep_status miep_linear_wgrad(const uint16_t* dy, const uint16_t* x, int64_t row
  *   residual [N][H] bf16, nullable; may be y itself
  *   workspace [N*K][I] bf16, of one call at a time
  * N at most 128; H, I % 8 == 0 (E4M3: % 128 == 0); weights of one expert under 4 GiB, workspace too; E * ceil(N/64) *
- * 8 + 6 * min(E, N*K) + 8 * N*K bytes at most 65,400.  Larger batches: dispatch.
+ * 8 + 6 * min(E, N*K) + 8 * N*K bytes at most 49,000.  Larger batches: dispatch.
  * Errors: EINVAL for null pointers, sizes, flags; EUNSUPPORTED for the limits above. */
 typedef struct miep_layer {
   int32_t num_tokens;    /* N >= 0                        */
