@@ -1124,6 +1124,7 @@ miep_status miep_gate_topk(const miep_gate* g, const void* logits, const float* 
   miep::GateArgs a{};
   miep_status st = gate_args(g, logits, &a);
   if (st != MIEP_OK) return st;
+  if ((st = check_array(bias, false, "bias")) != MIEP_OK) return st;
   if (a.N > 0 && (!topk_idx || !topk_weights)) return fail(MIEP_EINVAL, "topk_idx / topk_weights NULL");
   a.bias = bias;
   a.idx = topk_idx;

@@ -389,7 +389,7 @@ struct GateArgs {
   int groups, top_groups, group_best;
   float scale;
   int f32;                     // logits (and their gradient): fp32, or bf16
-  int per_group, wide_loads;   // set by the launcher
+  int per_group, lanes, each;  // set by the launcher
   FastDiv per_div;             // set by the launcher
   const void* logits;          // [N][E]
   const float* bias;           // [E] or null

@@ -262,3 +262,28 @@ def test_streams_graph_and_a_row_left_alone():
         want = miep.gate_topk(logits, K, "sigmoid", renormalize=True)
         assert torch.equal(idx[:N], want[0]) and torch.equal(w[:N], want[1])
         assert (idx[N] == -7).all() and (w[N] == -7).all()
+
+
+@pytest.mark.parametrize("E,groups,top", [(64, 1, 1), (64, 4, 2), (160, 8, 3), (256, 1, 1), (256, 8, 4), (384, 8, 4), (100, 5, 2), (512, 16, 5), (66, 1, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_near_neighbours(E, groups, top, score, dtype):
+    """Many logits (and with them scores, and sums of two) a rounding or a few apart from another expert's, at every
+    place of the order: a choice by 32 bits alone is by chance there."""
+    N, K = 400, min(7, E // groups * top)
+    g = gen(E + groups)
+    l = torch.randn(N, E, generator=g)
+    half = E // 2
+    step = 2.0 ** -torch.randint(17, 25, (N, half), generator=g).float()
+    near = l[:, :half] * (1 + step * torch.randint(-1, 2, (N, half), generator=g).float())
+    l[:, half:2 * half] = torch.where(torch.rand(N, half, generator=g) < 0.6, near, l[:, half:2 * half])
+    l = l[:, torch.randperm(E, generator=g)].to(dtype)
+    check(l, K, score, None, groups, top, 2, True)
+    check(l, K, score, None, groups, top, 1)
+    b = (torch.randn(E, generator=g) * 0.05).float()
+    b[::2] = 0.0
+    check(l, K, score, b, groups, top, 2, True, 2.5)
+    # all within a few roundings of each other: more candidates than 16
+    if groups == 1:
+        check((1 + l * 2.0 ** -21).float(), K, score, torch.zeros(E), 1, 1, 2)
+        check((1 + l * 2.0 ** -21).float(), K, score)
