@@ -86,24 +86,9 @@ void launch_few(const LinearArgs& a, hipStream_t st) {
 // Gradient through the activation: a lane 8 columns, a wavefront 512, the four
 // wavefronts of a workgroup every fourth row of its part.  The bias gradient is
 // summed from the unrounded values: by lane, by wavefront, then over the parts.
-template <bool DYF32>
-__device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
-  if constexpr (DYF32) {
-    const float* f = static_cast<const float*>(p) + at;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = f[i];
-  } else {
-    const v4u t = ld16(static_cast<const uint16_t*>(p) + at);
-    v[0] = bf16_lo(t.x); v[1] = bf16_hi(t.x); v[2] = bf16_lo(t.y); v[3] = bf16_hi(t.y);
-    v[4] = bf16_lo(t.z); v[5] = bf16_hi(t.z); v[6] = bf16_lo(t.w); v[7] = bf16_hi(t.w);
-  }
-}
-__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
-  *reinterpret_cast<v4u*>(p) = v4u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-}
-
-template <bool DYF32, bool SWIGLU>
+template <bool DYF32, int ACT>
 __global__ __launch_bounds__(256) void act_backward_kernel(ActBackwardArgs a) {
+  constexpr bool SWIGLU = ACT == kActSwiglu;
   __shared__ float sums[4][512][SWIGLU ? 2 : 1];
   const int lane = lane_id(), wave = threadIdx.x / kWave;
   const int width = SWIGLU ? a.N / 2 : a.N;
@@ -111,36 +96,56 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackwardArgs a) {
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * a.rows_per_part;
   const int64_t r1 = r0 + a.rows_per_part < a.rows ? r0 + a.rows_per_part : a.rows;
   float sg[8] = {}, su[8] = {};
-  if (c < width) {
-    for (int64_t r = r0 + wave; r < r1; r += 4) {
-      float dy[8], z[8], d[8];
-      load8<DYF32>(a.dy, r * width + c, dy);
+  // four rows' loads under way together: a wavefront has as few as four rows
+  constexpr int ROWS = 4;
+  for (int64_t r = r0 + wave; c < width && r < r1; r += 4 * ROWS) {
+    v4u dy[ROWS][DYF32 ? 2 : 1], z[ROWS], u[SWIGLU ? ROWS : 1];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const int64_t row = r + 4 * k < r1 ? r + 4 * k : r;
+      const uint8_t* d = static_cast<const uint8_t*>(a.dy) + (row * width + c) * (DYF32 ? 4 : 2);
+      dy[k][0] = ld16(d);
+      if constexpr (DYF32) dy[k][1] = ld16(d + 16);
+      if (ACT != kActNone) z[k] = ld16(a.z + row * a.N + c);
+      if constexpr (SWIGLU) u[k] = ld16(a.z + row * a.N + width + c);
+    }
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const int64_t row = r + 4 * k;
+      if (row >= r1) break;
+      float g[8], d[8];
+      if constexpr (DYF32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          g[i * 4] = __uint_as_float(dy[k][i].x); g[i * 4 + 1] = __uint_as_float(dy[k][i].y);
+          g[i * 4 + 2] = __uint_as_float(dy[k][i].z); g[i * 4 + 3] = __uint_as_float(dy[k][i].w);
+        }
+      } else {
+        widen(dy[k][0], g);
+      }
       if constexpr (SWIGLU) {
-        float u[8], du[8];
-        load8<false>(a.z, r * a.N + c, z);
-        load8<false>(a.z, r * a.N + width + c, u);
+        float gate[8], up[8], du[8];
+        widen(z[k], gate);
+        widen(u[k], up);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float s = sigmoid(z[i]);
-          d[i] = dy[i] * u[i] * s * (1.f + z[i] * (1.f - s));
-          du[i] = dy[i] * (z[i] * s);
+          const float s = sigmoid(gate[i]);
+          d[i] = g[i] * up[i] * s * (1.f + gate[i] * (1.f - s));
+          du[i] = g[i] * (gate[i] * s);
           sg[i] += d[i];
           su[i] += du[i];
         }
-        if (a.dz) store8(a.dz + r * a.N + width + c, du);
+        if (a.dz) *reinterpret_cast<v4u*>(a.dz + row * a.N + width + c) = narrow(du);
       } else {
-        if (a.act == kActNone) {
+        float x[8];
+        if (ACT != kActNone) widen(z[k], x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] = dy[i];
-        } else {
-          load8<false>(a.z, r * a.N + c, z);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] = dy[i] * activate_slope(z[i], a.act);
+        for (int i = 0; i < 8; ++i) {
+          d[i] = ACT == kActNone ? g[i] : g[i] * activate_slope(x[i], ACT);
+          sg[i] += d[i];
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sg[i] += d[i];
       }
-      if (a.dz) store8(a.dz + r * a.N + c, d);
+      if (a.dz) *reinterpret_cast<v4u*>(a.dz + row * a.N + c) = narrow(d);
     }
   }
   if (!a.dbias) return;
@@ -165,8 +170,13 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(ActBackwardArgs a) {
   const int lane = lane_id(), wave = threadIdx.x / kWave;
   const int c = blockIdx.x * 64 + lane;
   float s = 0.f;
-  if (c < a.N)
-    for (int p = wave; p < a.parts; p += 4) s += a.partial[static_cast<int64_t>(p) * a.N + c];
+  for (int p = wave; c < a.N && p < a.parts; p += 32) {               // eight loads under way together
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = p + 4 * k < a.parts ? a.partial[static_cast<int64_t>(p + 4 * k) * a.N + c] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += v[k];
+  }
   sums[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && c < a.N) {
@@ -178,6 +188,12 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(ActBackwardArgs a) {
 __global__ __launch_bounds__(256) void bias_zero_kernel(float* p, int n) {
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i < n) p[i] = 0.f;
+}
+
+template <int ACT>
+void launch_act(const ActBackwardArgs& a, dim3 grid, hipStream_t st) {
+  if (a.dy_f32) act_backward_kernel<true, ACT><<<grid, 256, 0, st>>>(a);
+  else act_backward_kernel<false, ACT><<<grid, 256, 0, st>>>(a);
 }
 
 }  // namespace
@@ -227,12 +243,13 @@ hipError_t launch_act_backward(const ActBackwardArgs& args, hipStream_t st) {
   a.rows_per_part = static_cast<int>(per);
   a.parts = static_cast<int>((a.rows + per - 1) / per);
   const dim3 grid(cols, a.parts);
-  if (a.act == kActSwiglu) {
-    if (a.dy_f32) act_backward_kernel<true, true><<<grid, 256, 0, st>>>(a);
-    else act_backward_kernel<false, true><<<grid, 256, 0, st>>>(a);
-  } else {
-    if (a.dy_f32) act_backward_kernel<true, false><<<grid, 256, 0, st>>>(a);
-    else act_backward_kernel<false, false><<<grid, 256, 0, st>>>(a);
+  switch (a.act) {
+    case kActNone: launch_act<kActNone>(a, grid, st); break;
+    case kActRelu: launch_act<kActRelu>(a, grid, st); break;
+    case kActSilu: launch_act<kActSilu>(a, grid, st); break;
+    case kActGelu: launch_act<kActGelu>(a, grid, st); break;
+    case kActGeluTanh: launch_act<kActGeluTanh>(a, grid, st); break;
+    default: launch_act<kActSwiglu>(a, grid, st); break;
   }
   if (a.dbias) bias_sum_kernel<<<(a.N + 63) / 64, 256, 0, st>>>(a);
   return hipGetLastError();

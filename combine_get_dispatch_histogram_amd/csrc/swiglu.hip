@@ -16,14 +16,6 @@
 
 namespace miep {
 
-__device__ __forceinline__ void widen(const v4u& v, float (&f)[8]) {
-  f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
-  f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
-}
-__device__ __forceinline__ v4u narrow(const float (&f)[8]) {
-  return v4u{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
-}
-
 // 16 bytes to memory; past the caches where the result is as large as half the
 // last-level cache (see launch_swiglu).
 template <bool STREAM>
