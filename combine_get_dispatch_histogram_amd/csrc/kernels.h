@@ -322,7 +322,7 @@ struct LinearArgs {
 };
 hipError_t launch_linear(const LinearArgs& a, hipStream_t st);
 hipError_t launch_gemm_linear(const GemmRowsArgs& a, hipStream_t st);   // more than a few rows
-constexpr int kLinearFewRows = 16;
+constexpr int kLinearFewRows = 64;
 
 // ---- gradient through bias and activation: dz = dy * f'(z), dbias = its sum over the rows
 struct ActBackwardArgs {

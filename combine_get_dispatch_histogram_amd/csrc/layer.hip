@@ -189,7 +189,7 @@ __device__ __forceinline__ void up_units(const LayerArgs& a, const Lists& l, uin
   move(at, blockIdx.x);
   while (at.place < l.count) {
     const Unit u = unit_of(at);
-    f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+    f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
     for (int i = 0; i < mine; ++i) {
       typename Ring::Frag f;
       ring.take(f, ahead.place < l.count);
@@ -197,7 +197,7 @@ __device__ __forceinline__ void up_units(const LayerArgs& a, const Lists& l, uin
       Ring::multiply(f, [](int p, int) { return p == 1; }, acc);
     }
 #pragma unroll
-    for (int p = 0; p < 2; ++p) *reinterpret_cast<f32x4*>(sums + ((wave * 16 + m) * 2 + p) * 16 + quarter * 4) = acc[p];
+    for (int p = 0; p < 2; ++p) *reinterpret_cast<f32x4*>(sums + ((wave * 16 + m) * 2 + p) * 16 + quarter * 4) = acc[p][0];
     all_read();
     for (int i = threadIdx.x; i < 128; i += kUpWaves * kWave) {
       const int col = i / 8, p = i % 8 * 2;
@@ -306,9 +306,9 @@ __device__ __forceinline__ void down_part(const LayerArgs& a, const Lists& l, ui
   };
   for (int i = 0; i < Ring::kDepth; ++i) issue();
 
-  f32x4 acc[TP];
+  f32x4 acc[TP][1];
 #pragma unroll
-  for (int i = 0; i < TP; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < TP; ++i) acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int64_t done = 0; done < mine; ++done) {
     const Walk now = at;
     const bool last = move(at, kDownWaves) || done + 1 == mine;
@@ -326,12 +326,12 @@ __device__ __forceinline__ void down_part(const LayerArgs& a, const Lists& l, ui
           f32x4* o = reinterpret_cast<f32x4*>(out + l.token[p] * P + i * 16 + quarter * 4);
           f32x4 v = *o;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(gate, acc[i][r], v[r]);
+          for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(gate, acc[i][0][r], v[r]);
           *o = v;
         }
       }
 #pragma unroll
-      for (int i = 0; i < TP; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < TP; ++i) acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
   }
 }

@@ -7,15 +7,15 @@ namespace miep {
 
 namespace {
 
-// At most 16 rows of x: a workgroup computes 16 * TP of the weight's rows (SwiGLU:
+// At most 64 rows of x (TQ tiles of 16): a workgroup computes 16 * TP of the weight's rows (SwiGLU:
 // half of them gate and the same ones of up, so that it has both); its wavefronts
 // take every 8th step of the contraction.
-template <int TP, int XL, bool SWIGLU>
+template <int TP, int XL, int TQ, bool SWIGLU>
 __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs a) {
-  constexpr int WAVES = 8, P = 16 * TP, RING = 16384;
-  using Ring = StreamRing<kGemmBf16, 2 * TP, XL, RING>;
+  constexpr int WAVES = 8, P = 16 * TP, Q = 16 * TQ, RING = 20480;
+  using Ring = StreamRing<kGemmBf16, 2 * TP, XL, RING, TQ>;
+  static_assert(Q * P * 4 <= RING, "a wavefront's sums take the place of its ring");
   __shared__ __align__(1024) uint8_t lds_mem[WAVES * RING];
-  __shared__ __align__(16) float sums[WAVES][16][P];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int m = lane & 15, quarter = lane >> 4;
   const int rows = static_cast<int>(a.rows), half = a.N / 2;
@@ -32,9 +32,11 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < XL; ++i) xoff[i] = min(Ring::x_row(i), rows - 1) * pitch + Ring::x_chunk(i) * 16;
-  f32x4 acc[TP];
+  f32x4 acc[TP][TQ];
 #pragma unroll
-  for (int i = 0; i < TP; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < TP; ++i)
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   Ring ring((uint32_t)(uintptr_t)(lds_byte*)lds_mem + wave * RING);
   const int steps = (a.K + 63) / 64, n = wave < steps ? (steps - wave + WAVES - 1) / WAVES : 0;
   auto issue = [&](int i) MIEP_INLINE {
@@ -50,8 +52,14 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs a) {
     if (i + Ring::kDepth < n) issue(i + Ring::kDepth);
     Ring::multiply(f, [](int, int) { return false; }, acc);
   }
+  // sums[wave][row][P], the pieces of 4 columns exchanged so that rows meet different banks
+  constexpr int PIECES = P / 4;
+  float* mine = reinterpret_cast<float*>(lds_mem + wave * RING);
 #pragma unroll
-  for (int i = 0; i < TP; ++i) *reinterpret_cast<f32x4*>(&sums[wave][m][i * 16 + quarter * 4]) = acc[i];
+  for (int i = 0; i < TP; ++i)
+#pragma unroll
+    for (int j = 0; j < TQ; ++j)
+      *reinterpret_cast<f32x4*>(mine + (j * 16 + m) * P + (((i * 4 + quarter) ^ m) & (PIECES - 1)) * 4) = acc[i][j];
   __syncthreads();
   constexpr int PAIRS = SWIGLU ? P / 4 : P / 2;
   for (int i = threadIdx.x; i < rows * PAIRS; i += WAVES * kWave) {
@@ -60,12 +68,13 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs a) {
     float v[2] = {}, u[2] = {};
 #pragma unroll
     for (int k = 0; k < WAVES; ++k) {
-      const float* s = sums[k][r] + p;
-      v[0] += s[0];
-      v[1] += s[1];
+      const float* s = reinterpret_cast<const float*>(lds_mem + k * RING) + r * P;
+      auto at = [&](int c) MIEP_INLINE { return s + ((c / 4 ^ r) & (PIECES - 1)) * 4 + c % 4; };
+      v[0] += at(p)[0];
+      v[1] += at(p)[1];
       if constexpr (SWIGLU) {
-        u[0] += s[P / 2];
-        u[1] += s[P / 2 + 1];
+        u[0] += at(p + P / 2)[0];
+        u[1] += at(p + P / 2)[1];
       }
     }
     if constexpr (SWIGLU) {
@@ -79,8 +88,10 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs a) {
 template <int TP, bool SWIGLU>
 void launch_few(const LinearArgs& a, hipStream_t st) {
   const unsigned grid = SWIGLU ? (a.N / 2 + 8 * TP - 1) / (8 * TP) : (a.N + 16 * TP - 1) / (16 * TP);
-  if (a.rows <= 8) linear_few_kernel<TP, 1, SWIGLU><<<grid, 512, 0, st>>>(a);
-  else linear_few_kernel<TP, 2, SWIGLU><<<grid, 512, 0, st>>>(a);
+  if (a.rows <= 8) linear_few_kernel<TP, 1, 1, SWIGLU><<<grid, 512, 0, st>>>(a);
+  else if (a.rows <= 16) linear_few_kernel<TP, 2, 1, SWIGLU><<<grid, 512, 0, st>>>(a);
+  else if (a.rows <= 32) linear_few_kernel<TP, 4, 2, SWIGLU><<<grid, 512, 0, st>>>(a);
+  else linear_few_kernel<TP, 8, 4, SWIGLU><<<grid, 512, 0, st>>>(a);
 }
 
 // Gradient through the activation: a lane 8 columns, a wavefront 512, the four

@@ -44,7 +44,7 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
 // 128 channels), and E4M3's two scales, of the blocks that the rows of W lie in
 // (read when they are needed, they would stop a wavefront for a memory's latency at
 // every tile and expert: 64 tokens over 55 experts, second product, 260 -> 150 us).
-template <int EL, int WL, int XL, int BYTES>
+template <int EL, int WL, int XL, int BYTES, int TQ = 1>
 struct StreamRing {
   static constexpr int TP = (WL + 1) / 2;                             // 16 x 16 results
   static constexpr bool kFp8 = EL != kGemmBf16;
@@ -54,13 +54,14 @@ struct StreamRing {
   static constexpr int kDepth = BYTES / kStep < 8 ? BYTES / kStep : 8;
   static constexpr int kLoads = WL + XL + (kFp8 ? 1 : 0);
   static_assert(kDepth >= 1 && kDepth * kLoads < 64, "ring");
+  static_assert(TQ == 1 || kXRows == 16 * TQ, "whole tiles of X");
 
   uint32_t lds;
   int head, tail;                                                     // buffers: next to fill, next to read
 
   struct Frag {
     u32x4 w[TP][2];
-    u32x4 x[kFp8 ? 4 : 2];
+    u32x4 x[TQ][kFp8 ? 4 : 2];
     float s[2];
   };
 
@@ -73,7 +74,7 @@ struct StreamRing {
   static __device__ __forceinline__ int x_row(int i) { return kFp8 ? i * 4 + lane_id() / 16 : i * 8 + lane_id() / 8; }
   static __device__ __forceinline__ int x_chunk(int i) {
     if constexpr (kFp8) return (lane_id() & 15) ^ (x_row(i) & 15);
-    else return (lane_id() & 7) ^ swz8(x_row(i));
+    else return (lane_id() & 7) ^ swz8(x_row(i) & 15);
   }
 
   // The next step's loads.  `scale`: the lane's, of the first block in even lanes
@@ -118,7 +119,8 @@ struct StreamRing {
 #pragma unroll
     for (int h = 0; h < (kFp8 ? 4 : 2); ++h) {
       const int chunk = kFp8 ? (((h >> 1) * 4 + quarter) * 2 + (h & 1)) ^ xm : (h * 4 + quarter) ^ swz8(xm);
-      f.x[h] = lds_read<u32x4>(at + kWBytes + xm * kXRow + chunk * 16);
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) f.x[j][h] = lds_read<u32x4>(at + kWBytes + (j * 16 + xm) * kXRow + chunk * 16);
     }
     if constexpr (kFp8) {
       const u32x2 t = lds_read<u32x2>(at + kScales);
@@ -131,21 +133,29 @@ struct StreamRing {
   // acc += W * X of a step; E4M3: second(i, r) says whether row r of result i's four
   // lies in the second block.
   template <class SECOND>
-  static __device__ __forceinline__ void multiply(const Frag& f, SECOND second, f32x4 (&acc)[TP]) {
+  static __device__ __forceinline__ void multiply(const Frag& f, SECOND second, f32x4 (&acc)[TP][TQ]) {
 #pragma unroll
     for (int i = 0; i < TP; ++i) {
       if constexpr (kFp8) {
-        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+        f32x4 d[TQ];
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16x8_of_e4m3(f.w[i][h >> 1][(h & 1) * 2], f.w[i][h >> 1][(h & 1) * 2 + 1]),
-                                                      __builtin_bit_cast(bf16x8, f.x[h]), d, 0, 0, 0);
+        for (int j = 0; j < TQ; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(d[r], second(i, r) ? f.s[1] : f.s[0], acc[i][r]);
+        for (int h = 0; h < 4; ++h) {
+          const bf16x8 w = bf16x8_of_e4m3(f.w[i][h >> 1][(h & 1) * 2], f.w[i][h >> 1][(h & 1) * 2 + 1]);
+#pragma unroll
+          for (int j = 0; j < TQ; ++j) d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, f.x[j][h]), d[j], 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < TQ; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[j][r], second(i, r) ? f.s[1] : f.s[0], acc[i][j][r]);
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.w[i][h]), __builtin_bit_cast(bf16x8, f.x[h]), acc[i], 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < TQ; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.w[i][h]), __builtin_bit_cast(bf16x8, f.x[j][h]), acc[i][j], 0, 0, 0);
       }
     }
   }
