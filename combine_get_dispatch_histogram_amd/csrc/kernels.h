@@ -343,22 +343,20 @@ hipError_t launch_act_backward(const ActBackwardArgs& a, hipStream_t st);
 constexpr int kLayerTokens = 128, kLayerListBytes = 49152;
 // Where a workgroup keeps its lists of experts and their tokens in LDS (bytes).
 struct ListsLayout {
-  int words, most, entries;    // 64-bit words of an expert's token mask; listed experts and positions at most
-  int off, active, token, expert, weight;
+  int words, shares, entries;  // 64-bit words of an expert's token mask; shares (16 tokens of an expert) and positions at most
+  int start, share, token, weight;
   int64_t end;
 };
 __host__ __device__ inline ListsLayout lists_layout(int N, int K, int E) {
   ListsLayout l;
   l.words = (N + 63) / 64;
   l.entries = N * K;
-  l.most = E < l.entries ? E : l.entries;
-  l.end = static_cast<int64_t>(E) * l.words * 8 + (l.most + 1) * 6ll + l.entries * 8ll + 32;
-  l.off = E * l.words * 8;
-  l.active = l.off + (l.most + 1) * 4;
-  l.token = l.active + l.most * 2;
-  l.expert = l.token + l.entries * 2;
-  l.weight = (l.expert + l.entries * 2 + 3) / 4 * 4;
-  l.end = (l.end + 15) / 16 * 16;
+  l.shares = (E < l.entries ? E : l.entries) + l.entries / 16;
+  l.end = (static_cast<int64_t>(E) * (l.words * 8 + 2) + l.shares * 8ll + l.entries * 6ll + 40) / 16 * 16;
+  l.start = E * l.words * 8;
+  l.share = (l.start + E * 2 + 7) / 8 * 8;
+  l.token = l.share + l.shares * 8;
+  l.weight = (l.token + l.entries * 2 + 3) / 4 * 4;
   return l;
 }
 struct LayerArgs {

@@ -19,94 +19,105 @@ namespace {
 // shorter rings where long lists leave no room for the others.
 constexpr int kUpWaves = 8, kDownWaves = 4, kMostLds = 163840;
 constexpr int kUpRing = 137216, kUpRingShort = 69632, kDownRing = 104448, kDownRingShort = 49152;
-constexpr int kUpSums = kUpWaves * 2048;
+constexpr int kUpSums = kUpWaves * 2048, kScratch = 128;
 
-// The experts that some token chose, ascending, with their tokens, in dynamic LDS.
+// The experts that some token chose, ascending, with their tokens, in dynamic LDS:
+// a share is at most 16 tokens of one expert, what a pass over its weights serves.
+struct Share {
+  int expert, first, n;        // its tokens are those of the positions from `first` on
+};
 struct Lists {
-  uint64_t* mask;              // [E][words] a bit a token
-  int* off;                    // [most + 1] first position of each listed expert
-  uint16_t* active;            // [most] the experts
-  uint16_t* token;             // [N*K] a position's token
-  uint16_t* expert;            // [N*K] and expert
-  float* weight;               // [N*K] its weight (an expert named twice: their sum)
-  int count, positions;        // listed experts, their tokens
+  v2u* share;                  // [count] expert | first << 16, n
+  uint16_t* token;             // [positions] a position's token
+  float* weight;               // [positions] its weight (an expert named twice: their sum)
+  int count, most;             // shares, the most tokens of one
+  __device__ __forceinline__ Share at(int i) const {
+    const v2u s = share[i];
+    const int x = __builtin_amdgcn_readfirstlane(static_cast<int>(s.x)), n = __builtin_amdgcn_readfirstlane(static_cast<int>(s.y));
+    return Share{x & 0xffff, static_cast<int>(static_cast<uint32_t>(x) >> 16), n};
+  }
 };
 
+// A bit a token for every expert, then the bits' ranks: no order depends on which
+// entry comes first.  Entries that are looked at twice are read once where a
+// thread has one (together with the weights, under the clearing of the masks).
 template <int WAVES, bool WEIGHTS>
-__device__ __forceinline__ Lists make_lists(const LayerArgs& a, uint8_t* lds, int* wave_sums) {
+__device__ __forceinline__ Lists make_lists(const LayerArgs& a, uint8_t* lds, int* scratch) {
   constexpr int THREADS = WAVES * kWave;
   const ListsLayout at = lists_layout(a.N, a.K, a.E);
+  uint64_t* mask = reinterpret_cast<uint64_t*>(lds);
+  uint16_t* start = reinterpret_cast<uint16_t*>(lds + at.start);      // [E] first position
   Lists l;
-  l.mask = reinterpret_cast<uint64_t*>(lds);
-  l.off = reinterpret_cast<int*>(lds + at.off);
-  l.active = reinterpret_cast<uint16_t*>(lds + at.active);
+  l.share = reinterpret_cast<v2u*>(lds + at.share);
   l.token = reinterpret_cast<uint16_t*>(lds + at.token);
-  l.expert = reinterpret_cast<uint16_t*>(lds + at.expert);
   l.weight = reinterpret_cast<float*>(lds + at.weight);
-  const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
-  for (int i = tid; i < a.E * at.words; i += THREADS) l.mask[i] = 0;
+  int *sums = scratch, *valid = scratch + WAVES, *most = scratch + 2 * WAVES;      // [WAVES] each
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave, words = at.words;
+  const int64_t own = tid < at.entries ? a.idx[tid] - a.first : -1;
+  const float own_weight = WEIGHTS && tid < at.entries ? a.wts[tid] : 0.f;
+  for (int i = tid; i < a.E * words; i += THREADS) mask[i] = 0;
   __syncthreads();
-  for (int i = tid; i < at.entries; i += THREADS) {
-    const int64_t e = a.idx[i] - a.first;
+  int named = 0;
+  for (int i0 = 0; i0 < at.entries; i0 += THREADS) {
+    const int i = i0 + tid;
+    const int64_t e = i0 == 0 ? own : i < at.entries ? a.idx[i] - a.first : -1;
     const int t = i / a.K;
-    if (e >= 0 && e < a.E)
-      atomicOr(reinterpret_cast<unsigned long long*>(l.mask + e * at.words + t / 64), 1ull << (t & 63));
+    const bool here = e >= 0 && e < a.E;
+    if (here) atomicOr(reinterpret_cast<unsigned long long*>(mask + e * words + t / 64), 1ull << (t & 63));
+    named += __builtin_popcountll(ballot(here));
   }
+  if (lane == 0) valid[wave] = named;
   __syncthreads();
-  int before = 0;                                                     // listed << 16 | positions
+  int before = 0, fullest = 0;                                        // shares << 16 | positions
   for (int e0 = 0; e0 < a.E; e0 += THREADS) {
     const int e = e0 + tid;
     int n = 0;
     if (e < a.E)
-      for (int w = 0; w < at.words; ++w) n += __builtin_popcountll(l.mask[e * at.words + w]);
-    const int both = n > 0 ? 1 << 16 | n : 0;
+      for (int w = 0; w < words; ++w) n += __builtin_popcountll(mask[e * words + w]);
+    fullest = max(fullest, n);
+    const int both = (n + 15) / 16 << 16 | n;
     const int inc = wave_inclusive_scan(both);
-    if (lane == 63) wave_sums[wave] = inc;
+    if (lane == 63) sums[wave] = inc;
     __syncthreads();
     int mine = before + inc - both;
     for (int w = 0; w < WAVES; ++w) {
-      if (w < wave) mine += wave_sums[w];
-      before += wave_sums[w];
+      if (w < wave) mine += sums[w];
+      before += sums[w];
     }
-    if (n > 0) {
-      const int place = mine >> 16;
-      int p = mine & 0xffff;
-      l.active[place] = static_cast<uint16_t>(e);
-      l.off[place] = p;
-      for (int w = 0; w < at.words; ++w)
-        for (uint64_t bits = l.mask[e * at.words + w]; bits; bits &= bits - 1) {
-          l.token[p] = static_cast<uint16_t>(w * 64 + __builtin_ctzll(bits));
-          l.expert[p++] = static_cast<uint16_t>(e);
-        }
-    }
-    __syncthreads();
+    if (n > 0) start[e] = static_cast<uint16_t>(mine & 0xffff);
+    for (int c = 0; c < n; c += 16)
+      l.share[(mine >> 16) + c / 16] = v2u{static_cast<uint32_t>(e | ((mine & 0xffff) + c) << 16), static_cast<uint32_t>(min(n - c, 16))};
+    if (e0 + THREADS < a.E) __syncthreads();
   }
   l.count = before >> 16;
-  l.positions = before & 0xffff;
-  if (tid == 0) l.off[l.count] = l.positions;
-  if constexpr (WEIGHTS) {
-    for (int p = tid; p < l.positions; p += THREADS) {
-      const int64_t t = l.token[p], e = a.first + l.expert[p];
-      float w = 0.f;
-      for (int k = 0; k < a.K; ++k) w += a.idx[t * a.K + k] == e ? a.wts[t * a.K + k] : 0.f;
+  for (int d = 32; d > 0; d >>= 1) fullest = max(fullest, __shfl_xor(fullest, d));
+  if (lane == 0) most[wave] = fullest;
+  __syncthreads();
+  named = 0;
+  for (int w = 0; w < WAVES; ++w) {
+    named += valid[w];
+    fullest = max(fullest, most[w]);
+  }
+  l.most = min(__builtin_amdgcn_readfirstlane(fullest), 16);
+  for (int i = tid; i < at.entries; i += THREADS) {
+    const int64_t e = i == tid ? own : a.idx[i] - a.first;
+    if (e < 0 || e >= a.E) continue;
+    const int t = i / a.K;
+    int p = start[e];
+    for (int w = 0; w < t / 64; ++w) p += __builtin_popcountll(mask[e * words + w]);
+    p += __builtin_popcountll(mask[e * words + t / 64] & ((1ull << (t & 63)) - 1));
+    l.token[p] = static_cast<uint16_t>(t);
+    if constexpr (WEIGHTS) {
+      float w = i == tid ? own_weight : a.wts[i];
+      if (named != (before & 0xffff)) {                                     // some token names an expert twice: all of its entries' sum
+        w = 0.f;
+        for (int k = 0; k < a.K; ++k) w += a.idx[t * a.K + k] - a.first == e ? a.wts[t * a.K + k] : 0.f;
+      }
       l.weight[p] = w;
     }
   }
   __syncthreads();
   return l;
-}
-
-// The most tokens of an expert.
-template <int WAVES>
-__device__ __forceinline__ int most_tokens(const Lists& l, int* wave_sums) {
-  int n = 0;
-  for (int i = threadIdx.x; i < l.count; i += WAVES * kWave) n = max(n, l.off[i + 1] - l.off[i]);
-  for (int d = 32; d > 0; d >>= 1) n = max(n, __shfl_xor(n, d));
-  if (lane_id() == 0) wave_sums[threadIdx.x / kWave] = n;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < WAVES; ++w) n = max(n, wave_sums[w]);
-  return __builtin_amdgcn_readfirstlane(n);
 }
 
 // ---- first products: units of 16 gate and 16 up channels of an expert, for 16 of
@@ -124,75 +135,50 @@ __device__ __forceinline__ void up_units(const LayerArgs& a, const Lists& l, uin
   const int steps = (a.H + Ring::kChannels - 1) / Ring::kChannels;
   const int mine = wave < steps ? (steps - wave + kUpWaves - 1) / kUpWaves : 0;         // this wavefront's steps of a unit
 
-  // units: every expert's tiles, a tile once for each 16 of its tokens
-  struct Unit { int place, i0, c0, n; };
-  struct Walk { int place, tile, c0; };                               // from here `skip` units on
-  auto move = [&](Walk& at, int skip) MIEP_INLINE {
-    while (at.place < l.count) {
-      const int n = __builtin_amdgcn_readfirstlane(l.off[at.place + 1] - l.off[at.place]);
-      const int blocks = (n + 15) / 16, left = (tiles - at.tile) * blocks - at.c0;
-      if (skip < left) {
-        const int u = at.tile * blocks + at.c0 + skip;
-        at.tile = u / blocks;
-        at.c0 = u - at.tile * blocks;
-        return;
-      }
-      skip -= left;
-      ++at.place;
-      at.tile = at.c0 = 0;
-    }
-  };
-  auto unit_of = [&](const Walk& at) MIEP_INLINE {
-    const int n = __builtin_amdgcn_readfirstlane(l.off[at.place + 1] - l.off[at.place]);
-    return Unit{at.place, at.tile * 16, at.c0 * 16, min(n - at.c0 * 16, 16)};
-  };
-
+  const int units = l.count * tiles;                                  // every share's tiles
   // the issuing side
   Ring ring((uint32_t)(uintptr_t)(lds_byte*)ring_mem + wave * (RING / kUpWaves));
-  Walk ahead{0, 0, 0};
-  move(ahead, blockIdx.x);
-  int ahead_step = 0;
+  int ahead = blockIdx.x, ahead_step = 0;
   const uint8_t *w = nullptr, *scale = nullptr;
   constexpr int SB = EL == kGemmFp8 ? 4 : 1;                          // bytes of a scale
   uint32_t woff[4], xoff[XL];
   auto set_unit = [&]() MIEP_INLINE {
-    const Unit u = unit_of(ahead);
-    const int e = __builtin_amdgcn_readfirstlane(static_cast<int>(l.active[u.place])), first = l.off[u.place] + u.c0;
-    w = static_cast<const uint8_t*>(a.w1) + (static_cast<int64_t>(e) * 2 * a.I + u.i0) * ldw;
+    const int place = ahead / tiles, i0 = (ahead - place * tiles) * 16;
+    const Share u = l.at(place);
+    w = static_cast<const uint8_t*>(a.w1) + (static_cast<int64_t>(u.expert) * 2 * a.I + i0) * ldw;
     if constexpr (F8)                                                 // of the gate rows' block, and of the up rows'
       scale = static_cast<const uint8_t*>(a.s1) +
-              (static_cast<int64_t>(e) * (2 * a.I / kFp8Group) + ((lane & 1) * a.I + u.i0) / kFp8Group) * kb * SB;
+              (static_cast<int64_t>(u.expert) * (2 * a.I / kFp8Group) + ((lane & 1) * a.I + i0) / kFp8Group) * kb * SB;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = Ring::w_row(i);
-      woff[i] = static_cast<uint32_t>(min(row & 15, a.I - 1 - u.i0) + (row >> 4) * a.I) * ldw + Ring::w_chunk(i) * 16;
+      woff[i] = static_cast<uint32_t>(min(row & 15, a.I - 1 - i0) + (row >> 4) * a.I) * ldw + Ring::w_chunk(i) * 16;
     }
 #pragma unroll
     for (int i = 0; i < XL; ++i)
-      xoff[i] = static_cast<uint32_t>(l.token[first + min(Ring::x_row(i), u.n - 1)]) * (a.H * 2u) + Ring::x_chunk(i) * 16;
+      xoff[i] = static_cast<uint32_t>(l.token[u.first + min(Ring::x_row(i), u.n - 1)]) * (a.H * 2u) + Ring::x_chunk(i) * 16;
   };
   auto issue = [&]() MIEP_INLINE {
-    if (ahead.place >= l.count) return;
+    if (ahead >= units) return;
     if (ahead_step == 0) set_unit();
     const int step = wave + ahead_step * kUpWaves;
     ring.issue(w + step * 128ll, woff, reinterpret_cast<const uint8_t*>(a.x) + step * static_cast<int64_t>(Ring::kXRow), xoff, scale + step * SB,
                a.H - step * Ring::kChannels);
     if (++ahead_step == mine) {
       ahead_step = 0;
-      move(ahead, gridDim.x);
+      ahead += gridDim.x;
     }
   };
   if (mine > 0)
     for (int i = 0; i < Ring::kDepth; ++i) issue();
 
-  Walk at{0, 0, 0};
-  move(at, blockIdx.x);
-  while (at.place < l.count) {
-    const Unit u = unit_of(at);
+  for (int at = blockIdx.x; at < units; at += gridDim.x) {
+    const int place = at / tiles, i0 = (at - place * tiles) * 16;
+    const Share u = l.at(place);
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
     for (int i = 0; i < mine; ++i) {
       typename Ring::Frag f;
-      ring.take(f, ahead.place < l.count);
+      ring.take(f, ahead < units);
       issue();
       Ring::multiply(f, [](int p, int) { return p == 1; }, acc);
     }
@@ -201,7 +187,7 @@ __device__ __forceinline__ void up_units(const LayerArgs& a, const Lists& l, uin
     all_read();
     for (int i = threadIdx.x; i < 128; i += kUpWaves * kWave) {
       const int col = i / 8, p = i % 8 * 2;
-      if (col >= u.n || u.i0 + p >= a.I) continue;
+      if (col >= u.n || i0 + p >= a.I) continue;
       float gx = 0.f, gy = 0.f, ux = 0.f, uy = 0.f;
 #pragma unroll
       for (int k = 0; k < kUpWaves; ++k) {
@@ -211,11 +197,10 @@ __device__ __forceinline__ void up_units(const LayerArgs& a, const Lists& l, uin
         ux += v[16];
         uy += v[17];
       }
-      *reinterpret_cast<uint32_t*>(a.a + static_cast<int64_t>(l.off[u.place] + u.c0 + col) * a.I + u.i0 + p) =
+      *reinterpret_cast<uint32_t*>(a.a + static_cast<int64_t>(u.first + col) * a.I + i0 + p) =
           pack_bf16x2(gx * sigmoid(gx) * ux, gy * sigmoid(gy) * uy);
     }
     all_read();
-    move(at, gridDim.x);
   }
 }
 
@@ -223,9 +208,8 @@ template <int EL, int RING>
 __global__ __launch_bounds__(kUpWaves * kWave) void layer_up_kernel(LayerArgs a) {
   extern __shared__ __align__(1024) uint8_t lds[];                    // rings, sums, lists
   float* sums = reinterpret_cast<float*>(lds + RING);
-  int* wave_sums = reinterpret_cast<int*>(lds + RING + kUpSums);
-  const Lists l = make_lists<kUpWaves, false>(a, lds + RING + kUpSums + 64, wave_sums);
-  const int most = most_tokens<kUpWaves>(l, wave_sums);
+  const Lists l = make_lists<kUpWaves, false>(a, lds + RING + kUpSums + kScratch, reinterpret_cast<int*>(lds + RING + kUpSums));
+  const int most = l.most;
   // as few of X's rows as the fullest expert has tokens
   if constexpr (EL == kGemmBf16) {
     if (most <= 8) up_units<EL, 1, RING>(a, l, lds, sums);
@@ -252,27 +236,19 @@ __device__ __forceinline__ void down_part(const LayerArgs& a, const Lists& l, ui
   const uint32_t ldw = static_cast<uint32_t>(a.I) * EB, ldx = static_cast<uint32_t>(a.I) * 2;
   const int steps = (a.I + Ring::kChannels - 1) / Ring::kChannels;
 
-  int64_t total = 0;
-  for (int p = lane; p < l.count; p += kWave) total += (l.off[p + 1] - l.off[p] + 15) / 16;
-  for (int d = 32; d > 0; d >>= 1) total += __shfl_xor(static_cast<int>(total), d);
-  total = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(total))) * steps;
-  struct Walk { int place, c0, step; };                               // an expert, its 16 tokens from c0 on, a step
-  auto tokens = [&](const Walk& at) MIEP_INLINE { return __builtin_amdgcn_readfirstlane(l.off[at.place + 1] - l.off[at.place]); };
-  auto move = [&](Walk& at, int by) MIEP_INLINE {                     // true: to other tokens or another expert
+  const int total = l.count * steps;                                  // (a share's weights are under 4 GiB, its steps under 2^15)
+  struct Walk { int share, step; };
+  auto move = [&](Walk& at, int by) MIEP_INLINE {                     // true: to another share
     at.step += by;
     if (at.step < steps) return false;
-    while (at.step >= steps && at.place < l.count) {
+    while (at.step >= steps) {
       at.step -= steps;
-      at.c0 += 16;
-      if (at.c0 >= tokens(at)) {
-        at.c0 = 0;
-        ++at.place;
-      }
+      ++at.share;
     }
     return true;
   };
-  const int64_t mine = total > wave ? (total - wave + kDownWaves - 1) / kDownWaves : 0;
-  Walk at{0, 0, 0};
+  const int mine = total > wave ? (total - wave + kDownWaves - 1) / kDownWaves : 0;
+  Walk at{0, 0};
   move(at, wave);
 
   Ring ring((uint32_t)(uintptr_t)(lds_byte*)ring_mem + wave * (RING / kDownWaves));
@@ -284,20 +260,19 @@ __device__ __forceinline__ void down_part(const LayerArgs& a, const Lists& l, ui
   const int border = kFp8Group - h0 % kFp8Group;
   const int second = border < min(a.tile, a.H - h0) ? kb : 0;
   Walk ahead = at;
-  int64_t issued = 0;
+  int issued = 0;
   const uint8_t *w = nullptr, *scale = nullptr;
   bool fresh = true;
   auto issue = [&]() MIEP_INLINE {
     if (issued >= mine) return;
     if (fresh) {
-      const int e = __builtin_amdgcn_readfirstlane(static_cast<int>(l.active[ahead.place]));
-      const int first = l.off[ahead.place] + ahead.c0, n = tokens(ahead) - ahead.c0;
-      w = static_cast<const uint8_t*>(a.w2) + (static_cast<int64_t>(e) * a.H + h0) * ldw;
+      const Share u = l.at(ahead.share);
+      w = static_cast<const uint8_t*>(a.w2) + (static_cast<int64_t>(u.expert) * a.H + h0) * ldw;
       if constexpr (F8)
         scale = static_cast<const uint8_t*>(a.s2) +
-                ((static_cast<int64_t>(e) * (a.H / kFp8Group) + h0 / kFp8Group) * kb + (lane & 1) * second) * SB;
+                ((static_cast<int64_t>(u.expert) * (a.H / kFp8Group) + h0 / kFp8Group) * kb + (lane & 1) * second) * SB;
 #pragma unroll
-      for (int i = 0; i < XL; ++i) xoff[i] = static_cast<uint32_t>(first + min(Ring::x_row(i), n - 1)) * ldx + Ring::x_chunk(i) * 16;
+      for (int i = 0; i < XL; ++i) xoff[i] = static_cast<uint32_t>(u.first + min(Ring::x_row(i), u.n - 1)) * ldx + Ring::x_chunk(i) * 16;
     }
     ring.issue(w + ahead.step * 128ll, woff, reinterpret_cast<const uint8_t*>(a.a) + ahead.step * static_cast<int64_t>(Ring::kXRow), xoff,
                scale + ahead.step * SB, a.I - ahead.step * Ring::kChannels);
@@ -309,7 +284,7 @@ __device__ __forceinline__ void down_part(const LayerArgs& a, const Lists& l, ui
   f32x4 acc[TP][1];
 #pragma unroll
   for (int i = 0; i < TP; ++i) acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int64_t done = 0; done < mine; ++done) {
+  for (int done = 0; done < mine; ++done) {
     const Walk now = at;
     const bool last = move(at, kDownWaves) || done + 1 == mine;
     typename Ring::Frag f;
@@ -317,9 +292,9 @@ __device__ __forceinline__ void down_part(const LayerArgs& a, const Lists& l, ui
     issue();
     Ring::multiply(f, [&](int i, int r) { return i * 16 + quarter * 4 + r >= border; }, acc);
     if (last) {
-      const int col = now.c0 + m;
-      if (col < tokens(now)) {
-        const int p = l.off[now.place] + col;
+      const Share u = l.at(now.share);
+      if (m < u.n) {
+        const int p = u.first + m;
         const float gate = l.weight[p];
 #pragma unroll
         for (int i = 0; i < TP; ++i) {
@@ -345,9 +320,8 @@ __global__ __launch_bounds__(kDownWaves* kWave) void layer_down_kernel(LayerArgs
   float* out = sums + wave * a.N * P;
   for (int i = lane_id(); i < a.N * (P / 4); i += kWave) reinterpret_cast<f32x4*>(out)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   uint8_t* rest = lds + RING + kDownWaves * a.N * P * 4;
-  int* wave_sums = reinterpret_cast<int*>(rest);
-  const Lists l = make_lists<kDownWaves, true>(a, rest + 64, wave_sums);
-  const int most = most_tokens<kDownWaves>(l, wave_sums);
+  const Lists l = make_lists<kDownWaves, true>(a, rest + kScratch, reinterpret_cast<int*>(rest));
+  const int most = l.most;
   if constexpr (EL == kGemmBf16) {
     if (most <= 8) down_part<EL, WL, 1, RING>(a, l, lds, out);
     else down_part<EL, WL, 2, RING>(a, l, lds, out);
@@ -388,8 +362,8 @@ hipError_t launch_down(const LayerArgs& a, unsigned rest, hipStream_t st) {
 template <int EL>
 hipError_t launch_typed(const LayerArgs& a, hipStream_t st) {
   const ListsLayout lists = lists_layout(a.N, a.K, a.E);
-  const int64_t units = static_cast<int64_t>(lists.most) * ((a.I + 15) / 16) * ((a.N + 15) / 16);
-  const unsigned grid = static_cast<unsigned>(units < 256 ? units : 256), rest = static_cast<unsigned>(lists.end) + 64;
+  const int64_t units = static_cast<int64_t>(lists.shares) * ((a.I + 15) / 16);
+  const unsigned grid = static_cast<unsigned>(units < 256 ? units : 256), rest = static_cast<unsigned>(lists.end) + kScratch;
   if (kUpRing + kUpSums + rest <= kMostLds) layer_up_kernel<EL, kUpRing><<<grid, kUpWaves * kWave, kUpRing + kUpSums + rest, st>>>(a);
   else layer_up_kernel<EL, kUpRingShort><<<grid, kUpWaves * kWave, kUpRingShort + kUpSums + rest, st>>>(a);
   hipError_t e = hipGetLastError();

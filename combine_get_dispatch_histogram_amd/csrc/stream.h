@@ -83,7 +83,7 @@ struct StreamRing {
   __device__ __forceinline__ void issue(const uint8_t* w, const uint32_t (&woff)[WL], const uint8_t* x, const uint32_t (&xoff)[XL], const uint8_t* scale, int left) {
     w = uniform(w);
     x = uniform(x);
-    const uint32_t to = lds + head * kStep;
+    const uint32_t to = __builtin_amdgcn_readfirstlane(lds + head * kStep);
     head = head == kDepth - 1 ? 0 : head + 1;
     if (kFp8 || left >= kChannels) {
 #pragma unroll

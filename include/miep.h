@@ -583,8 +583,8 @@ miep_status miep_linear_wgrad(const uint16_t* dy, const uint16_t* x, int64_t row
  *   Codes are multiplied as bf16 numbers, which they are exactly: x is not cast.
  *   residual [N][H] bf16, nullable; may be y itself
  *   workspace [N*K][I] bf16, of one call at a time
- * N at most 128; H, I % 8 == 0 (E4M3: % 128 == 0); weights of one expert under 4 GiB, workspace too; E * ceil(N/64) *
- * 8 + 6 * min(E, N*K) + 8 * N*K bytes at most 49,000.  Larger batches: dispatch.
+ * N at most 128; H, I % 8 == 0 (E4M3: % 128 == 0); weights of one expert under 4 GiB, workspace too; E * (8 *
+ * ceil(N/64) + 2) + 8 * min(E, N*K) + 6.5 * N*K bytes at most 49,000.  Larger batches: dispatch.
  * Errors: EINVAL for null pointers, sizes, flags; EUNSUPPORTED for the limits above. */
 typedef struct miep_layer {
   int32_t num_tokens;    /* N >= 0                        */
