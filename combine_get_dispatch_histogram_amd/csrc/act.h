@@ -62,9 +62,9 @@ __device__ __forceinline__ float activate_slope(float z, int act) {
     }
     case kActGelu:                                                    // the distribution function and z times its density
       return fmaf(z * 0.398942280f, __builtin_amdgcn_exp2f(z * z * -0.721347520f), normal_cdf(z));
-    case kActGeluTanh: {
-      const float s = gelu_tanh_sigmoid(z);
-      return s + z * s * (1.f - s) * (1.59576912f * fmaf(0.134145f * z, z, 1.f));
+    case kActGeluTanh: {                                              // (s is 0 or 1 long before 64, where the square could overflow)
+      const float s = gelu_tanh_sigmoid(z), c = fminf(fmaxf(z, -64.f), 64.f);
+      return z != z ? z : s + c * s * (1.f - s) * (1.59576912f * fmaf(0.134145f * c, c, 1.f));
     }
     default: return 1.f;
   }

@@ -345,6 +345,7 @@ miep_status layer_args(const miep_layer* q, int type, const uint16_t* x, const i
   if (!q) return fail(MIEP_EINVAL, "layer is NULL");
   const int32_t N = q->num_tokens, K = q->num_topk, E = q->num_experts, H = q->hidden, I = q->inner;
   if (N < 0 || K <= 0 || E <= 0 || H <= 0 || I <= 0) return fail(MIEP_EINVAL, "sizes must be positive");
+  if (q->first_expert < 0) return fail(MIEP_EINVAL, "first_expert must be >= 0");
   if (N > miep::kLayerTokens) return fail(MIEP_EUNSUPPORTED, "num_tokens > %d", miep::kLayerTokens);
   if (K > 64) return fail(MIEP_EUNSUPPORTED, "num_topk > 64");
   const int unit = type == miep::kGemmBf16 ? 8 : miep::kFp8Group, bytes = type == miep::kGemmBf16 ? 2 : 1;

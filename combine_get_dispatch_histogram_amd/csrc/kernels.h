@@ -340,7 +340,7 @@ struct ActBackwardArgs {
 hipError_t launch_act_backward(const ActBackwardArgs& a, hipStream_t st);
 
 // ---- a few tokens through their experts
-constexpr int kLayerTokens = 128, kLayerListBytes = 49152;
+constexpr int kLayerTokens = 128, kLayerListBytes = 49024;
 // Where a workgroup keeps its lists of experts and their tokens in LDS (bytes).
 struct ListsLayout {
   int words, shares, entries;  // 64-bit words of an expert's token mask; shares (16 tokens of an expert) and positions at most

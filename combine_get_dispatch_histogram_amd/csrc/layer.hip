@@ -20,6 +20,8 @@ namespace {
 constexpr int kUpWaves = 8, kDownWaves = 4, kMostLds = 163840;
 constexpr int kUpRing = 137216, kUpRingShort = 69632, kDownRing = 104448, kDownRingShort = 49152;
 constexpr int kUpSums = kUpWaves * 2048, kScratch = 128;
+static_assert(kUpRingShort + kUpSums + kScratch + kLayerListBytes <= kMostLds, "the longest lists");
+static_assert(kDownRingShort + kDownWaves * kLayerTokens * 2 * 64 + kScratch + kLayerListBytes <= kMostLds, "the longest lists");
 
 // The experts that some token chose, ascending, with their tokens, in dynamic LDS:
 // a share is at most 16 tokens of one expert, what a pass over its weights serves.

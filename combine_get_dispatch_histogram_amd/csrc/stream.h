@@ -125,7 +125,10 @@ struct StreamRing {
     if constexpr (kFp8) {
       const u32x2 t = lds_read<u32x2>(at + kScales);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) f.s[i] = __uint_as_float(EL == kGemmFp8 ? t[i] : t[i] << 23);   // a power of two's exponent byte
+      for (int i = 0; i < 2; ++i) {
+        if constexpr (EL == kGemmFp8) f.s[i] = __uint_as_float(t[i]);
+        else f.s[i] = __uint_as_float(t[i] << 23 | ((t[i] + 1 & 0xfe) == 0 ? 1u << 22 : 0u));   // exponent byte: 0 is 2^-127, 255 NaN
+      }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }

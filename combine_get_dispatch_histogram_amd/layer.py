@@ -60,7 +60,7 @@ def gate_topk(logits: torch.Tensor, num_topk: int, score: str = "softmax", bias:
     K largest scores + ``bias`` [experts] are chosen (the bias enters the choice alone), equal ones by the lower
     index, with ``num_groups`` among the experts of the ``topk_groups`` groups whose ``group_best`` (1 or 2) largest
     add up to most.  Weights are the scores, divided by their sum with ``renormalize``, times ``scale``.  A logit of
-    -inf or NaN masks an expert; where fewer than K are left the last entries are -1 with weight 0, which every
+    -inf or NaN masks an expert (a bias of them leaves it out of the choice); where fewer than K are left the last entries are -1 with weight 0, which every
     dispatch skips.
     """
     shape = (logits.shape[0], num_topk)

@@ -514,7 +514,8 @@ miep_status miep_swiglu_backward(const miep_row_groups* g, const uint16_t* da, c
  *   topk_weights = scale * s, or with renormalize scale * s / (sum of the chosen s).
  * bias enters the choice alone.  Without bias and groups the logits themselves are compared, otherwise s + bias in
  * 64 bits, so that the choice is the formula's.  A logit of -inf or NaN is a masked expert: never chosen, score 0;
- * +inf counts as the type's largest number.  Where fewer than K experts are left, the last topk_idx are -1, weight 0.
+ * +inf counts as the type's largest number.  A bias of -inf or NaN leaves its expert out of the choice.  Where fewer
+ * than K experts are left, the last topk_idx are -1, weight 0.
  *   logits [num_tokens][E] fp32 (logits_f32) or bf16;  bias [E] fp32, nullable;  both 16-byte aligned
  *   topk_idx [num_tokens][K] int64 out, descending;  topk_weights [num_tokens][K] fp32 out
  * Errors: EINVAL for sizes, flags or null pointers; EUNSUPPORTED for E > 2048, K > 64, num_groups > 64. */
@@ -579,12 +580,12 @@ miep_status miep_linear_wgrad(const uint16_t* dy, const uint16_t* x, int64_t row
  * between the products, y once; a token's experts are added in ascending order, an expert named twice with the sum
  * of its weights.
  *   x [N][H] bf16;  w1 [E][2I][H] = [gate | up], w2 [E][H][I], all bf16, or all E4M3 codes with a scale for each 128 x
- *   128 block: w1_scales [E][2I/128][H/128], w2_scales [E][H/128][I/128], fp32 or (scales_ue8m0) exponent bytes.
- *   Codes are multiplied as bf16 numbers, which they are exactly: x is not cast.
+ *   128 block: w1_scales [E][2I/128][H/128], w2_scales [E][H/128][I/128], fp32 or (scales_ue8m0) exponent bytes
+ *   (2^(byte-127); 255 is NaN).  Codes are multiplied as bf16 numbers, which they are exactly: x is not cast.
  *   residual [N][H] bf16, nullable; may be y itself
  *   workspace [N*K][I] bf16, of one call at a time
  * N at most 128; H, I % 8 == 0 (E4M3: % 128 == 0); weights of one expert under 4 GiB, workspace too; E * (8 *
- * ceil(N/64) + 2) + 8 * min(E, N*K) + 6.5 * N*K bytes at most 49,000.  Larger batches: dispatch.
+ * ceil(N/64) + 2) + 8 * min(E, N*K) + 6.5 * N*K under 49,000 bytes.  Larger batches: dispatch.
  * Errors: EINVAL for null pointers, sizes, flags; EUNSUPPORTED for the limits above. */
 typedef struct miep_layer {
   int32_t num_tokens;    /* N >= 0                        */
@@ -593,7 +594,7 @@ typedef struct miep_layer {
   int32_t hidden;        /* H                             */
   int32_t inner;         /* I                             */
   int32_t scales_ue8m0;  /* E4M3: scales are exponent bytes */
-  int64_t first_expert;
+  int64_t first_expert;  /* >= 0                          */
 } miep_layer;
 miep_status miep_expert_layer(const miep_layer* q, const uint16_t* x, const int64_t* topk_idx,
                               const float* topk_weights, const uint16_t* w1, const uint16_t* w2,

@@ -247,3 +247,65 @@ def test_streams_and_graphs():
     # the same bits on every call
     a = run(x, idx, wts, q1, q2)
     assert all(torch.equal(a, run(x, idx, wts, q1, q2)) for _ in range(5))
+
+
+# the longest lists that are taken: two words a token mask and few entries, and many entries
+@pytest.mark.parametrize("E,K", [(2619, 1), (604, 40)])
+@pytest.mark.parametrize("H", [64, 4104])
+def test_longest_lists(E, K, H):
+    check_whole(128, K, E, H, 8)
+
+
+def test_offsets_past_32_bits():
+    """Weights of more than 4 GiB: the last expert's."""
+    N, E, H, I = 3, 152, 4096, 2048
+    assert 2 * E * I * H > 2 ** 31
+    w1 = torch.zeros(E, 2 * I, H, dtype=BF, device=DEV)
+    w2 = torch.zeros(E, H, I, dtype=BF, device=DEV)
+    x, idx, wts, q1, q2, v1, v2 = whole(N, 1, 1, H, I, 4)
+    w1[-1], w2[-1] = q1[0][0], q2[0][0]
+    assert torch.equal(miep.expert_layer(x, idx + E - 1, wts, w1, w2), miep.expert_layer(x, idx, wts, *q1, *q2))
+
+
+@pytest.mark.parametrize("product", [1, 2])
+def test_exponent_bytes_at_their_ends(product):
+    """0 is 2^-127, 254 2^127 and 255 NaN, in either product."""
+    H = I = 128
+    one = torch.tensor(1.0).to(F8).view(torch.uint8).item()
+    w1 = torch.zeros(1, 2 * I, H, dtype=torch.uint8, device=DEV)
+    w1[0, :I, 0], w1[0, I:, 1] = one, one                             # gate: x[0], up: x[1]
+    w2 = torch.zeros(1, H, I, dtype=torch.uint8, device=DEV)
+    w2[0, torch.arange(H), torch.arange(I)] = one
+    idx, wts = torch.zeros(1, 1, dtype=torch.int64, device=DEV), torch.ones(1, 1, device=DEV)
+    x = torch.zeros(1, H, dtype=BF, device=DEV)
+    for byte in (0, 1, 254, 255):
+        s1 = torch.full((1, 2, 1), 127, dtype=torch.uint8, device=DEV)
+        s2 = torch.full((1, 1, 1), 127, dtype=torch.uint8, device=DEV)
+        x[0, 0] = 64.0
+        x[0, 1] = 2.0 ** 60 if byte < 128 else 2.0 ** -60
+        (s1[0, 1:] if product == 1 else s2)[:] = byte
+        y = miep.expert_layer_fp8(x, idx, wts, w1.view(F8), s1, w2.view(F8), s2)
+        if byte == 255:
+            assert torch.isnan(y).all()
+        else:
+            assert torch.equal(y.double(), torch.full_like(y.double(), 64.0 * float(x[0, 1]) * 2.0 ** (byte - 127)))
+
+
+def test_two_streams_at_once():
+    """Calls of two streams side by side, each with a workspace and an output of its own."""
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    cases = []
+    for N, fp8 in ((5, None), (40, "ue8m0")):
+        x, idx, wts, q1, q2, v1, v2 = whole(N, 3, 8, 512, 256, N, fp8=fp8)
+        want, _ = plain(x, idx, wts, v1, v2, exact=True)
+        f = miep.expert_layer_fp8_into if fp8 else miep.expert_layer_into
+        y, ws = torch.empty(N, 512, dtype=BF, device=DEV), torch.empty(N * 3, 256, dtype=BF, device=DEV)
+        cases.append((lambda f=f, a=(x, idx, wts, *q1, *q2, y, ws): f(*a), y, want.to(BF)))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for side, (call, y, _) in zip(sides, cases):
+            with torch.cuda.stream(side):
+                call()
+    torch.cuda.synchronize()
+    for _, y, want in cases:
+        assert torch.equal(y, want)

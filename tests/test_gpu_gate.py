@@ -287,3 +287,46 @@ def test_near_neighbours(E, groups, top, score, dtype):
     if groups == 1:
         check((1 + l * 2.0 ** -21).float(), K, score, torch.zeros(E), 1, 1, 2)
         check((1 + l * 2.0 ** -21).float(), K, score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K", [(64, 6), (160, 8), (700, 8)])
+def test_a_bias_that_is_no_number(score, E, K):
+    """leaves its expert out of the choice, and in the softmax's sum"""
+    logits, bias = torch.randn(20, E, generator=gen(E)), torch.randn(E, generator=gen(E + 1)) * 0.2
+    out = torch.zeros(E, dtype=torch.bool)
+    out[::3] = True
+    bias[::6], bias[3::6] = float("-inf"), float("nan")
+    for groups in (1, 4):
+        idx, w = miep.gate_topk(logits.to(DEV), K, score, bias.to(DEV), groups, groups // 2 or 1)
+        l = clean(logits)
+        v = scores(l, score) + bias.double().numpy()
+        v[:, out.numpy()] = -np.inf
+        if groups > 1:
+            best = -np.sort(-v.reshape(20, groups, -1), axis=2)[:, :, :2].sum(2)
+            keep = np.argsort(-best, axis=1, kind="stable")[:, :groups // 2]
+            for n in range(20):
+                for g in set(range(groups)) - set(keep[n]):
+                    v[n, g * (E // groups):(g + 1) * (E // groups)] = -np.inf
+        want = np.argsort(-v, axis=1, kind="stable")[:, :K]
+        assert np.array_equal(idx.cpu().numpy(), want)
+        ww = weights(l, want, score, False, 1.0)
+        spread = 2 * np.abs(l).max()
+        assert (np.abs(w.double().cpu().numpy() - ww) <= ww * (2 * spread + 60) * ULP).all()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 logits: the last tokens, and their gradient."""
+    N, E, K, last = 4200000, 512, 4, 50
+    assert N * E > 2 ** 31
+    logits = torch.zeros(N, E, dtype=torch.bfloat16, device=DEV)
+    tail = (torch.randn(last, E, generator=gen(1)) * 2).bfloat16()
+    logits[-last:] = tail.to(DEV)
+    idx, w = miep.gate_topk(logits, K)
+    assert np.array_equal(idx[-last:].cpu().numpy(), choice(clean(tail.float()), K, "softmax", None, 1, 1, 2))
+    assert torch.equal(idx[N // 2], torch.arange(K, device=DEV)) and torch.equal(idx[:1], idx[N - last - 1:N - last])
+    d = torch.ones(N, K, device=DEV)
+    d[:, 0] = 2
+    got = miep.gate_topk_backward(d, logits, idx)
+    part = miep.gate_topk_backward(d[-last:].contiguous(), tail.to(DEV), idx[-last:].contiguous())
+    assert torch.equal(got[-last:], part) and torch.equal(got[0], got[N - last - 1])

@@ -267,3 +267,69 @@ def test_streams_and_graphs():
         wdx, wdw, wdb = miep.linear_backward(dy, x, w, "swiglu", wz, bias=True)
         for g, t in zip(got, (wy, wz, wdx, wdw, wdb)):
             assert torch.equal(g, t)
+
+
+FAR = [64.0, 128.0, 1e4, 1e10, 1e20, 1e30, 3e38]
+
+
+@pytest.mark.parametrize("act", ACTS[1:])
+@pytest.mark.parametrize("M", [2, 100, 700])
+def test_far_values(M, act):
+    """Every f is z or 0 there and f' is 1 or 0, to a few fp32 roundings (2^-20 of them and the smallest normal number),
+    with nothing that overflows between."""
+    z = torch.tensor(FAR + [-v for v in FAR] + [0.0, 1.0], device=DEV).to(BF)
+    n = z.numel()
+    w = torch.zeros(2 * n if act == "swiglu" else n, 8, dtype=BF, device=DEV)
+    w[:n, 0] = z
+    w[n:, 0] = 1                                                      # SwiGLU's up
+    x = torch.zeros(M, 8, dtype=BF, device=DEV)
+    x[:, 0] = 1
+    y, saved = miep.linear(x, w, activation=act, dtype=torch.float32, save=True)
+    assert torch.equal(saved, w[:, 0].expand(M, -1))
+    zz = saved.double()
+    want = f64(zz, act)
+    close(y, want, 2.0 ** -20 * want.abs() + 2.0 ** -126 + (1e-7 if act == "gelu" else 0), "y")
+    dz = torch.empty_like(saved)
+    miep.linear_backward_into(torch.ones_like(y), x, w, act, saved, dz=dz)
+    s = slope(saved, act)
+    close(dz, s, (BF_HALF + 2.0 ** -20) * s.abs() + 2.0 ** -126 + (1e-7 if act == "gelu" else 0), "dz")
+    nan = torch.full_like(saved, float("nan"))
+    miep.linear_backward_into(torch.ones_like(y), x, w, act, nan, dz=dz)
+    assert act == "relu" or torch.isnan(dz).all()
+
+
+def test_offsets_past_32_bits():
+    """Results, saved values and gradients of more than 2^31 elements: the last rows."""
+    M, N, K, last = 34000, 65536, 64, 40
+    assert M * N > 2 ** 31
+    x, w = torch.zeros(M, K, dtype=BF, device=DEV), ints((N, K), 3, 1)
+    x[-last:] = ints((last, K), 3, 2)
+    y, z = miep.linear(x, w, activation="relu", save=True)
+    zz = x[-last:].double() @ w.double().t()
+    assert torch.equal(z[-last:].double(), zz.to(BF).double()) and torch.equal(y[-last:], z[-last:].clamp(min=0))
+    assert not y[:-last].any()
+    y.zero_()
+    y[-last:] = ints((last, N), 1, 3)
+    dx, dw, db = miep.linear_backward(y, x, w, "relu", z, bias=True)
+    dz = y[-last:].double() * (zz > 0)
+    assert not dx[:-last].any()
+    want = dz @ w.double()
+    close(dx[-last:], want, (N + 2) * ULP * (dz.abs() @ w.double().abs()) + BF_HALF * want.abs(), "dx")
+    assert torch.equal(dw.double(), dz.t() @ x[-last:].double()) and torch.equal(db.double(), dz.sum(0))
+
+
+def test_two_streams_at_once():
+    """Calls of two streams side by side, each with outputs of its own."""
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    cases = []
+    for M, N, K in ((16, 512, 2048), (200, 512, 1024)):
+        x, w = ints((M, K), 3, M), ints((N, K), 3, M + 1, 2.0 ** -5)
+        cases.append((x, w, torch.empty(M, N, device=DEV), x.double() @ w.double().t()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for side, (x, w, y, _) in zip(sides, cases):
+            with torch.cuda.stream(side):
+                miep.linear_into(x, w, y)
+    torch.cuda.synchronize()
+    for x, w, y, want in cases:
+        assert torch.equal(y.double(), want)

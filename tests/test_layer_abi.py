@@ -101,6 +101,26 @@ def test_layer_sizes(lib, kw, status):
     assert lib.miep_last_error()
 
 
+@pytest.mark.parametrize("N,K,fits", [(128, 1, 2619), (128, 40, 604), (64, 8, 4157), (1, 1, 4898)])
+def test_layer_lists(lib, N, K, fits):
+    """E * (8 * ceil(N/64) + 2) + 8 * min(E, N*K) + 6.5 * N*K under 49,000 is accepted: the next check is another one's."""
+    def call(E):
+        return lib.miep_expert_layer(layer(num_tokens=N, num_topk=K, num_experts=E), 16, 16, 16, 16, 16, None, 16, 8, None)
+
+    def size(E):
+        return E * (8 * -(-N // 64) + 2) + 8 * min(E, N * K) + 6.5 * N * K
+
+    assert size(fits) < 49000 <= size(fits + 1)
+    assert call(fits) == EUNSUPPORTED and b"y" in lib.miep_last_error() and b"lists" not in lib.miep_last_error()
+    for E in range(fits + 1, fits + 12):
+        if size(E) >= 49016:                                                  # (the lists' own rounding up to 16)
+            assert call(E) == EUNSUPPORTED and b"lists" in lib.miep_last_error()
+
+
+def test_layer_first_expert(lib):
+    assert lib.miep_expert_layer(layer(first_expert=-1), 16, 16, 16, 16, 16, None, 16, 16, None) == EINVAL
+
+
 def test_layer_arguments(lib):
     q = layer()
     args = [16, 16, 16, 16, 16, None, 16, 16]
