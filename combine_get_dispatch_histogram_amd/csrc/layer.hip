@@ -17,11 +17,11 @@ namespace {
 
 // LDS of a workgroup: RING bytes of rings, its wavefronts' sums, the lists; the
 // shorter rings where long lists leave no room for the others.
-constexpr int kUpWaves = 8, kDownWaves = 4, kMostLds = 163840;
+constexpr int kUpWaves = 8, kMostLds = 163840;
 constexpr int kUpRing = 137216, kUpRingShort = 69632, kDownRing = 104448, kDownRingShort = 49152;
 constexpr int kUpSums = kUpWaves * 2048, kScratch = 128;
 static_assert(kUpRingShort + kUpSums + kScratch + kLayerListBytes <= kMostLds, "the longest lists");
-static_assert(kDownRingShort + kDownWaves * kLayerTokens * 2 * 64 + kScratch + kLayerListBytes <= kMostLds, "the longest lists");
+static_assert(kDownRingShort + 4 * kLayerTokens * 2 * 64 + kScratch + kLayerListBytes <= kMostLds, "the longest lists");
 
 // The experts that some token chose, ascending, with their tokens, in dynamic LDS:
 // a share is at most 16 tokens of one expert, what a pass over its weights serves.
@@ -118,6 +118,9 @@ __device__ __forceinline__ Lists make_lists(const LayerArgs& a, uint8_t* lds, in
       l.weight[p] = w;
     }
   }
+  // No load is left open: the compiler would wait for all loads, the rings' too,
+  // wherever one's register is used again (fp8, 64 tokens, the second product: 139 -> 198 us).
+  __builtin_amdgcn_s_waitcnt(0x0f70);                                 // vmcnt(0)
   __syncthreads();
   return l;
 }
@@ -171,8 +174,10 @@ __device__ __forceinline__ void up_units(const LayerArgs& a, const Lists& l, uin
       ahead += gridDim.x;
     }
   };
-  if (mine > 0)
+  if (mine > 0) {
+#pragma unroll 1
     for (int i = 0; i < Ring::kDepth; ++i) issue();
+  }
 
   for (int at = blockIdx.x; at < units; at += gridDim.x) {
     const int place = at / tiles, i0 = (at - place * tiles) * 16;
@@ -227,10 +232,10 @@ __global__ __launch_bounds__(kUpWaves * kWave) void layer_up_kernel(LayerArgs a)
 // after the other (an expert's once for each 16 of its tokens) go to its wavefronts
 // in turn, so that together they read whole rows.  At an expert's end a wavefront
 // adds its results, times the gate weights, to its own sums of every token.
-template <int EL, int WL, int XL, int RING>
+template <int EL, int WAVES, int WL, int XL, int RING>
 __device__ __forceinline__ void down_part(const LayerArgs& a, const Lists& l, uint8_t* ring_mem, float* out) {
   constexpr bool F8 = EL != kGemmBf16;
-  using Ring = StreamRing<EL, WL, XL, RING / kDownWaves>;
+  using Ring = StreamRing<EL, WL, XL, RING / WAVES>;
   constexpr int EB = F8 ? 1 : 2, TP = Ring::TP, P = 16 * TP;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int m = lane & 15, quarter = lane >> 4;
@@ -249,11 +254,11 @@ __device__ __forceinline__ void down_part(const LayerArgs& a, const Lists& l, ui
     }
     return true;
   };
-  const int mine = total > wave ? (total - wave + kDownWaves - 1) / kDownWaves : 0;
+  const int mine = total > wave ? (total - wave + WAVES - 1) / WAVES : 0;
   Walk at{0, 0};
   move(at, wave);
 
-  Ring ring((uint32_t)(uintptr_t)(lds_byte*)ring_mem + wave * (RING / kDownWaves));
+  Ring ring((uint32_t)(uintptr_t)(lds_byte*)ring_mem + wave * (RING / WAVES));
   uint32_t woff[WL], xoff[XL];
 #pragma unroll
   for (int i = 0; i < WL; ++i) woff[i] = static_cast<uint32_t>(min(Ring::w_row(i), min(a.tile, a.H - h0) - 1)) * ldw + Ring::w_chunk(i) * 16;
@@ -278,9 +283,10 @@ __device__ __forceinline__ void down_part(const LayerArgs& a, const Lists& l, ui
     }
     ring.issue(w + ahead.step * 128ll, woff, reinterpret_cast<const uint8_t*>(a.a) + ahead.step * static_cast<int64_t>(Ring::kXRow), xoff,
                scale + ahead.step * SB, a.I - ahead.step * Ring::kChannels);
-    fresh = move(ahead, kDownWaves);
+    fresh = move(ahead, WAVES);
     ++issued;
   };
+#pragma unroll 1
   for (int i = 0; i < Ring::kDepth; ++i) issue();
 
   f32x4 acc[TP][1];
@@ -288,7 +294,7 @@ __device__ __forceinline__ void down_part(const LayerArgs& a, const Lists& l, ui
   for (int i = 0; i < TP; ++i) acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int done = 0; done < mine; ++done) {
     const Walk now = at;
-    const bool last = move(at, kDownWaves) || done + 1 == mine;
+    const bool last = move(at, WAVES) || done + 1 == mine;
     typename Ring::Frag f;
     ring.take(f, issued < mine);
     issue();
@@ -313,24 +319,24 @@ __device__ __forceinline__ void down_part(const LayerArgs& a, const Lists& l, ui
   }
 }
 
-template <int EL, int WL, int RING>
-__global__ __launch_bounds__(kDownWaves* kWave) void layer_down_kernel(LayerArgs a) {
-  constexpr int P = (WL + 1) / 2 * 16, THREADS = kDownWaves * kWave;
+template <int EL, int WAVES, int WL, int RING>
+__global__ __launch_bounds__(WAVES* kWave) void layer_down_kernel(LayerArgs a) {
+  constexpr int P = (WL + 1) / 2 * 16, THREADS = WAVES * kWave;
   extern __shared__ __align__(1024) uint8_t lds[];                    // rings, sums, lists
   float* sums = reinterpret_cast<float*>(lds + RING);                 // [wavefront][token][P]
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   float* out = sums + wave * a.N * P;
   for (int i = lane_id(); i < a.N * (P / 4); i += kWave) reinterpret_cast<f32x4*>(out)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  uint8_t* rest = lds + RING + kDownWaves * a.N * P * 4;
-  const Lists l = make_lists<kDownWaves, true>(a, rest + kScratch, reinterpret_cast<int*>(rest));
+  uint8_t* rest = lds + RING + WAVES * a.N * P * 4;
+  const Lists l = make_lists<WAVES, true>(a, rest + kScratch, reinterpret_cast<int*>(rest));
   const int most = l.most;
   if constexpr (EL == kGemmBf16) {
-    if (most <= 8) down_part<EL, WL, 1, RING>(a, l, lds, out);
-    else down_part<EL, WL, 2, RING>(a, l, lds, out);
+    if (most <= 8) down_part<EL, WAVES, WL, 1, RING>(a, l, lds, out);
+    else down_part<EL, WAVES, WL, 2, RING>(a, l, lds, out);
   } else {
-    if (most <= 4) down_part<EL, WL, 1, RING>(a, l, lds, out);
-    else if (most <= 8) down_part<EL, WL, 2, RING>(a, l, lds, out);
-    else down_part<EL, WL, 4, RING>(a, l, lds, out);
+    if (most <= 4) down_part<EL, WAVES, WL, 1, RING>(a, l, lds, out);
+    else if (most <= 8) down_part<EL, WAVES, WL, 2, RING>(a, l, lds, out);
+    else down_part<EL, WAVES, WL, 4, RING>(a, l, lds, out);
   }
   __syncthreads();
   const int h0 = blockIdx.x * a.tile, pairs = min(a.tile, a.H - h0) / 2;
@@ -338,7 +344,7 @@ __global__ __launch_bounds__(kDownWaves* kWave) void layer_down_kernel(LayerArgs
     const int t = i / pairs, p = (i - t * pairs) * 2;
     float x = 0.f, y = 0.f;
 #pragma unroll
-    for (int k = 0; k < kDownWaves; ++k) {
+    for (int k = 0; k < WAVES; ++k) {
       x += sums[(k * a.N + t) * P + p];
       y += sums[(k * a.N + t) * P + p + 1];
     }
@@ -354,10 +360,11 @@ __global__ __launch_bounds__(kDownWaves* kWave) void layer_down_kernel(LayerArgs
 
 template <int EL, int WL>
 hipError_t launch_down(const LayerArgs& a, unsigned rest, hipStream_t st) {
-  const unsigned tiles = (a.H + a.tile - 1) / a.tile, threads = kDownWaves * kWave;
-  const unsigned sums = kDownWaves * a.N * ((WL + 1) / 2) * 64;
-  if (kDownRing + sums + rest <= kMostLds) layer_down_kernel<EL, WL, kDownRing><<<tiles, threads, kDownRing + sums + rest, st>>>(a);
-  else layer_down_kernel<EL, WL, kDownRingShort><<<tiles, threads, kDownRingShort + sums + rest, st>>>(a);
+  const unsigned tiles = (a.H + a.tile - 1) / a.tile;
+  const unsigned sums = a.N * ((WL + 1) / 2) * 64;                    // of a wavefront
+  if (kDownRing + 8 * sums + rest <= kMostLds && a.N <= 16) layer_down_kernel<EL, 8, WL, kDownRing><<<tiles, 8 * kWave, kDownRing + 8 * sums + rest, st>>>(a);
+  else if (kDownRing + 4 * sums + rest <= kMostLds) layer_down_kernel<EL, 4, WL, kDownRing><<<tiles, 4 * kWave, kDownRing + 4 * sums + rest, st>>>(a);
+  else layer_down_kernel<EL, 4, WL, kDownRingShort><<<tiles, 4 * kWave, kDownRingShort + 4 * sums + rest, st>>>(a);
   return hipGetLastError();
 }
 
