@@ -1,5 +1,9 @@
 // linear.hip -- dense products with an epilogue for a few rows (more of them:
 // gemm_linear.hip), and the gradient through activation and bias.
+//
+// Both are bound by memory: few rows by the weight (16 rows of SwiGLU over 4096 x 7168:
+// 11.2 us, 59 MB, 5.3 TB/s; 64 rows of 7168 x 2048: 11.2 us), the gradient by dy, z
+// and dz (4096 rows of 2 x 2048, SwiGLU: 19 us, 84 MB).
 #include "gemm_epilogue.h"
 #include "stream.h"
 
