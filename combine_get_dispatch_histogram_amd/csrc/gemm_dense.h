@@ -8,8 +8,9 @@ namespace miep {
 // The rows kernel's product for few tiles: a workgroup computes 64 x 64, each of
 // its 8 wavefronts all of it over every eighth step of the contraction, through
 // a buffer of its own, so without barriers; their sums are added up in
-// wavefront order in LDS.  A wavefront that has read a step's operands into
-// registers starts the next step's loads and multiplies under them.  Against
+// wavefront order in LDS.  A wavefront that has read one operand of a step into
+// registers starts the next step's loads of it, and multiplies under them (both
+// operands together: 4096 x 256 x 7168 24.1 us, so 23.4).  Against
 // tiles whose wavefronts share each step, an operand leaves LDS once instead of
 // up to four times, which is what bounds a 64 x 64 tile.
 struct DenseSplit {
@@ -65,22 +66,30 @@ __global__ __launch_bounds__(512, 2) void gemm_dense_split_kernel(GemmRowsArgs a
     }
     qoff[i] = static_cast<uint32_t>(min(row, live - 1) * ldq) + ((lane & 7) ^ swz(row)) * 16;
   }
-  auto issue = [&](int step) MIEP_INLINE {
+  auto issue_p = [&](int step) MIEP_INLINE {
     const uint8_t* pb = pbase + static_cast<int64_t>(step) * (PT ? 64 * ldp : kStepBytes);
-    const uint8_t* qb = qbase + static_cast<int64_t>(step) * kStepBytes;
     if ((step + 1) * 64 <= C) {
 #pragma unroll
       for (int i = 0; i < S::kLoads; ++i) dma16s(pb, poff[i], mine + i * 1024);
-#pragma unroll
-      for (int i = 0; i < S::kLoads; ++i) dma16s(qb, qoff[i], mine + S::kBytes + i * 1024);
     } else {                                                          // behind the contraction's end: zeros
 #pragma unroll
       for (int i = 0; i < S::kLoads; ++i) {
         const int row = i * 8 + lane / 8;
-        const bool qin = step * 64 + ((lane & 7) ^ swz(row)) * 8 < C;
-        const bool pin = PT ? step * 64 + row < C : qin;
-        dma16(pin ? static_cast<const void*>(pb + poff[i]) : static_cast<const void*>(g_zero16), mine + i * 1024);
-        dma16(qin ? static_cast<const void*>(qb + qoff[i]) : static_cast<const void*>(g_zero16), mine + S::kBytes + i * 1024);
+        const bool in = PT ? step * 64 + row < C : step * 64 + ((lane & 7) ^ swz(row)) * 8 < C;
+        dma16(in ? static_cast<const void*>(pb + poff[i]) : static_cast<const void*>(g_zero16), mine + i * 1024);
+      }
+    }
+  };
+  auto issue_q = [&](int step) MIEP_INLINE {
+    const uint8_t* qb = qbase + static_cast<int64_t>(step) * kStepBytes;
+    if ((step + 1) * 64 <= C) {
+#pragma unroll
+      for (int i = 0; i < S::kLoads; ++i) dma16s(qb, qoff[i], mine + S::kBytes + i * 1024);
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::kLoads; ++i) {
+        const bool in = step * 64 + ((lane & 7) ^ swz(i * 8 + lane / 8)) * 8 < C;
+        dma16(in ? static_cast<const void*>(qb + qoff[i]) : static_cast<const void*>(g_zero16), mine + S::kBytes + i * 1024);
       }
     }
   };
@@ -90,16 +99,20 @@ __global__ __launch_bounds__(512, 2) void gemm_dense_split_kernel(GemmRowsArgs a
   for (int i = 0; i < T; ++i)
 #pragma unroll
     for (int j = 0; j < T; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (wave < nk) issue(wave);
+  if (wave < nk) {
+    issue_p(wave);
+    issue_q(wave);
+  }
   for (int step = wave; step < nk; step += S::kWaves) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const bool more = step + S::kWaves < nk;
     bf16x8 p[2][T], q[2][T];
+    // P has come; its operands have left the buffer before the next step's come
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::kLoads) : "memory");
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < T; ++i) {
         const uint32_t at = (i * 16 + m) * kStepBytes + (((h * 4 + quarter) ^ swz(m)) * 16);
-        q[h][i] = lds_read<bf16x8>(mine + S::kBytes + at);
         if constexpr (PT) {
           const int r = h * 32 + quarter * 8 + m / 4;
           const uint32_t tr = mine + r * kStepBytes + ((i * 2 + (m & 3) / 2) ^ swz_t64(r)) * 16 + (m & 1) * 8;
@@ -111,9 +124,20 @@ __global__ __launch_bounds__(512, 2) void gemm_dense_split_kernel(GemmRowsArgs a
           p[h][i] = lds_read<bf16x8>(mine + at);
         }
       }
-    // the operands have left the buffer before the next step's come
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (step + S::kWaves < nk) issue(step + S::kWaves);
+    if (more) {
+      issue_p(step + S::kWaves);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::kLoads) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < T; ++i)
+        q[h][i] = lds_read<bf16x8>(mine + S::kBytes + (i * 16 + m) * kStepBytes + (((h * 4 + quarter) ^ swz(m)) * 16));
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (more) issue_q(step + S::kWaves);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
