@@ -263,7 +263,7 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
           one = bigger(one, x);
           j = j + 1 == a.per_group ? 0 : j + 1;
         }
-        if (a.group_best == 2 && a.per_group > 1) one += two;
+        if (a.group_best == 2) one += two;
       }
       __builtin_amdgcn_wave_barrier();
       int before = 0;
@@ -716,6 +716,7 @@ hipError_t launch_gate(const GateArgs& args, bool backward, hipStream_t st) {
   if (a.N == 0) return hipSuccess;
   a.per_group = a.E / a.groups;
   a.per_div = make_fastdiv(a.per_group);
+  if (a.per_group == 1) a.group_best = 1;                             // there is no second member to add
   const bool scores = a.bias || a.groups > 1;
   const int64_t wgs = (a.N + 3) / 4;
   const unsigned grid = static_cast<unsigned>(wgs < (1 << 20) ? wgs : (1 << 20));
