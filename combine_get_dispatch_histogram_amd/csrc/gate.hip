@@ -425,10 +425,10 @@ __global__ __launch_bounds__(256, V <= 16 ? 4 : 2) void gate_rows_kernel(GateArg
     for (int v = 0; v < V; ++v) sorted[wave][lane][v] = key[v];
     auto place = [&](int k) MIEP_INLINE { return EXACT ? 0xffff - (k & 0xffff) : e0 + expert_of<PER>(LOW - (k & LOW), a.lanes, in_group, wide); };
     // the nearest that two keys may be to stand for their order
+    constexpr float kStep = V <= 16 ? 0x1p-18f : 0x1p-17f;            // both keys' last bits
     auto apart = [&](float x) MIEP_INLINE {
       const float y = fabsf(x);
-      constexpr float step = V <= 16 ? 0x1p-18f : 0x1p-17f;           // both keys' last bits
-      return SCORES ? (step + 0x1p-21f) * (y > 1.f ? y : 1.f) : __builtin_fmaxf(step * y, 0x1p-120f);
+      return SCORES ? (kStep + 0x1p-21f) * (y > 1.f ? y : 1.f) : __builtin_fmaxf(kStep * y, 0x1p-120f);
     };
     // what an expert is compared by, in 64 bits
     double denominator = 1.0;
@@ -468,10 +468,17 @@ __global__ __launch_bounds__(256, V <= 16 ? 4 : 2) void gate_rows_kernel(GateArg
         };
         float one = of_key(key[0]), two = of_key(key[1]);
         best_two(one, two);
-        const float score = a.group_best == 2 ? one + two : one;
+        // Half a sum (so that none overflows), and its distance from the formula's at most: half of what
+        // its members' keys may be off, which is each one's own size and not the sum's (s + 1000 and s -
+        // 1000 make one near 1); a quarter of a step for the sum's rounding and the softmax's denominator.
+        // Any two groups are then in order where they are farther apart than the largest of these, twice.
+        const bool both = a.group_best == 2;
+        const float score = both ? 0.5f * one + 0.5f * two : one;
+        float off = both ? 0.25f * apart(one) + 0.25f * apart(two) : 0.5f * apart(one);
+        off = row_max(score > kNone ? off + 0.125f * kStep : 0.f);    // (a group that has none scores -inf, exactly)
         bool in = before(score) < a.top_groups && group < a.groups;
         const float least = -row_max(in ? -score : kNone), next = row_max(in || group >= a.groups ? kNone : score);
-        const bool near = least - next <= 2.f * apart(least);         // (both -inf: by the index)
+        const bool near = least - next <= 2.f * off;                  // (both -inf: by the index)
         if (ballot(near) != 0) {
           // the same from each lane's first two in 64 bits, unless a third may be one of its group's two
           const bool third = key[2] != kNoKey && of_key(key[2]) >= two - 2.f * apart(two);

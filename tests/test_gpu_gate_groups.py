@@ -9,16 +9,40 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
 import combine_get_dispatch_histogram_amd as miep  # noqa: E402
-from test_gpu_gate import check, choice, clean, gen  # noqa: E402
+from test_gpu_gate import check, choice, clean, gen, scores  # noqa: E402
 
 DEV = torch.device("cuda:0")
 
 
+def undecided(l, score, bias, groups, top, best):
+    """Tokens whose groups 64 bits cannot order.  exp, the division and the softmax's sum (some 25 additions of equal signs
+    one after the other, half an ulp each) leave s within 2^-48 of itself, s + b adds 2^-53 of itself and so does the sum of
+    two: two evaluations of one score differ by less than tol = 2^-46 (1 + |b|).  Where a chosen group and another one are within that
+    and are not of the very same numbers (which tie on either side), either is right."""
+    v = np.where(np.isinf(l), -np.inf, scores(l, score) + bias.double().numpy()).reshape(len(l), groups, -1)
+    places = np.argsort(-v, axis=2, kind="stable")[:, :, :best]
+    g = np.take_along_axis(v, places, 2).sum(2)
+    order = np.argsort(-g, axis=1, kind="stable")
+    tol = 2.0 ** -46 * (1 + np.abs(bias.numpy()).max())
+    out = np.zeros(len(l), bool)
+    for n in np.flatnonzero((top < groups) & np.isfinite(g).all(1)):
+        last, rest = g[n, order[n, top - 1]], g[n, order[n, min(top, groups - 1)]]
+        if last - rest > tol:
+            continue
+        of = [i for i in range(groups) if rest - tol <= g[n, i] <= last + tol]
+        what = {tuple(sorted((l[n].reshape(groups, -1)[i, p], bias.view(groups, -1)[i, p].item()) for p in places[n, i])) for i in of}
+        out[n] = len(what) > 1
+    return out
+
+
 def same_choice(logits, K, score, bias, groups, top, best):
     print("[case]", tuple(logits.shape), logits.dtype, K, score, groups, top, best, flush=True)
-    idx, _ = miep.gate_topk(logits.to(DEV), K, score, None if bias is None else bias.to(DEV), groups, top, best)
-    want = choice(clean(logits.float()), K, score, bias, groups, top, best)
+    idx, _ = miep.gate_topk(logits.to(DEV), K, score, bias.to(DEV), groups, top, best)
+    l = clean(logits.float())
+    want = choice(l, K, score, bias, groups, top, best)
     wrong = (idx.cpu().numpy() != want).any(1)
+    if wrong.any():
+        wrong &= ~undecided(l, score, bias, groups, top, best)
     assert not wrong.any(), "%d of %d tokens, first %d: got %s want %s" % (wrong.sum(), len(wrong), wrong.argmax(), idx[int(wrong.argmax())].tolist(),
                                                                             want[wrong.argmax()].tolist())
 
@@ -37,3 +61,32 @@ def test_groups_of_one_expert(E, top, best, score):
         check(logits, K, score, None, E, top, best, True, 1.5)
         check(logits, K, score, torch.randn(E, generator=gen(9)) * 0.3, E, top, best)
         check(logits, min(E, top + 2), score, None, E, top, best)     # more choices than groups are left
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [4.0, 16.0, 100.0, 1000.0, 1e5])
+def test_sums_that_cancel(size, score):
+    """One expert of every group at +size, the others at -size: a group's score is near 1 where its terms' roundings
+    are those of `size`."""
+    groups, per = 4, 16
+    bias = torch.full((groups, per), -size)
+    bias[:, 5] = size
+    logits = torch.randn(100000, groups * per, generator=gen(int(size)))
+    same_choice(logits, 6, score, bias.view(-1), groups, 2, 2)
+
+
+@pytest.mark.parametrize("E,groups,top", [(64, 4, 2), (48, 8, 3), (256, 8, 4), (160, 5, 2), (512, 16, 5), (1024, 8, 3)])
+@pytest.mark.parametrize("size", [16.0, 100.0, 1000.0])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_cancelling_sums_near_each_other(E, groups, top, size, dtype):
+    """The same with the groups' scores a few of those roundings apart, and with one group of them so."""
+    N, per, g = 4000, E // groups, gen(E)
+    base = torch.randn(N, 1, per, generator=g)
+    logits = (base + torch.randn(N, groups, per, generator=g) * size * 1e-5).to(dtype).view(N, E)
+    bias = torch.full((groups, per), -size)
+    bias[:, per // 2] = size
+    for score in ("softmax", "sigmoid"):
+        same_choice(logits, 3, score, bias.view(-1), groups, top, 2)
+        one = bias.clone()
+        one[1:] *= 2.0 ** -30
+        same_choice(logits, 3, score, one.view(-1), groups, top, 2)
