@@ -90,3 +90,15 @@ def test_cancelling_sums_near_each_other(E, groups, top, size, dtype):
         one = bias.clone()
         one[1:] *= 2.0 ** -30
         same_choice(logits, 3, score, one.view(-1), groups, top, 2)
+
+
+@pytest.mark.parametrize("E", [64, 1024])
+@pytest.mark.parametrize("best", [1, 2])
+def test_sums_past_the_type(E, best):
+    """Groups' scores beyond fp32's largest number keep their order."""
+    groups, per = 4, E // 4
+    logits = torch.randn(37, E, generator=gen(E))
+    for rows in ([2.9e38, 3.0e38, 3.1e38, 3.3e38], [3.3e38, 1.0, -3.3e38, 3.4e38], [-3.0e38, -3.1e38, -2.9e38, -3.3e38]):
+        bias = torch.tensor(rows)[:, None].expand(groups, per).reshape(-1)
+        same_choice(logits, 6, "sigmoid", bias, groups, 2, best)
+        same_choice(logits, 6, "softmax", bias, groups, 1, best)
