@@ -245,8 +245,8 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int e = lane * V + v;
-      if (a.bias && e < E) c[v] += a.bias[e];
-      if (!(l[v] > kNone) || !(c[v] == c[v])) c[v] = kNone;
+      if (a.bias && e < E) c[v] += usable<true>(a.bias[e]);
+      if (!(l[v] > kNone)) c[v] = kNone;
     }
     if (a.groups > 1) {
       // a lane a group: its best one or two scores, from LDS; lanes start at
@@ -443,7 +443,7 @@ __global__ __launch_bounds__(256, V <= 16 ? 4 : 2) void gate_rows_kernel(GateArg
       const double l = logit<F32>(row, e);
       if constexpr (!SCORES) return l;
       const double s = a.score == kGateSoftmax ? exp(l - static_cast<double>(top)) / denominator : 1.0 / (1.0 + exp(-l));
-      return a.bias ? s + static_cast<double>(a.bias[e]) : s;
+      return a.bias ? s + static_cast<double>(usable<true>(a.bias[e])) : s;
     };
     bool open = false;                                                // for gate_token
     if constexpr (SCORES) {

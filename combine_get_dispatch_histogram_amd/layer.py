@@ -59,9 +59,10 @@ def gate_topk(logits: torch.Tensor, num_topk: int, score: str = "softmax", bias:
     logits [tokens, experts] float32 or bfloat16.  ``score``: "softmax" over the experts, or "sigmoid" of each.  The
     K largest scores + ``bias`` [experts] are chosen (the bias enters the choice alone), equal ones by the lower
     index, with ``num_groups`` among the experts of the ``topk_groups`` groups whose ``group_best`` (1 or 2) largest
-    add up to most.  Weights are the scores, divided by their sum with ``renormalize``, times ``scale``.  A logit of
-    -inf or NaN masks an expert (a bias of them leaves it out of the choice); where fewer than K are left the last entries are -1 with weight 0, which every
-    dispatch skips.
+    add up to most (of groups of one expert: whose expert has most).  Weights are the scores, divided by their sum with
+    ``renormalize``, times ``scale``.  A logit of -inf or NaN masks an expert, a bias of them leaves it out of the choice
+    (a group that has fewer than ``group_best`` left comes last); +inf counts as the type's largest number.  Where fewer
+    than K are left the last entries are -1 with weight 0, which every dispatch skips.
     """
     shape = (logits.shape[0], num_topk)
     idx = torch.empty(shape, dtype=_I64, device=logits.device)

@@ -514,8 +514,9 @@ miep_status miep_swiglu_backward(const miep_row_groups* g, const uint16_t* da, c
  *   topk_weights = scale * s, or with renormalize scale * s / (sum of the chosen s).
  * bias enters the choice alone.  Without bias and groups the logits themselves are compared, otherwise s + bias in
  * 64 bits, so that the choice is the formula's.  A logit of -inf or NaN is a masked expert: never chosen, score 0;
- * +inf counts as the type's largest number.  A bias of -inf or NaN leaves its expert out of the choice.  Where fewer
- * than K experts are left, the last topk_idx are -1, weight 0.
+ * +inf counts as the type's largest number.  A bias of -inf or NaN leaves its expert out of the choice, +inf counts as
+ * fp32's largest number.  A group of one expert scores what that does; one that has fewer than group_best of its
+ * experts left comes behind all others.  Where fewer than K experts are left, the last topk_idx are -1, weight 0.
  *   logits [num_tokens][E] fp32 (logits_f32) or bf16;  bias [E] fp32, nullable;  both 16-byte aligned
  *   topk_idx [num_tokens][K] int64 out, descending;  topk_weights [num_tokens][K] fp32 out
  * Errors: EINVAL for sizes, flags or null pointers; EUNSUPPORTED for E > 2048, K > 64, num_groups > 64. */

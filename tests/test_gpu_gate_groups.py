@@ -102,3 +102,23 @@ def test_sums_past_the_type(E, best):
         bias = torch.tensor(rows)[:, None].expand(groups, per).reshape(-1)
         same_choice(logits, 6, "sigmoid", bias, groups, 2, best)
         same_choice(logits, 6, "softmax", bias, groups, 1, best)
+
+
+@pytest.mark.parametrize("E", [64, 1024])
+def test_an_infinite_bias(E):
+    """counts as fp32's largest number, as an infinite logit does: its group has a score, or none where it is the only
+    expert that is left."""
+    groups, per = 4, E // 4
+    logits = torch.randn(37, E, generator=gen(E))
+    bias = torch.zeros(E)
+    bias[per + 3] = bias[2 * per + 1] = float("inf")
+    logits[::2, per:2 * per] = float("-inf")
+    logits[::2, per + 3] = 1.0                                        # the only one of its group
+    number = bias.clamp(max=torch.finfo(torch.float32).max)
+    for best in (1, 2):
+        for score in ("softmax", "sigmoid"):
+            idx, w = miep.gate_topk(logits.to(DEV), 5, score, bias.to(DEV), groups, 2, best)
+            got, ww = miep.gate_topk(logits.to(DEV), 5, score, number.to(DEV), groups, 2, best)
+            want = choice(clean(logits), 5, score, number, groups, 2, best)
+            assert np.array_equal(got.cpu().numpy(), want)
+            assert torch.equal(idx, got) and torch.equal(w, ww)
