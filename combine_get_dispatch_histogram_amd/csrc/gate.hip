@@ -591,8 +591,9 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(GateArgs a) {
     const void* row = static_cast<const uint8_t*>(a.logits) + t * pitch;
     const int64_t e64 = sub < K ? a.idx[t * K + sub] : -1;
     const int mine = e64 >= 0 && e64 < E ? static_cast<int>(e64) : -1;
-    float g = mine >= 0 ? a.d_w[t * K + sub] * a.scale : 0.f;
+    const float given = mine >= 0 ? a.d_w[t * K + sub] * a.scale : 0.f;
     const float own = mine >= 0 ? logit<F32>(row, mine) : kNone;
+    float g = own > kNone ? given : 0.f;                              // (a masked expert's weight is 0 and stays so, whatever d_w holds there)
     float p[V];
     float dot = 0.f;
     if (dense) {

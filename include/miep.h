@@ -536,8 +536,9 @@ miep_status miep_gate_topk(const miep_gate* g, const void* logits, const float* 
                            float* topk_weights, void* stream);
 
 /* gate_topk_backward -- gradient of the logits, [N][E] in the logits' type,
- * from the weights' (the choice itself has none; entries outside [0, E) add
- * nothing, an expert named twice adds both). */
+ * from the weights' (the choice itself has none; entries outside [0, E) and
+ * those of masked experts add nothing, whatever d_topk_weights holds there; an
+ * expert named twice adds both). */
 miep_status miep_gate_topk_backward(const miep_gate* g, const float* d_topk_weights, const void* logits,
                                     const int64_t* topk_idx, void* d_logits, void* stream);
 

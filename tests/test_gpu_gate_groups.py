@@ -122,3 +122,25 @@ def test_an_infinite_bias(E):
             want = choice(clean(logits), 5, score, number, groups, 2, best)
             assert np.array_equal(got.cpu().numpy(), want)
             assert torch.equal(idx, got) and torch.equal(w, ww)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E,K", [(9, 4), (64, 6), (256, 8), (300, 20), (1024, 8)])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
+def test_gradient_of_a_masked_experts_weight(E, K, score, renorm, what):
+    """That weight is 0 whatever the logits are: its gradient reaches none of them, a number or not."""
+    N, g = 21, gen(E)
+    logits = torch.randn(N, E, generator=g)
+    idx = torch.rand(N, E, generator=g).topk(K, 1).indices
+    d = torch.randn(N, K, generator=g)
+    for n in range(N):                                                # one, two .. all of a token's choices
+        off = idx[n, :n % K + 1]
+        logits[n, off] = float("-inf") if n % 2 else float("nan")
+    masked = ~torch.isfinite(logits.gather(1, idx))
+    for dtype in (torch.float32, torch.bfloat16):
+        l = logits.to(dtype).to(DEV)
+        got = miep.gate_topk_backward(d.masked_fill(masked, what).to(DEV), l, idx.to(DEV), score, renorm, 2.0)
+        want = miep.gate_topk_backward(d.masked_fill(masked, 0.0).to(DEV), l, idx.to(DEV), score, renorm, 2.0)
+        assert torch.isfinite(want).all() and torch.equal(got, want)
+        assert (got.cpu()[~torch.isfinite(logits)] == 0).all()
