@@ -140,11 +140,11 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
 
 def linear_backward_into(dy, x, w, activation: Optional[str] = None, z=None, dx=None, dw=None, dbias=None, dz=None,
                          workspace=None, accumulate: bool = False) -> None:
-    """linear_backward into those of dx [rows, K] bfloat16, dw [N, K] (float32 or bfloat16) and dbias [N] float32 that
-    are given (allocates nothing).  Where there is an activation, or dy is float32, dz [rows, N] bfloat16 is needed
-    for dx and dw: the gradient before the activation, which both products read.  dbias needs a workspace
-    [parts, N] float32 (parts: one for every 16 rows, up to 256, is enough), of one call at a time.  ``accumulate``
-    adds to dw (float32) and dbias."""
+    """linear_backward into those of dx [rows, K] bfloat16, dw [N, K] (float32 or bfloat16), dbias [N] float32 and dz
+    [rows, N] bfloat16 that are given (allocates nothing).  dz is the gradient before the activation, rounded: dx and dw
+    need it where there is an activation, or dy is float32, as both products read it; elsewhere it is a copy of dy that
+    costs its writing.  dbias needs a workspace [parts, N] float32 (parts: one for every 16 rows, up to 256, is enough),
+    of one call at a time.  ``accumulate`` adds to dw (float32) and dbias."""
     act = _activation(activation)
     rows, N, K, width = _linear_sizes(x, w, act)
     kind = dy.dtype
@@ -171,9 +171,8 @@ def linear_backward_into(dy, x, w, activation: Optional[str] = None, z=None, dx=
     dx_p = a.opt(dx, "dx", _BF16, (rows, K))
     dw_p = None if dw is None else a.arg(dw, "dw", dw.dtype, (N, K))
     db_p, ws_p = a.opt(dbias, "dbias", _F32, (N,)), a.opt(workspace, "workspace", _F32, None if dbias is None else (parts, N))
-    if dz is not None and through or dbias is not None:
-        _run(a, "miep_linear_act_backward", dy_p, kind == _F32, z_p, rows, N, act, dz_p if through else None, db_p, bool(accumulate),
-             ws_p, parts)
+    if dz is not None or dbias is not None:
+        _run(a, "miep_linear_act_backward", dy_p, kind == _F32, z_p, rows, N, act, dz_p, db_p, bool(accumulate), ws_p, parts)
     grad = dz_p if through else dy_p
     if dx is not None:
         _run(a, "miep_linear_dgrad", grad, rows, w_p, N, K, dx_p)
