@@ -552,7 +552,7 @@ miep_status miep_gate_topk_backward(const miep_gate* g, const float* d_topk_weig
  *   z [rows][N] bf16 out, nullable: kept for the backward pass
  *   y [rows][N or N/2] out, bf16 or fp32 (y_f32)
  * Everything 16-byte aligned, rows at most 2^31-2^16; N, K % 8 == 0 (SwiGLU: N % 16 == 0), at most 2^21; SwiGLU's w
- * under 4 GiB less 1024 rows.
+ * under 4 GiB less 1024 rows; (rows / 32 + 2) * (max(N, K) / 128 + 1), in whole numbers, at most 2^31-2^16 (tiles).
  * Errors: EINVAL for null pointers, sizes, flags; EUNSUPPORTED for the limits above. */
 enum { MIEP_ACT_NONE = 0, MIEP_ACT_RELU = 1, MIEP_ACT_SILU = 2, MIEP_ACT_GELU = 3, MIEP_ACT_GELU_TANH = 4, MIEP_ACT_SWIGLU = 5 };
 miep_status miep_linear(const uint16_t* x, int64_t rows, const uint16_t* w, int32_t n, int32_t k, const float* bias,
@@ -565,7 +565,10 @@ miep_status miep_linear(const uint16_t* x, int64_t rows, const uint16_t* w, int3
  *   dy [rows][N or N/2] bf16 or fp32 (dy_f32);  z [rows][N] bf16 from miep_linear (MIEP_ACT_NONE: ignored)
  *   workspace [parts][N] fp32, parts >= 1, where dbias is given: the parts the rows may be summed in (one for
  *   every 16 rows, up to 256, is enough to fill the GPU); of one call at a time
- * linear_dgrad -- dx = dy w.  linear_wgrad -- dw = dy^T x, fp32 (dw_f32; accumulate: added) or bf16. */
+ * relu's f' is 1 for z > 0 and 0 elsewhere, also where z is no number.
+ * linear_dgrad -- dx = dy w.  linear_wgrad -- dw = dy^T x, fp32 (dw_f32; accumulate: added) or bf16.
+ * Alignment, limits and errors of all three: as linear's (linear_act_backward: without K), and for linear_wgrad at most
+ * 2^24 tiles of 128 x 128 of dw. */
 miep_status miep_linear_act_backward(const void* dy, int32_t dy_f32, const uint16_t* z, int64_t rows, int32_t n,
                                      int32_t activation, uint16_t* dz, float* dbias, int32_t accumulate,
                                      float* workspace, int32_t parts, void* stream);
