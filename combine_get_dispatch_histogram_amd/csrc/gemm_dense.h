@@ -197,18 +197,24 @@ hipError_t launch_dense_split(const GemmRowsArgs& a, hipStream_t st) {
 // being as many tiles as the GPU holds at a time.  `busy` is what a step takes
 // longer with every CU at work than with few (power, L2).  All bf16, weights not
 // in a cache; us by the tiles 32x32 / 64x64 (both split over wavefronts) / 128x64 /
-// 128x128 / 128x192 / 128x256 / 256x256, the rule's choice marked:
-//   1000 x  256 x 7168   *14.3 /  24.0 /  37.9 /  47.4 /  57.9 /  74.4 / 100.9
-//    128 x 4096 x 7168    40.4 / *33.9 /  55.0 /  69.4 /  71.1 /  75.4 / 108.9
-//   4096 x  256 x 7168    61.7 / *32.8 /  54.6 /  69.2 /  83.8 / 101.9 / 111.4
-//   4096 x 1024 x 1024    47.4 /  25.8 / *14.8 /  15.3 /  18.0 /  19.7 /  25.2
-//   1024 x 4096 x 7168   230.2 / 105.9 /  87.1 / *68.1 /  78.9 /  95.8 / 106.9
-//    700 x 7168 x 2048    96.7 /  50.3 /  37.4 /  38.3 / *28.0 /  29.8 /  37.7
-//   1003 x 7168 x 2048   135.4 /  80.8 /  50.7 /  43.5 /  45.7 / *33.3 /  38.8
-// Gradients of the rows (C = N), 64 x 64 / 128 x 64 / 128 x 128 / 128 x 256:
-//    777 x 4096 -> 1024  *17.9 /  23.3 /  29.8 /  45.5
-//    500 x 4096 -> 7168   72.1 /  53.7 / *40.6 /  52.6
-//   1024 x 4096 -> 7168  128.8 / 101.3 /  79.5 / *56.7
+// 128x128 / 128x192 / 128x256 / 256x192 / 256x256, the rule's choice marked (of the
+// last two the wide kernel's own rule takes one, by rounds):
+//   1000 x  256 x 7168   *14.4 /  22.9 /  37.6 /  46.3 /  56.9 /  73.3 /  97.9 / 127.7
+//    128 x 4096 x 7168    40.3 / *33.8 /  55.3 /  70.0 /  72.2 /  74.5 / 106.5 / 107.3
+//   4096 x  256 x 7168    61.0 / *32.3 /  53.4 /  66.9 /  81.0 /  98.6 / 108.1 / 141.0
+//   4096 x 1024 x 1024    48.3 /  24.9 /  13.7 / *13.4 /  15.2 /  17.0 /  20.9 /  26.7
+//   1024 x 4096 x 7168   229.2 / 106.6 /  86.6 / *67.6 /  78.6 /  94.7 / 105.2 / 137.4
+//    700 x 7168 x 2048    98.0 /  48.8 /  37.6 /  38.3 / *26.5 /  30.2 /  36.6 /  45.8
+//   1003 x 7168 x 2048   136.2 /  67.9 /  50.0 /  42.2 /  44.7 / *32.0 /  36.6 /  46.9
+//   3000 x 4096 x 4096   513.0 / 171.0 / 122.2 / 105.7 /  92.4 / 103.9 / *77.9 /  90.3
+//   2000 x 8192 x 2048   328.8 / 150.0 /  95.5 /  82.0 /  74.1 /  64.9 /  72.8 / *54.8
+//   8192 x 4096 x 7168    2167 / 747.1 / 587.2 / 507.3 / 450.3 / 395.0 / 373.9 /*341.3
+// Gradients of the rows (C = N):
+//    777 x 4096 -> 1024   42.5 / *17.1 /  22.8 /  29.5 /  36.5 /  46.0 /  59.7 /  77.5
+//    500 x 4096 -> 7168  175.8 /  68.5 /  53.7 / *40.6 /  44.7 /  52.6 /  62.9 /  82.0
+//   1024 x 4096 -> 7168  291.4 / 119.0 / 101.4 /  79.5 /  80.7 / *55.7 /  65.3 /  81.1
+//   3000 x 4096 -> 4096  577.4 / 169.7 / 128.6 / 105.9 /  92.1 / 104.3 / *78.0 /  88.9
+//   4096 x 4096 -> 7168   1148 / 445.9 / 349.8 / 277.1 / 229.1 / 222.9 / 212.4 /*191.8
 struct DenseTile {
   int p, q, slots;
   float step, busy, fixed;

@@ -1,9 +1,12 @@
 // linear.hip -- dense products with an epilogue for a few rows (more of them:
 // gemm_linear.hip), and the gradient through activation and bias.
 //
-// Both are bound by memory: few rows by the weight (16 rows of SwiGLU over 4096 x 7168:
-// 11.2 us, 59 MB, 5.3 TB/s; 64 rows of 7168 x 2048: 11.2 us), the gradient by dy, z
-// and dz (4096 rows of 2 x 2048, SwiGLU: 19 us, 84 MB).
+// Up to 16 rows are bound by reading the weight (SwiGLU over 4096 x 7168: 11.2 us,
+// 59 MB, 5.3 TB/s).  Of 64 rows two thirds of what a step brings to LDS are x, and
+// a ring holds one or two steps, so its loads are not covered (7168 x 2048: 11.2 us,
+// 31 MB).  The gradient of 4096 rows of 2 x 2048, SwiGLU, takes 19 us for its 84 MB
+// (4.4 TB/s): 16 wavefronts a CU are one round, in each of which the loads of four
+// rows, 960 instructions and the stores follow one another.
 #include "gemm_epilogue.h"
 #include "stream.h"
 
