@@ -472,9 +472,9 @@ __global__ __launch_bounds__(256, V <= 16 ? 4 : 2) void gate_rows_kernel(GateArg
         float one = of_key(key[0]), two = of_key(key[1]);
         best_two(one, two);
         // Half a sum (so that none overflows), and its distance from the formula's at most: half of what
-        // its members' keys may be off, which is each one's own size and not the sum's (s + 1000 and s -
-        // 1000 make one near 1); a quarter of a step for the sum's rounding and the softmax's denominator.
-        // Any two groups are then in order where they are farther apart than the largest of these, twice.
+        // its members' keys may be off, which goes by each one's own size and not the sum's (s + 1000 and
+        // s - 1000 make one near 1); an eighth of a step for roundings and the softmax's denominator (some
+        // 30 of 2^-24).  Any two groups farther apart than twice the largest of these are in order.
         const bool both = a.group_best == 2;
         const float score = both ? 0.5f * one + 0.5f * two : one;
         float off = both ? 0.25f * apart(one) + 0.25f * apart(two) : 0.5f * apart(one);
